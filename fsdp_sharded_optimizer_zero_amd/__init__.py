@@ -34,12 +34,20 @@ ZS_EINVAL_REDUCE = -12
 ZS_EZERO_TOKENS = -13
 ZS_EINVAL_UNITS = -14
 ZS_ESCRATCH = -15
+ZS_EINVAL_EMBED = -16
+ZS_EINVAL_DISTILL = -17
 ZS_SCRATCH_BYTES = 16 << 20
 ZS_GRAD_BF16 = 0
 ZS_GRAD_F32 = 1
 ZS_MAX_RANKS = 64
 ZS_OUT_GATHER = 0
 ZS_OUT_SHARD = 1
+ZS_BF16 = 0
+ZS_F32 = 1
+ZS_ID_I32 = 0
+ZS_ID_I64 = 1
+ZS_EMBED_MAX = 1 << 24
+ZS_DISTILL_MAX_K = 1024
 
 
 class ZSError(RuntimeError):
@@ -67,6 +75,25 @@ class zs_adamw(C.Structure):
 class zs_reduce(C.Structure):
     _fields_ = [("grad_dtype", C.c_int32), ("micro", C.c_int32), ("micro_count", C.c_int32),
                 ("reserved", C.c_int32), ("rank_tokens", C.POINTER(C.c_int64))]
+
+
+class zs_embed(C.Structure):
+    _fields_ = [("tokens", C.c_int64), ("rows", C.c_int64), ("first_row", C.c_int64),
+                ("dim", C.c_int64), ("table_pitch", C.c_int64), ("act_pitch", C.c_int64),
+                ("id_dtype", C.c_int32), ("table_dtype", C.c_int32), ("act_dtype", C.c_int32),
+                ("reserved", C.c_int32), ("scale", C.c_double)]
+
+
+class zs_distill(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("vocab", C.c_int64), ("logits_pitch", C.c_int64),
+                ("grad_pitch", C.c_int64), ("k", C.c_int32), ("logits_dtype", C.c_int32),
+                ("teacher_dtype", C.c_int32), ("id_dtype", C.c_int32),
+                ("temperature", C.c_double), ("alpha", C.c_double), ("scale", C.c_double)]
+
+
+class zs_targets(C.Structure):
+    _fields_ = [("teacher_ids", C.c_void_p), ("teacher_logits", C.c_void_p),
+                ("teacher_lse", C.c_void_p), ("labels", C.c_void_p)]
 
 
 _lib = None
@@ -106,6 +133,22 @@ def _open(path: str):
     L.zs_strerror.restype = C.c_char_p
     L.shard_grad_sqnorm_noalloc.argtypes = [P(zs_shard), vp, vp, vp, i32, vp]
     L.shard_grad_sqnorm_noalloc.restype = C.c_int
+    L.embed_lookup.argtypes = [P(zs_embed), vp, vp, vp, vp]
+    L.embed_lookup.restype = C.c_int
+    L.zs_embed_workspace_bytes.argtypes = [P(zs_embed)]
+    L.zs_embed_workspace_bytes.restype = C.c_size_t
+    L.embed_grad.argtypes = [P(zs_embed), vp, vp, vp, i32, vp, C.c_size_t, vp]
+    L.embed_grad.restype = C.c_int
+    L.zs_distill_workspace_bytes.argtypes = [P(zs_distill)]
+    L.zs_distill_workspace_bytes.restype = C.c_size_t
+    L.distill_loss.argtypes = [P(zs_distill), vp, P(zs_targets), vp, vp, vp, vp, i32, vp,
+                               C.c_size_t, vp]
+    L.distill_loss.restype = C.c_int
+    L.distill_grad.argtypes = [P(zs_distill), vp, P(zs_targets), vp, vp, vp, vp]
+    L.distill_grad.restype = C.c_int
+    L.distill_loss_grad.argtypes = [P(zs_distill), vp, P(zs_targets), vp, vp, vp, vp, vp, vp,
+                                    i32, vp, C.c_size_t, vp]
+    L.distill_loss_grad.restype = C.c_int
     L.zs_init.argtypes = []
     L.zs_init.restype = C.c_int
     return L
@@ -143,6 +186,7 @@ def _check(rc: int, what: str) -> None:
 
 _F32 = ("float32",)
 _F64 = ("float64",)
+_I64 = ("int64",)
 _B16 = ("int16", "bfloat16", "uint16")      # bf16 bit patterns
 _ANY = None
 
@@ -347,6 +391,132 @@ def shard_pack_gather(s: zs_shard, master, param_out, stream=None) -> None:
     _check(lib().shard_pack_gather(C.byref(s), _ptr(master, "master", _F32, s.valid_len),
                                    _ptr(param_out, "param_out", _B16, _out_len(s)),
                                    _stream(stream)), "shard_pack_gather")
+
+
+# ---- the vocabulary table: embedding lookup and gradient, distillation ----------------
+
+_IDS = {ZS_ID_I32: ("int32",), ZS_ID_I64: ("int64",)}
+_ELEM = {ZS_BF16: _B16, ZS_F32: _F32}
+
+
+def _rows_ptr(t, what: str, dtypes, rows: int, width: int, pitch: int):
+    """As _ptr for `rows` rows of `width` elements, `pitch` apart: either a
+    contiguous tensor that holds them, or a 2-D view with that row stride."""
+    if t is not None and not isinstance(t, int) and hasattr(t, "stride") and t.dim() == 2 \
+            and not t.is_contiguous():
+        if t.shape[0] < rows or t.shape[1] < width or (width > 1 and t.stride(1) != 1) \
+                or (rows > 1 and t.stride(0) != pitch):
+            raise ValueError(f"{what}: shape {tuple(t.shape)} with strides {t.stride()}, the call "
+                             f"needs {rows} rows of {width} elements, {pitch} apart")
+        # the checks of _ptr on its first row; the rows' extent is checked above
+        return _ptr(t[0, :width], what, dtypes)
+    return _ptr(t, what, dtypes, (rows - 1) * pitch + width if rows > 0 else 0)
+
+
+def _sized(workspace, workspace_bytes, need: int):
+    """(address, bytes) of a workspace argument."""
+    if workspace_bytes is None:
+        workspace_bytes = (workspace.numel() * workspace.element_size()
+                           if hasattr(workspace, "numel") else need)
+    return _bytes_ptr(workspace, "workspace", workspace_bytes), workspace_bytes
+
+
+def make_embed(tokens: int, rows: int, dim: int, first_row: int = 0, table_pitch=None,
+               act_pitch=None, id_dtype: int = ZS_ID_I64, table_dtype: int = ZS_BF16,
+               act_dtype: int = ZS_BF16, scale: float = 1.0) -> zs_embed:
+    return zs_embed(tokens, rows, first_row, dim, dim if table_pitch is None else table_pitch,
+                    dim if act_pitch is None else act_pitch, id_dtype, table_dtype, act_dtype, 0,
+                    float(scale))
+
+
+def zs_embed_workspace_bytes(e: zs_embed) -> int:
+    return lib().zs_embed_workspace_bytes(C.byref(e))
+
+
+def embed_lookup(e: zs_embed, ids, table, out, stream=None) -> None:
+    _check(lib().embed_lookup(
+        C.byref(e), _ptr(ids, "ids", _IDS.get(e.id_dtype), e.tokens),
+        _rows_ptr(table, "table", _ELEM.get(e.table_dtype), e.rows, e.dim, e.table_pitch),
+        _rows_ptr(out, "out", _ELEM.get(e.act_dtype), e.tokens, e.dim, e.act_pitch),
+        _stream(stream)), "embed_lookup")
+
+
+def embed_grad(e: zs_embed, ids, grad_out, grad_table, workspace, accumulate: bool = False,
+               stream=None, workspace_bytes=None) -> None:
+    """The gradient of embed_lookup: grad_out are the T gradients of its rows,
+    grad_table (of e.table_dtype) receives the table's."""
+    ws, nbytes = _sized(workspace, workspace_bytes, zs_embed_workspace_bytes(e))
+    _check(lib().embed_grad(
+        C.byref(e), _ptr(ids, "ids", _IDS.get(e.id_dtype), e.tokens),
+        _rows_ptr(grad_out, "grad_out", _ELEM.get(e.act_dtype), e.tokens, e.dim, e.act_pitch),
+        _rows_ptr(grad_table, "grad_table", _ELEM.get(e.table_dtype), e.rows, e.dim,
+                  e.table_pitch),
+        1 if accumulate else 0, ws, nbytes, _stream(stream)), "embed_grad")
+
+
+def make_distill(rows: int, vocab: int, k: int, logits_pitch=None, grad_pitch=None,
+                 logits_dtype: int = ZS_BF16, teacher_dtype: int = ZS_F32,
+                 id_dtype: int = ZS_ID_I64, temperature: float = 1.0, alpha: float = 1.0,
+                 scale: float = 1.0) -> zs_distill:
+    return zs_distill(rows, vocab, vocab if logits_pitch is None else logits_pitch,
+                      vocab if grad_pitch is None else grad_pitch, k, logits_dtype, teacher_dtype,
+                      id_dtype, float(temperature), float(alpha), float(scale))
+
+
+def zs_distill_workspace_bytes(d: zs_distill) -> int:
+    return lib().zs_distill_workspace_bytes(C.byref(d))
+
+
+def _targets(d: zs_distill, teacher_ids, teacher_logits, teacher_lse, labels) -> zs_targets:
+    ids = _IDS.get(d.id_dtype)
+    return zs_targets(
+        _ptr(teacher_ids, "teacher_ids", ids, d.rows * d.k),
+        _ptr(teacher_logits, "teacher_logits", _ELEM.get(d.teacher_dtype), d.rows * d.k),
+        _ptr(teacher_lse, "teacher_lse", _F32, d.rows), _ptr(labels, "labels", ids, d.rows))
+
+
+def _logits_ptr(d: zs_distill, t, what: str, pitch: int):
+    return _rows_ptr(t, what, _ELEM.get(d.logits_dtype), d.rows, d.vocab, pitch)
+
+
+def distill_loss(d: zs_distill, logits, teacher_ids, teacher_logits, loss, lse, teacher_lse=None,
+                 labels=None, loss_sum=None, counted=None, accumulate: bool = False,
+                 workspace=None, stream=None, workspace_bytes=None) -> None:
+    """Row losses (loss: fp32[T], lse: fp32[T, 2]); loss_sum: one fp32 and
+    counted: one int64, or None."""
+    t = _targets(d, teacher_ids, teacher_logits, teacher_lse, labels)
+    ws, nbytes = _sized(workspace, workspace_bytes, zs_distill_workspace_bytes(d))
+    _check(lib().distill_loss(
+        C.byref(d), _logits_ptr(d, logits, "logits", d.logits_pitch), C.byref(t),
+        _ptr(loss, "loss", _F32, d.rows), _ptr(lse, "lse", _F32, 2 * d.rows),
+        _ptr(loss_sum, "loss_sum", _F32, 1), _ptr(counted, "counted", _I64, 1),
+        1 if accumulate else 0, ws, nbytes, _stream(stream)), "distill_loss")
+
+
+def distill_grad(d: zs_distill, logits, teacher_ids, teacher_logits, lse, grad, teacher_lse=None,
+                 labels=None, row_grad=None, stream=None) -> None:
+    """The logits' gradient from the lse of distill_loss; grad may be logits."""
+    t = _targets(d, teacher_ids, teacher_logits, teacher_lse, labels)
+    _check(lib().distill_grad(
+        C.byref(d), _logits_ptr(d, logits, "logits", d.logits_pitch), C.byref(t),
+        _ptr(lse, "lse", _F32, 2 * d.rows), _ptr(row_grad, "row_grad", _F32, d.rows),
+        _logits_ptr(d, grad, "grad", d.grad_pitch), _stream(stream)), "distill_grad")
+
+
+def distill_loss_grad(d: zs_distill, logits, teacher_ids, teacher_logits, loss, grad,
+                      teacher_lse=None, labels=None, lse=None, row_grad=None, loss_sum=None,
+                      counted=None, accumulate: bool = False, workspace=None, stream=None,
+                      workspace_bytes=None) -> None:
+    """distill_loss and distill_grad in one call; grad may be logits."""
+    t = _targets(d, teacher_ids, teacher_logits, teacher_lse, labels)
+    ws, nbytes = _sized(workspace, workspace_bytes, zs_distill_workspace_bytes(d))
+    _check(lib().distill_loss_grad(
+        C.byref(d), _logits_ptr(d, logits, "logits", d.logits_pitch), C.byref(t),
+        _ptr(loss, "loss", _F32, d.rows), _ptr(lse, "lse", _F32, 2 * d.rows),
+        _ptr(row_grad, "row_grad", _F32, d.rows),
+        _logits_ptr(d, grad, "grad", d.grad_pitch), _ptr(loss_sum, "loss_sum", _F32, 1),
+        _ptr(counted, "counted", _I64, 1), 1 if accumulate else 0, ws, nbytes,
+        _stream(stream)), "distill_loss_grad")
 
 
 def build(verbose: bool = False) -> str:

@@ -80,7 +80,11 @@ int sqnorm_pass(const zs_shard* s, const uint16_t* const* grad_slices, float* me
 }  // namespace
 }  // namespace zs
 
-extern "C" int zs_init(void) { return prepare_device(); }
+extern "C" int zs_init(void)
+{
+    const int rc = prepare_device();
+    return rc != ZS_OK ? rc : prepare_vocab();
+}
 
 extern "C" int shard_grad_sqnorm(const zs_shard* s, const uint16_t* const* grad_slices,
                                  float* mean_out, void* workspace, size_t workspace_bytes,
@@ -245,4 +249,185 @@ extern "C" int shard_pack_gather(const zs_shard* s, const float* master, uint16_
     if (s->valid_len > 0 && !master) return ZS_ENULL;
     if (!aligned16(param_out) || (master && !aligned16(master))) return ZS_EALIGN;
     return enqueue_pack(master, slot_base(s, param_out), s->valid_len, s->shard_len, stream);
+}
+
+// ---- the vocabulary table --------------------------------------------------------
+
+namespace zs {
+namespace {
+
+bool aligned_to(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+uintptr_t elem_bytes(int32_t dtype) { return dtype == ZS_F32 ? 4 : 2; }
+uintptr_t id_bytes(int32_t dtype) { return dtype == ZS_ID_I64 ? 8 : 4; }
+
+EmbedArgs embed_args(const zs_embed* e, const void* ids, const void* src, void* dst)
+{
+    EmbedArgs a{};
+    a.ids = ids;
+    a.src = src;
+    a.dst = dst;
+    a.tokens = e->tokens;
+    a.rows = e->rows;
+    a.first_row = e->first_row;
+    a.dim = e->dim;
+    a.table_pitch = e->table_pitch;
+    a.act_pitch = e->act_pitch;
+    a.scale = static_cast<float>(e->scale);
+    a.id64 = e->id_dtype == ZS_ID_I64;
+    a.table_f32 = e->table_dtype == ZS_F32;
+    a.act_f32 = e->act_dtype == ZS_F32;
+    return a;
+}
+
+// What the distillation calls share: the struct, the logits and the targets
+// into the kernel arguments.
+int distill_args(const zs_distill* d, const void* logits, const zs_targets* t, DistillArgs* a)
+{
+    int rc = check_distill(d);
+    if (rc != ZS_OK) return rc;
+    if (!t) return ZS_ENULL;
+    const bool kd = d->alpha > 0.0, ce = d->alpha < 1.0;
+    if (d->rows > 0) {
+        if (!logits || (ce && !t->labels)) return ZS_ENULL;
+        if (kd && d->k > 0 && (!t->teacher_ids || !t->teacher_logits)) return ZS_ENULL;
+    }
+    if (!aligned_to(logits, elem_bytes(d->logits_dtype)) ||
+        !aligned_to(t->teacher_ids, id_bytes(d->id_dtype)) ||
+        !aligned_to(t->teacher_logits, elem_bytes(d->teacher_dtype)) ||
+        !aligned_to(t->teacher_lse, 4) || !aligned_to(t->labels, id_bytes(d->id_dtype)))
+        return ZS_EALIGN;
+    *a = DistillArgs{};
+    a->logits = logits;
+    a->teacher_ids = t->teacher_ids;
+    a->teacher_logits = t->teacher_logits;
+    a->teacher_lse = t->teacher_lse;
+    a->labels = t->labels;
+    a->rows = d->rows;
+    a->vocab = d->vocab;
+    a->logits_pitch = d->logits_pitch;
+    a->grad_pitch = d->grad_pitch;
+    a->k = kd ? d->k : 0;
+    a->f32 = d->logits_dtype == ZS_F32;
+    a->teacher_f32 = d->teacher_dtype == ZS_F32;
+    a->id64 = d->id_dtype == ZS_ID_I64;
+    a->kd = kd;
+    a->ce = ce;
+    a->inv_tau = static_cast<float>(1.0 / d->temperature);
+    a->loss_kd = static_cast<float>(d->alpha * d->temperature * d->temperature);
+    a->loss_ce = static_cast<float>(1.0 - d->alpha);
+    a->grad_kd = static_cast<float>(d->alpha * d->temperature * d->scale);
+    a->grad_ce = static_cast<float>((1.0 - d->alpha) * d->scale);
+    return ZS_OK;
+}
+
+int set_grad(const zs_distill* d, const float* row_grad, void* grad_out, DistillArgs* a)
+{
+    if (d->rows > 0 && !grad_out) return ZS_ENULL;
+    if (!aligned_to(grad_out, elem_bytes(d->logits_dtype)) || !aligned_to(row_grad, 4))
+        return ZS_EALIGN;
+    if (grad_out == a->logits && d->rows > 1 && d->grad_pitch != d->logits_pitch)
+        return ZS_EINVAL_DISTILL;
+    a->row_grad = row_grad;
+    a->grad = grad_out;
+    return ZS_OK;
+}
+
+int set_loss(const zs_distill* d, float* loss_out, float* lse_out, float* loss_sum,
+             int64_t* counted, int32_t accumulate, void* workspace, size_t workspace_bytes,
+             DistillArgs* a)
+{
+    if (!workspace || (d->rows > 0 && !loss_out)) return ZS_ENULL;
+    if (!aligned16(workspace) || !aligned_to(loss_out, 4) || !aligned_to(lse_out, 4) ||
+        !aligned_to(loss_sum, 4) || !aligned_to(counted, 8))
+        return ZS_EALIGN;
+    if (workspace_bytes < zs_distill_workspace_bytes(d)) return ZS_EWORKSPACE;
+    const DistillSpace w = distill_space(d->rows, d->vocab, d->k);
+    char* base = static_cast<char*>(workspace);
+    a->counts = reinterpret_cast<int32_t*>(base + w.counts);
+    a->parts = reinterpret_cast<float*>(base + w.parts);
+    a->picked = reinterpret_cast<float*>(base + w.picked);
+    a->loss = loss_out;
+    a->lse_out = lse_out;
+    a->loss_sum = loss_sum;
+    a->counted = counted;
+    a->accumulate = accumulate ? 1 : 0;
+    return ZS_OK;
+}
+
+}  // namespace
+}  // namespace zs
+
+extern "C" int embed_lookup(const zs_embed* e, const void* ids, const void* table, void* out,
+                            void* stream)
+{
+    const int rc = check_embed(e);
+    if (rc != ZS_OK) return rc;
+    if (e->tokens == 0) return ZS_OK;
+    if (!ids || !table || !out) return ZS_ENULL;
+    if (!aligned_to(ids, id_bytes(e->id_dtype)) || !aligned_to(table, elem_bytes(e->table_dtype)) ||
+        !aligned_to(out, elem_bytes(e->act_dtype)))
+        return ZS_EALIGN;
+    return enqueue_embed_lookup(embed_args(e, ids, table, out), stream);
+}
+
+extern "C" int embed_grad(const zs_embed* e, const void* ids, const void* grad_out,
+                          void* grad_table, int32_t accumulate, void* workspace,
+                          size_t workspace_bytes, void* stream)
+{
+    const int rc = check_embed(e);
+    if (rc != ZS_OK) return rc;
+    if (e->tokens > ZS_EMBED_MAX || e->rows > ZS_EMBED_MAX) return ZS_EUNSUPPORTED;
+    if (!grad_table || !workspace) return ZS_ENULL;
+    if (e->tokens > 0 && (!ids || !grad_out)) return ZS_ENULL;
+    if (!aligned16(workspace) || !aligned_to(ids, id_bytes(e->id_dtype)) ||
+        !aligned_to(grad_out, elem_bytes(e->act_dtype)) ||
+        !aligned_to(grad_table, elem_bytes(e->table_dtype)))
+        return ZS_EALIGN;
+    if (workspace_bytes < zs_embed_workspace_bytes(e)) return ZS_EWORKSPACE;
+    if (e->tokens == 0 && accumulate) return ZS_OK;
+    return enqueue_embed_grad(embed_args(e, ids, grad_out, grad_table), accumulate != 0, workspace,
+                              stream);
+}
+
+extern "C" int distill_loss(const zs_distill* d, const void* logits, const zs_targets* t,
+                            float* loss_out, float* lse_out, float* loss_sum, int64_t* counted,
+                            int32_t accumulate, void* workspace, size_t workspace_bytes,
+                            void* stream)
+{
+    DistillArgs a;
+    int rc = distill_args(d, logits, t, &a);
+    if (rc != ZS_OK) return rc;
+    if (d->rows > 0 && !lse_out) return ZS_ENULL;
+    rc = set_loss(d, loss_out, lse_out, loss_sum, counted, accumulate, workspace, workspace_bytes,
+                  &a);
+    return rc != ZS_OK ? rc : enqueue_distill_loss(a, false, stream);
+}
+
+extern "C" int distill_grad(const zs_distill* d, const void* logits, const zs_targets* t,
+                            const float* lse_in, const float* row_grad, void* grad_out,
+                            void* stream)
+{
+    DistillArgs a;
+    int rc = distill_args(d, logits, t, &a);
+    if (rc != ZS_OK) return rc;
+    if (d->rows > 0 && !lse_in) return ZS_ENULL;
+    if (!aligned_to(lse_in, 4)) return ZS_EALIGN;
+    if ((rc = set_grad(d, row_grad, grad_out, &a)) != ZS_OK) return rc;
+    a.lse_in = lse_in;
+    return enqueue_distill_grad(a, stream);
+}
+
+extern "C" int distill_loss_grad(const zs_distill* d, const void* logits, const zs_targets* t,
+                                 float* loss_out, float* lse_out, const float* row_grad,
+                                 void* grad_out, float* loss_sum, int64_t* counted,
+                                 int32_t accumulate, void* workspace, size_t workspace_bytes,
+                                 void* stream)
+{
+    DistillArgs a;
+    int rc = distill_args(d, logits, t, &a);
+    if (rc != ZS_OK) return rc;
+    if ((rc = set_grad(d, row_grad, grad_out, &a)) != ZS_OK) return rc;
+    rc = set_loss(d, loss_out, lse_out, loss_sum, counted, accumulate, workspace, workspace_bytes,
+                  &a);
+    return rc != ZS_OK ? rc : enqueue_distill_loss(a, true, stream);
 }

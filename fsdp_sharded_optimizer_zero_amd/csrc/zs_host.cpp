@@ -1,5 +1,6 @@
 // zs_host.cpp -- host part of libzero_shard: shard layout, model-state and
-// communication accounting, argument checks, error strings.  No HIP calls.
+// communication accounting, workspace layouts, argument checks, error
+// strings.  No HIP calls.
 //
 // Layout: "Data parallelism, ZeRO and FSDP", section 2 "What is redundant"
 // (rank k owns slice k) and "How FSDP implements ZeRO-3" step 1 (a unit's
@@ -44,6 +45,69 @@ int check_hparams(const zs_adamw* h)
     if (h->weight_decay < 0.0) return ZS_EINVAL_HPARAM;
     if (h->step < 1) return ZS_EINVAL_HPARAM;
     return ZS_OK;
+}
+
+int check_embed(const zs_embed* e)
+{
+    if (!e) return ZS_ENULL;
+    if (e->tokens < 0 || e->rows < 1 || e->first_row < 0 || e->dim < 1) return ZS_EINVAL_EMBED;
+    // every buffer's size in bytes, and one past the last id, fit in 63 bits
+    const int64_t most = int64_t(1) << 40;
+    if (e->tokens > most || e->rows > most || e->first_row > INT64_MAX - e->rows)
+        return ZS_EINVAL_EMBED;
+    if (e->table_pitch < e->dim || e->act_pitch < e->dim) return ZS_EINVAL_EMBED;
+    if (e->table_pitch > (int64_t(1) << 60) / e->rows ||
+        e->act_pitch > (int64_t(1) << 60) / (e->tokens > 0 ? e->tokens : 1))
+        return ZS_EINVAL_EMBED;
+    if (e->id_dtype != ZS_ID_I32 && e->id_dtype != ZS_ID_I64) return ZS_EINVAL_EMBED;
+    if (e->table_dtype != ZS_BF16 && e->table_dtype != ZS_F32) return ZS_EINVAL_EMBED;
+    if (e->act_dtype != ZS_BF16 && e->act_dtype != ZS_F32) return ZS_EINVAL_EMBED;
+    if (e->reserved != 0 || !std::isfinite(static_cast<float>(e->scale))) return ZS_EINVAL_EMBED;
+    return ZS_OK;
+}
+
+int check_distill(const zs_distill* d)
+{
+    if (!d) return ZS_ENULL;
+    if (d->rows < 0 || d->rows > INT32_MAX || d->vocab < 1 || d->vocab > INT32_MAX)
+        return ZS_EINVAL_DISTILL;
+    const int64_t pitch = (int64_t(1) << 60) / (d->rows > 0 ? d->rows : 1);
+    if (d->logits_pitch < d->vocab || d->grad_pitch < d->vocab || d->logits_pitch > pitch ||
+        d->grad_pitch > pitch)
+        return ZS_EINVAL_DISTILL;
+    if (d->k < 0 || d->k > ZS_DISTILL_MAX_K) return ZS_EINVAL_DISTILL;
+    if (d->logits_dtype != ZS_BF16 && d->logits_dtype != ZS_F32) return ZS_EINVAL_DISTILL;
+    if (d->teacher_dtype != ZS_BF16 && d->teacher_dtype != ZS_F32) return ZS_EINVAL_DISTILL;
+    if (d->id_dtype != ZS_ID_I32 && d->id_dtype != ZS_ID_I64) return ZS_EINVAL_DISTILL;
+    // tau, its reciprocal and its square are normal fp32 numbers
+    if (!(d->temperature >= 1e-6 && d->temperature <= 1e6)) return ZS_EINVAL_DISTILL;
+    if (!(d->alpha >= 0.0 && d->alpha <= 1.0)) return ZS_EINVAL_DISTILL;
+    if (!std::isfinite(static_cast<float>(d->scale))) return ZS_EINVAL_DISTILL;
+    return ZS_OK;
+}
+
+EmbedSpace embed_space(int64_t tokens, int64_t rows, int64_t dim)
+{
+    EmbedSpace w;
+    w.order = 0;
+    w.row_of = w.order + round_up(tokens * 4, 256);
+    w.starts = w.row_of + round_up(tokens * 4, 256);
+    w.partials = w.starts + round_up((rows + 1) * 4, 256);
+    // one chunk has no run that crosses into another
+    const int64_t chunks = embed_chunks(tokens);
+    w.bytes = w.partials + (chunks > 1 ? round_up(chunks * 2 * dim * 4, 256) : 0);
+    return w;
+}
+
+DistillSpace distill_space(int64_t rows, int64_t vocab, int32_t k)
+{
+    DistillSpace w;
+    const int64_t splits = distill_splits(rows, vocab);
+    w.counts = 0;
+    w.parts = round_up(rows > 0 ? rows * 4 : 4, 256);
+    w.picked = w.parts + (splits > 1 ? round_up(rows * splits * kDistillPart * 4, 256) : 0);
+    w.bytes = w.picked + (splits > 1 ? round_up(rows * (k + 1) * 4, 256) : 0);
+    return w;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -135,6 +199,18 @@ size_t zs_workspace_bytes_units(const zs_shard* s, int32_t units)
     return static_cast<size_t>(zs::round_up(bytes > 0 ? bytes : 1, 256));
 }
 
+size_t zs_embed_workspace_bytes(const zs_embed* e)
+{
+    if (zs::check_embed(e) != ZS_OK || e->tokens > ZS_EMBED_MAX || e->rows > ZS_EMBED_MAX) return 0;
+    return static_cast<size_t>(zs::embed_space(e->tokens, e->rows, e->dim).bytes);
+}
+
+size_t zs_distill_workspace_bytes(const zs_distill* d)
+{
+    if (zs::check_distill(d) != ZS_OK) return 0;
+    return static_cast<size_t>(zs::distill_space(d->rows, d->vocab, d->k).bytes);
+}
+
 double zs_state_bytes(double psi, int32_t n_d, int32_t stage, double K)
 {
     if (!(psi > 0.0) || n_d < 1) return -1.0;
@@ -176,6 +252,9 @@ const char* zs_strerror(int code)
     case ZS_EZERO_TOKENS: return "global token count is zero: the update is rejected";
     case ZS_EINVAL_UNITS: return "units must be at least 1";
     case ZS_ESCRATCH: return "shard too large for the static scratch array (ZS_SCRATCH_BYTES)";
+    case ZS_EINVAL_EMBED: return "invalid zs_embed (a size, pitch, type or scale out of range)";
+    case ZS_EINVAL_DISTILL:
+        return "invalid zs_distill (a size, pitch, type, temperature, alpha or scale out of range)";
     default: return "unknown error";
     }
 }

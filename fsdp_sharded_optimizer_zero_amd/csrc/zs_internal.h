@@ -115,6 +115,104 @@ int enqueue_pack(const float* master, uint16_t* out, int64_t valid_len, int64_t 
 int prepare_device();
 int static_scratch(void** ptr);
 
+// ---- the vocabulary table (zs_vocab.hip) -----------------------------------------
+
+struct EmbedArgs {
+    const void* ids;
+    const void* src;        // lookup: table; gradient: activation gradients
+    void* dst;              // lookup: activations; gradient: table gradient
+    int64_t tokens, rows, first_row, dim;
+    int64_t table_pitch, act_pitch;
+    float scale;
+    int32_t id64, table_f32, act_f32;
+};
+
+// embed_grad sorts the tokens by row, cuts the sorted order into chunks of
+// embed_chunk positions and sums each chunk's runs; a run that crosses chunks
+// leaves one partial row in each (at most two per chunk) for the join.
+// Longer chunks mean fewer partials, shorter ones more parallel work: 8
+// positions until the chunks number 1024, then twice as many, up to 64.
+inline int32_t embed_chunk(int64_t tokens)
+{
+    int32_t c = 8;
+    while (c < 64 && tokens > 1024 * static_cast<int64_t>(c)) c *= 2;
+    return c;
+}
+inline int64_t embed_chunks(int64_t tokens)
+{
+    const int64_t c = embed_chunk(tokens);
+    return (tokens + c - 1) / c;
+}
+
+// Workspace of embed_grad, in bytes from its start.
+struct EmbedSpace {
+    int64_t order;     // int32[tokens]: token positions sorted by row
+    int64_t row_of;    // int32[tokens]: their rows
+    int64_t starts;    // int32[rows + 1]: first sorted position of each row
+    int64_t partials;  // fp32[chunks][2][dim]
+    int64_t bytes;
+};
+EmbedSpace embed_space(int64_t tokens, int64_t rows, int64_t dim);
+
+int enqueue_embed_lookup(const EmbedArgs& a, void* stream);
+int enqueue_embed_grad(const EmbedArgs& a, bool accumulate, void* workspace, void* stream);
+
+struct DistillArgs {
+    const void* logits;
+    const void* teacher_ids;
+    const void* teacher_logits;
+    const float* teacher_lse;
+    const void* labels;
+    const float* lse_in;
+    const float* row_grad;
+    float* loss;
+    float* lse_out;
+    void* grad;
+    int32_t* counts;        // workspace: 1 for a row that counts
+    float* parts;           // workspace: fp32[rows][splits][kDistillPart]
+    float* picked;          // workspace: fp32[rows][k + 1], logits at the entries and the label
+    float* loss_sum;
+    int64_t* counted;
+    int64_t rows, vocab, logits_pitch, grad_pitch;
+    int64_t part_cols;      // columns of one part (a multiple of 8)
+    int32_t splits;         // parts a row is cut into
+    int32_t k;              // 0 where alpha is 0
+    int32_t accumulate;
+    int32_t f32, teacher_f32, id64, kd, ce;
+    float inv_tau;          // 1/tau
+    float loss_kd, loss_ce; // alpha tau^2, 1 - alpha
+    float grad_kd, grad_ce; // alpha tau scale, (1 - alpha) scale
+};
+
+// A row cut into parts leaves per part: the maximum, and the sums of
+// exp((s - max)/tau) and exp(s - max).
+constexpr int kDistillPart = 4;
+// Rows below this number leave CUs idle, or a ragged last turn, at one block
+// a row: each row is then cut into parts.
+constexpr int64_t kDistillRows = 512;
+// Parts a row is cut into: about two blocks per CU in all, at least 4096
+// columns each.
+inline int32_t distill_splits(int64_t rows, int64_t vocab)
+{
+    if (rows < 1 || rows >= kDistillRows) return 1;
+    const int64_t want = (kDistillRows + rows - 1) / rows, most = (vocab + 4095) / 4096;
+    return static_cast<int32_t>(want < most ? want : most);
+}
+struct DistillSpace {
+    int64_t counts, parts, picked, bytes;
+};
+DistillSpace distill_space(int64_t rows, int64_t vocab, int32_t k);
+
+int enqueue_distill_loss(DistillArgs a, bool with_grad, void* stream);
+int enqueue_distill_grad(DistillArgs a, void* stream);
+
+// Loads the vocabulary kernels on the current device (so that a first call
+// may be captured); ZS_OK or ZS_ELAUNCH.
+int prepare_vocab();
+
+int check_embed(const zs_embed* e);
+int check_distill(const zs_distill* d);
+
 // Host-side checks; each returns ZS_OK or the error code to report.
 int check_shard(const zs_shard* s);
 int check_hparams(const zs_adamw* h);

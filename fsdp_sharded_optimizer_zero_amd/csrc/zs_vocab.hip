@@ -1,0 +1,1089 @@
+// zs_vocab.hip -- CDNA4 (gfx950) kernels of the vocabulary table: embedding
+// lookup and gradient, distillation loss and gradient; their launch shapes,
+// and the enqueue_* functions through which the C-ABI entry points
+// (zs_abi.cpp) run them.
+//
+// What is computed is stated with the entry points in zero_shard.h.  All of
+// it is bound by HBM: a lookup and an embedding gradient do one product or
+// sum per element moved, a distillation about ten operations and one or two
+// exponentials per logit (nothing here is a contraction, so no MFMA).
+//
+// Rows of odd length start anywhere: every 16-byte access is declared with
+// the alignment of its element, which compiles to the same one instruction
+// (global memory takes any byte address in the unaligned access mode the HSA
+// ABI sets), and the elements behind a row's last full vector go one by one.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "zs_internal.h"
+
+namespace zs {
+namespace {
+
+#ifndef ZS_MAX_LAUNCH_THREADS
+#define ZS_MAX_LAUNCH_THREADS (int64_t(1) << 31)
+#endif
+constexpr int64_t max_blocks(int threads) { return ZS_MAX_LAUNCH_THREADS / threads; }
+
+constexpr int kWave = 64;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLowest = -3.402823466e38f;
+
+// ---- elements ------------------------------------------------------------------
+
+typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(2)));
+
+__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
+
+// fp32 -> bf16, round to nearest even, any NaN to 0x7FC0 (as the pack does).
+__device__ __forceinline__ uint32_t bf16_rne(float f)
+{
+    const uint32_t u = __float_as_uint(f);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0x7FC0u;
+    return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
+{
+    return bf16_rne(lo) | (bf16_rne(hi) << 16);
+}
+
+__device__ __forceinline__ float widen(uint16_t x)
+{
+    return __uint_as_float(static_cast<uint32_t>(x) << 16);
+}
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ void put(uint16_t* p, float v) { *p = static_cast<uint16_t>(bf16_rne(v)); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+
+// N consecutive elements from any element address.
+template <int N>
+__device__ __forceinline__ void load_n(const uint16_t* p, float v[N])
+{
+    if constexpr (N == 8) {
+        const u32x4_u b = *reinterpret_cast<const u32x4_u*>(p);
+        v[0] = bf16_lo(b.x); v[1] = bf16_hi(b.x);
+        v[2] = bf16_lo(b.y); v[3] = bf16_hi(b.y);
+        v[4] = bf16_lo(b.z); v[5] = bf16_hi(b.z);
+        v[6] = bf16_lo(b.w); v[7] = bf16_hi(b.w);
+    } else {
+        const u32x2_u b = *reinterpret_cast<const u32x2_u*>(p);
+        v[0] = bf16_lo(b.x); v[1] = bf16_hi(b.x);
+        v[2] = bf16_lo(b.y); v[3] = bf16_hi(b.y);
+    }
+}
+template <int N>
+__device__ __forceinline__ void load_n(const float* p, float v[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const f32x4_u b = *reinterpret_cast<const f32x4_u*>(p + i);
+        v[i] = b.x; v[i + 1] = b.y; v[i + 2] = b.z; v[i + 3] = b.w;
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_n(uint16_t* p, const float v[N])
+{
+    if constexpr (N == 8)
+        *reinterpret_cast<u32x4_u*>(p) = u32x4_u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                 pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    else
+        *reinterpret_cast<u32x2_u*>(p) = u32x2_u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+template <int N>
+__device__ __forceinline__ void store_n(float* p, const float v[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+        *reinterpret_cast<f32x4_u*>(p + i) = f32x4_u{v[i], v[i + 1], v[i + 2], v[i + 3]};
+}
+
+// Subtracting in 64 bits without a sign: an id below first gives a number
+// above every row count.
+__device__ __forceinline__ uint64_t row_of_id(int64_t id, int64_t first)
+{
+    return static_cast<uint64_t>(id) - static_cast<uint64_t>(first);
+}
+
+__device__ __forceinline__ int64_t read_id(const void* ids, int id64, int64_t i)
+{
+    return id64 ? static_cast<const int64_t*>(ids)[i]
+                : static_cast<int64_t>(static_cast<const int32_t*>(ids)[i]);
+}
+
+// ---- embedding lookup -------------------------------------------------------------
+
+constexpr int kEmbedThreads = 256;
+
+// Lanes (a power of two, as a shift) that share one row of `dim` elements at
+// n a lane, `most` at most.
+int lane_shift(int64_t dim, int n, int most)
+{
+    int s = 0;
+    while (s < most && (int64_t(n) << s) < dim) ++s;
+    return s;
+}
+
+// 1 << shift lanes take one token each time; a block takes 256 >> shift.
+template <typename TT, typename AT, int N>
+__global__ void __launch_bounds__(kEmbedThreads)
+    k_embed_lookup(EmbedArgs a, int shift, int64_t b0)
+{
+    const int64_t t = ((b0 + blockIdx.x) << (8 - shift)) + (threadIdx.x >> shift);
+    if (t >= a.tokens) return;
+    const int lanes = 1 << shift;
+    const uint64_t row = row_of_id(read_id(a.ids, a.id64, t), a.first_row);
+    const bool here = row < static_cast<uint64_t>(a.rows);
+    const TT* src = static_cast<const TT*>(a.src) + (here ? row * a.table_pitch : 0);
+    AT* dst = static_cast<AT*>(a.dst) + t * a.act_pitch;
+    for (int64_t c = static_cast<int64_t>(threadIdx.x & (lanes - 1)) * N; c < a.dim;
+         c += static_cast<int64_t>(lanes) * N) {
+        if (c + N <= a.dim) {
+            float v[N];
+            if (here) {
+                load_n<N>(src + c, v);
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] *= a.scale;
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] = 0.0f;
+            }
+            store_n<N>(dst + c, v);
+        } else {
+            for (int64_t i = c; i < a.dim; ++i)
+                put(dst + i, here ? widen(src[i]) * a.scale : 0.0f);
+        }
+    }
+}
+
+// ---- embedding gradient: sort -----------------------------------------------------
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / kWave;
+constexpr int kSortRows = 960;      // rows of one bucket at most: the counts of 16
+                                    // waves and the sums fit 64 KB of LDS
+constexpr int kSortBuckets = 256;   // buckets at least (one per CU), rows permitting
+
+struct SortShape {
+    int64_t buckets;
+    uint32_t rows;      // rows of a bucket
+    int32_t bits;       // bits of a row number inside a bucket
+};
+SortShape sort_shape(int64_t rows)
+{
+    SortShape s;
+    s.buckets = rows < kSortBuckets ? rows : kSortBuckets;
+    if (rows > s.buckets * kSortRows) s.buckets = (rows + kSortRows - 1) / kSortRows;
+    s.rows = static_cast<uint32_t>((rows + s.buckets - 1) / s.buckets);
+    s.buckets = (rows + s.rows - 1) / s.rows;
+    s.bits = 0;
+    while ((1u << s.bits) < s.rows) ++s.bits;
+    return s;
+}
+
+// Lanes of the wave whose row equals this lane's, among those with `in`
+// set (0 bits elsewhere): the intersection over the row's bits of the lanes
+// that agree in that bit.
+__device__ __forceinline__ uint64_t same_row(bool in, int row, int bits)
+{
+    uint64_t m = __ballot(in);
+    for (int b = 0; b < bits; ++b) {
+        const bool bit = (row >> b) & 1;
+        const uint64_t set = __ballot(bit);
+        m &= bit ? set : ~set;
+    }
+    return m;
+}
+
+// A stable counting sort of the tokens by row, one block per bucket of
+// consecutive rows and no exchange between blocks: every block reads all ids
+// (a batch of ids is small and comes from L2 after the first block), counts
+// the tokens of earlier buckets (where its own part of the order begins) and
+// of each of its rows, and then places its tokens.  Each wave takes one
+// contiguous part of the tokens, so a token's place is: the row's start, the
+// tokens of that row in earlier waves, those in earlier turns of its wave,
+// and those in lower lanes.
+__global__ void __launch_bounds__(kSortThreads)
+    k_embed_sort(EmbedArgs a, SortShape s, int32_t* order, int32_t* row_of, int32_t* starts)
+{
+    __shared__ int32_t hist[kSortWaves][kSortRows];
+    __shared__ int32_t wave_sum[kSortWaves];
+    __shared__ int32_t wave_below[kSortWaves];
+    const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
+    // this bucket's rows: [lo, lo + here)
+    const uint64_t lo = static_cast<uint64_t>(blockIdx.x) * s.rows;
+    const uint64_t rows = a.rows;
+    const uint32_t here = rows - lo < s.rows ? static_cast<uint32_t>(rows - lo) : s.rows;
+    for (int w = 0; w < kSortWaves; ++w)
+        for (uint32_t r = tid; r < here; r += kSortThreads) hist[w][r] = 0;
+    __syncthreads();
+
+    const int tokens = static_cast<int>(a.tokens);
+    const int turns = (tokens + kSortThreads - 1) / kSortThreads;   // of one wave
+    const int t0 = wave * turns * kWave;
+    const uint64_t lower = (uint64_t(1) << lane) - 1;
+    int below = 0;
+    for (int i = 0; i < turns; ++i) {
+        const int t = t0 + i * kWave + lane;
+        uint64_t row = UINT64_MAX;
+        if (t < tokens) row = row_of_id(read_id(a.ids, a.id64, t), a.first_row);
+        below += row < lo;
+        const bool in = row - lo < here;
+        const int r = static_cast<int>(row - lo);
+        if (__ballot(in) == 0) continue;
+        const uint64_t same = same_row(in, r, s.bits);
+        if (in && (same & lower) == 0) hist[wave][r] += __popcll(same);
+    }
+    for (int o = kWave / 2; o > 0; o >>= 1) below += __shfl_xor(below, o);
+    if (lane == 0) wave_below[wave] = below;
+    __syncthreads();
+
+    // per row: counts of earlier waves, then the row's start in the bucket
+    int total = 0;
+    if (tid < static_cast<int>(here)) {
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int n = hist[w][tid];
+            hist[w][tid] = total;
+            total += n;
+        }
+    }
+    int incl = total;
+    for (int o = 1; o < kWave; o <<= 1) {
+        const int v = __shfl_up(incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == kWave - 1) wave_sum[wave] = incl;
+    __syncthreads();
+    int base = incl - total;
+    for (int w = 0; w < kSortWaves; ++w) {
+        base += wave_below[w];
+        if (w < wave) base += wave_sum[w];
+    }
+    if (tid < static_cast<int>(here)) {
+        starts[lo + tid] = base;
+        if (lo + tid == rows - 1) starts[rows] = base + total;
+        for (int w = 0; w < kSortWaves; ++w) hist[w][tid] += base;
+    }
+    __syncthreads();
+
+    for (int i = 0; i < turns; ++i) {
+        const int t = t0 + i * kWave + lane;
+        uint64_t row = UINT64_MAX;
+        if (t < tokens) row = row_of_id(read_id(a.ids, a.id64, t), a.first_row);
+        const bool in = row - lo < here;
+        const int r = static_cast<int>(row - lo);
+        if (__ballot(in) == 0) continue;
+        const uint64_t same = same_row(in, r, s.bits);
+        int first = 0;
+        if (in) first = hist[wave][r];
+        // every lane has read before the first lane of each row adds
+        __builtin_amdgcn_wave_barrier();
+        if (in) {
+            const int before = __popcll(same & lower);
+            if (before == 0) hist[wave][r] = first + __popcll(same);
+            order[first + before] = t;
+            row_of[first + before] = static_cast<int32_t>(row);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// ---- embedding gradient: sums -------------------------------------------------------
+
+struct SumPlan {
+    const int32_t* order;
+    const int32_t* row_of;
+    const int32_t* starts;
+    float* partials;        // [chunks][2][dim]: a run that began before the
+                            // chunk, a run that goes on behind it
+    int64_t chunks;
+    int64_t splits;         // column parts of a row
+    int64_t sum_blocks;     // blocks that sum; the rest clear empty rows
+    int32_t chunk;          // sorted positions of a chunk
+    int32_t shift;          // log2 of the lanes of one column part
+    int32_t zero_shift;     // log2 of the lanes that clear one row
+};
+
+// scale * acc into the gradient row (added to it if ADD).
+template <typename GT, int N, bool ADD>
+__device__ __forceinline__ void put_row(const EmbedArgs& a, int64_t row, int64_t c,
+                                        const float acc[N])
+{
+    GT* g = static_cast<GT*>(a.dst) + row * a.table_pitch + c;
+    if (c + N <= a.dim) {
+        float v[N];
+        if constexpr (ADD) {
+            load_n<N>(g, v);
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += a.scale * acc[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = a.scale * acc[i];
+        }
+        store_n<N>(g, v);
+    } else {
+        for (int i = 0; i < N; ++i)
+            if (c + i < a.dim)
+                put(g + i, ADD ? widen(g[i]) + a.scale * acc[i] : a.scale * acc[i]);
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void put_partial(float* p, int64_t c, int64_t dim, const float acc[N])
+{
+    if (c + N <= dim) {
+        store_n<N>(p + c, acc);
+    } else {
+        for (int i = 0; i < N; ++i)
+            if (c + i < dim) p[c + i] = acc[i];
+    }
+}
+
+constexpr int kSumUnroll = 8;   // divides every embed_chunk
+
+// One worker (1 << shift lanes) sums one chunk of sorted positions over one
+// part of the columns: it walks the positions, kSumUnroll loads in flight,
+// and hands a run's sum on where the row changes.
+template <typename AT, typename GT, int N, bool ADD>
+__global__ void __launch_bounds__(kEmbedThreads)
+    k_embed_sum(EmbedArgs a, SumPlan p, int64_t b0)
+{
+    const int64_t block = b0 + blockIdx.x;
+    if (!ADD && block >= p.sum_blocks) {
+        const int64_t row = ((block - p.sum_blocks) << (8 - p.zero_shift)) +
+                            (threadIdx.x >> p.zero_shift);
+        if (row >= a.rows || p.starts[row] != p.starts[row + 1]) return;
+        const int lanes = 1 << p.zero_shift;
+        GT* g = static_cast<GT*>(a.dst) + row * a.table_pitch;
+        const float z[N] = {};
+        for (int64_t c = static_cast<int64_t>(threadIdx.x & (lanes - 1)) * N; c < a.dim;
+             c += static_cast<int64_t>(lanes) * N) {
+            if (c + N <= a.dim) {
+                store_n<N>(g + c, z);
+            } else {
+                for (int64_t i = c; i < a.dim; ++i) put(g + i, 0.0f);
+            }
+        }
+        return;
+    }
+    const int64_t worker = (block << (8 - p.shift)) + (threadIdx.x >> p.shift);
+    const int64_t chunk = worker / p.splits;
+    const int lanes = 1 << p.shift;
+    const int64_t c = ((worker - chunk * p.splits) * lanes + (threadIdx.x & (lanes - 1))) * N;
+    const int32_t n = p.starts[a.rows];
+    const int64_t p0 = chunk * p.chunk;
+    if (p0 >= n || c >= a.dim) return;
+    const int64_t p1 = p0 + p.chunk < n ? p0 + p.chunk : n;
+    const AT* src = static_cast<const AT*>(a.src) + c;
+    const bool full = c + N <= a.dim;
+    float* partial = p.partials + chunk * 2 * a.dim;
+
+    int row = p.row_of[p0];
+    bool began = p0 == 0 || p.row_of[p0 - 1] != row;
+    float acc[N] = {};
+    for (int64_t q = p0; q < p1; q += kSumUnroll) {
+        float x[kSumUnroll][N];
+        int rows[kSumUnroll];
+#pragma unroll
+        for (int u = 0; u < kSumUnroll; ++u) {
+            const int64_t at = q + u < p1 ? q + u : p1 - 1;
+            rows[u] = p.row_of[at];
+            const AT* s = src + p.order[at] * a.act_pitch;
+            if (full) {
+                load_n<N>(s, x[u]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) x[u][i] = c + i < a.dim ? widen(s[i]) : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kSumUnroll; ++u) {
+            if (q + u >= p1) break;
+            if (rows[u] != row) {
+                if (began) put_row<GT, N, ADD>(a, row, c, acc);
+                else put_partial<N>(partial, c, a.dim, acc);
+                row = rows[u];
+                began = true;
+#pragma unroll
+                for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[i] += x[u][i];
+        }
+    }
+    const bool ends = p1 >= n || p.row_of[p1] != row;
+    if (!began) put_partial<N>(partial, c, a.dim, acc);
+    else if (ends) put_row<GT, N, ADD>(a, row, c, acc);
+    else put_partial<N>(partial + a.dim, c, a.dim, acc);
+}
+
+// The runs that cross chunks: the block of the chunk a run begins in adds
+// its partials in order, each group of lanes a contiguous part of them.
+template <typename GT, int N, bool ADD>
+__global__ void __launch_bounds__(kEmbedThreads)
+    k_embed_join(EmbedArgs a, SumPlan p, int64_t b0)
+{
+    __shared__ float sums[kEmbedThreads * N];
+    const int64_t block = b0 + blockIdx.x;
+    const int64_t chunk = block / p.splits;
+    const int32_t n = p.starts[a.rows];
+    const int64_t p0 = chunk * p.chunk, p1 = p0 + p.chunk;
+    if (p1 >= n) return;
+    const int32_t row = p.row_of[p1];
+    const int32_t begin = p.starts[row];
+    if (begin < p0 || begin >= p1) return;      // begins in another chunk
+    const int64_t count = (p.starts[row + 1] - 1) / p.chunk - chunk + 1;
+    const int lanes = 1 << p.shift, groups = kEmbedThreads >> p.shift;
+    const int group = threadIdx.x >> p.shift, lane = threadIdx.x & (lanes - 1);
+    const int64_t c = ((block - chunk * p.splits) * lanes + lane) * N;
+    float acc[N] = {};
+    if (c < a.dim) {
+        for (int64_t i = group * count / groups; i < (group + 1) * count / groups; ++i) {
+            const float* s = p.partials + ((chunk + i) * 2 + (i == 0 ? 1 : 0)) * a.dim + c;
+            float x[N];
+            if (c + N <= a.dim) {
+                load_n<N>(s, x);
+            } else {
+                for (int j = 0; j < N; ++j) x[j] = c + j < a.dim ? s[j] : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc[j] += x[j];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) sums[threadIdx.x * N + j] = acc[j];
+    __syncthreads();
+    if (group != 0 || c >= a.dim) return;
+    for (int g = 1; g < groups; ++g)
+        for (int j = 0; j < N; ++j) acc[j] += sums[(g * lanes + lane) * N + j];
+    put_row<GT, N, ADD>(a, row, c, acc);
+}
+
+// ---- distillation -------------------------------------------------------------------
+
+constexpr int kDistillThreads = 512;
+constexpr int kDistillWaves = kDistillThreads / kWave;
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Running statistics of a softmax: the maximum so far and the sums of
+// exp((s - m)/tau) and (CE) exp(s - m).  The maximum starts at the lowest
+// finite value, so that -Inf logits have weight 0 and no Inf - Inf occurs.
+struct Stat {
+    float m, a, b;
+};
+
+template <bool CE>
+__device__ __forceinline__ void rescale(Stat& s, float m, float c)
+{
+    s.a *= exp2_hw((s.m - m) * c);
+    if constexpr (CE) s.b *= exp2_hw((s.m - m) * kLog2e);
+    s.m = m;
+}
+
+template <bool CE>
+__device__ __forceinline__ void join(Stat& s, Stat o, float c)
+{
+    const float m = fmaxf(s.m, o.m);
+    rescale<CE>(s, m, c);
+    rescale<CE>(o, m, c);
+    s.a += o.a;
+    if constexpr (CE) s.b += o.b;
+}
+
+template <bool CE>
+__device__ __forceinline__ Stat wave_join(Stat s, float c)
+{
+    for (int o = kWave / 2; o > 0; o >>= 1) {
+        Stat t;
+        t.m = __shfl_xor(s.m, o);
+        t.a = __shfl_xor(s.a, o);
+        t.b = CE ? __shfl_xor(s.b, o) : 0.0f;
+        join<CE>(s, t, c);
+    }
+    return s;
+}
+
+template <bool CE>
+__device__ __forceinline__ Stat block_join(Stat s, float c, float* lds)
+{
+    const int wave = threadIdx.x / kWave;
+    s = wave_join<CE>(s, c);
+    __syncthreads();
+    if (threadIdx.x % kWave == 0) {
+        lds[wave * 3] = s.m;
+        lds[wave * 3 + 1] = s.a;
+        lds[wave * 3 + 2] = s.b;
+    }
+    __syncthreads();
+    Stat r = {lds[0], lds[1], lds[2]};
+    for (int w = 1; w < kDistillWaves; ++w)
+        join<CE>(r, Stat{lds[w * 3], lds[w * 3 + 1], lds[w * 3 + 2]}, c);
+    return r;
+}
+
+__device__ __forceinline__ float block_sum(float x, float* lds)
+{
+    for (int o = kWave / 2; o > 0; o >>= 1) x += __shfl_xor(x, o);
+    __syncthreads();
+    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = x;
+    __syncthreads();
+    float r = lds[0];
+    for (int w = 1; w < kDistillWaves; ++w) r += lds[w];
+    return r;
+}
+
+__device__ __forceinline__ float block_max(float x, float* lds)
+{
+    for (int o = kWave / 2; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o));
+    __syncthreads();
+    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = x;
+    __syncthreads();
+    float r = lds[0];
+    for (int w = 1; w < kDistillWaves; ++w) r = fmaxf(r, lds[w]);
+    return r;
+}
+
+// Elements of one 16-byte vector of logits.
+template <typename T>
+constexpr int kVec = 16 / sizeof(T);
+
+// The statistics of columns [c0, c1) of a row, over the block's threads.
+template <typename T, bool CE>
+__device__ __forceinline__ Stat scan(const T* row, int64_t c0, int64_t c1, float c)
+{
+    constexpr int N = kVec<T>;
+    Stat s = {kLowest, 0.0f, 0.0f};
+    const int64_t nv = (c1 - c0) / N;
+    for (int64_t v = threadIdx.x; v < nv; v += kDistillThreads) {
+        float x[N];
+        load_n<N>(row + c0 + v * N, x);
+        float m = x[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
+        if (m > s.m) rescale<CE>(s, m, c);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            s.a += exp2_hw((x[i] - s.m) * c);
+            if constexpr (CE) s.b += exp2_hw((x[i] - s.m) * kLog2e);
+        }
+    }
+    const int64_t e = c0 + nv * N + threadIdx.x;
+    if (e < c1) {
+        const float x = widen(row[e]);
+        if (x > s.m) rescale<CE>(s, x, c);
+        s.a += exp2_hw((x - s.m) * c);
+        if constexpr (CE) s.b += exp2_hw((x - s.m) * kLog2e);
+    }
+    return s;
+}
+
+// A row's targets in LDS: entry k's column (-1: no entry), its log p and p
+// (the label, with CE, is entry K), and the logit at each.
+struct Entries {
+    int32_t* col;
+    float* logp;
+    float* p;
+    float* s;
+    int n;          // K, or K + 1 with the label
+    int label;
+    float mass;     // sum of p
+    bool counts;
+};
+
+// Entries a row can hold, a multiple of 4 (col is searched four at a time).
+__host__ __device__ constexpr int entry_slots(int k) { return (k + 1 + 3) / 4 * 4; }
+size_t entry_bytes(int k) { return static_cast<size_t>(entry_slots(k)) * 16; }
+
+__device__ __forceinline__ int read_column(const void* ids, int id64, int64_t i, int64_t vocab)
+{
+    const int64_t id = read_id(ids, id64, i);
+    return id >= 0 && id < vocab ? static_cast<int>(id) : -1;
+}
+
+// Whether the row counts, and its label (-1: none).
+__device__ __forceinline__ bool row_counts(const DistillArgs& a, int64_t row, int* label)
+{
+    *label = -1;
+    if (a.labels) {
+        *label = read_column(a.labels, a.id64, row, a.vocab);
+        if (*label < 0) return false;
+    }
+    if (a.ce) return true;
+    int any = 0;
+    for (int k = threadIdx.x; k < a.k; k += kDistillThreads) {
+        const int64_t at = row * a.k + k;
+        const float u = a.teacher_f32 ? static_cast<const float*>(a.teacher_logits)[at]
+                                      : widen(static_cast<const uint16_t*>(a.teacher_logits)[at]);
+        any |= read_column(a.teacher_ids, a.id64, at, a.vocab) >= 0 && !(u == -INFINITY);
+    }
+    return __syncthreads_or(any) != 0;
+}
+
+__device__ __forceinline__ Entries load_targets(const DistillArgs& a, int64_t row, char* lds,
+                                                float* red)
+{
+    const int slots = entry_slots(a.k);
+    Entries e;
+    e.col = reinterpret_cast<int32_t*>(lds);
+    e.logp = reinterpret_cast<float*>(lds + slots * 4);
+    e.p = e.logp + slots;
+    e.s = e.p + slots;
+    e.n = a.k + a.ce;
+    e.counts = row_counts(a, row, &e.label);
+    e.mass = 0.0f;
+    if (!e.counts) return e;
+    float top = kLowest;
+    for (int k = threadIdx.x; k < slots; k += kDistillThreads) {
+        int col = -1;
+        float u = 0.0f;
+        if (k < a.k) {
+            const int64_t at = row * a.k + k;
+            col = read_column(a.teacher_ids, a.id64, at, a.vocab);
+            u = a.teacher_f32 ? static_cast<const float*>(a.teacher_logits)[at]
+                              : widen(static_cast<const uint16_t*>(a.teacher_logits)[at]);
+            if (u == -INFINITY) col = -1;
+            u *= a.inv_tau;
+            if (col >= 0) top = fmaxf(top, u);
+        } else if (k == a.k && a.ce) {
+            col = e.label;
+        }
+        e.col[k] = col;
+        e.logp[k] = u;
+    }
+    if (a.k == 0) {
+        __syncthreads();
+        return e;
+    }
+    float norm;
+    if (a.teacher_lse) {
+        norm = a.teacher_lse[row];
+    } else {
+        top = block_max(top, red);
+        float sum = 0.0f;
+        for (int k = threadIdx.x; k < a.k; k += kDistillThreads)
+            if (e.col[k] >= 0) sum += expf(e.logp[k] - top);
+        norm = top + logf(block_sum(sum, red));
+    }
+    float mass = 0.0f;
+    for (int k = threadIdx.x; k < a.k; k += kDistillThreads) {
+        const float logp = e.logp[k] - norm;
+        const float p = e.col[k] >= 0 ? expf(logp) : 0.0f;
+        e.logp[k] = logp;
+        e.p[k] = p;
+        mass += p;
+    }
+    e.mass = block_sum(mass, red);
+    return e;
+}
+
+// The row's loss from its statistics (all threads get it).
+template <typename LogitAt>
+__device__ __forceinline__ float row_loss(const DistillArgs& a, const Entries& e, const Stat& st,
+                                          LogitAt logit, float* red)
+{
+    float kd = 0.0f;
+    const float log_a = logf(st.a);
+    for (int k = threadIdx.x; k < a.k; k += kDistillThreads)
+        if (e.col[k] >= 0 && e.p[k] != 0.0f)
+            kd += e.p[k] * (e.logp[k] - ((logit(k) - st.m) * a.inv_tau - log_a));
+    float loss = a.kd ? a.loss_kd * block_sum(kd, red) : 0.0f;
+    if (a.ce) loss += a.loss_ce * (logf(st.b) - (logit(a.k) - st.m));
+    return loss;
+}
+
+// A softmax as the gradient needs it: value * exp2((s - m) * c).
+struct Slope {
+    float m_kd, g_kd, m_ce, g_ce;
+};
+
+template <bool CE>
+__device__ __forceinline__ float slope_at(const Slope& g, float x, float c)
+{
+    float v = g.g_kd * exp2_hw((x - g.m_kd) * c);
+    if constexpr (CE) v += g.g_ce * exp2_hw((x - g.m_ce) * kLog2e);
+    return v;
+}
+
+// The gradient of columns [c0, c1) of a row.  The entries' columns are
+// written a second time, after a barrier, with their share taken off before
+// the one rounding: the first entry of a column adds up all of that column's.
+template <typename T, bool CE>
+__device__ __forceinline__ void put_grad(const DistillArgs& a, const Entries& e, const Slope& g,
+                                         float row_grad, const T* row, T* out, int64_t c0,
+                                         int64_t c1, float c)
+{
+    constexpr int N = kVec<T>;
+    // the logits at the entries, before they may be overwritten
+    for (int k = threadIdx.x; k < e.n; k += kDistillThreads) {
+        const int col = e.col[k];
+        if (col >= c0 && col < c1) e.s[k] = widen(row[col]);
+    }
+    __syncthreads();
+    const int64_t nv = (c1 - c0) / N;
+    for (int64_t v = threadIdx.x; v < nv; v += kDistillThreads) {
+        float x[N];
+        load_n<N>(row + c0 + v * N, x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = slope_at<CE>(g, x[i], c);
+        store_n<N>(out + c0 + v * N, x);
+    }
+    const int64_t at = c0 + nv * N + threadIdx.x;
+    if (at < c1) put(out + at, slope_at<CE>(g, widen(row[at]), c));
+    __syncthreads();
+    for (int k = threadIdx.x; k < e.n; k += kDistillThreads) {
+        const int col = e.col[k];
+        if (col < c0 || col >= c1) continue;
+        bool first = true;
+        for (int j = 0; j < k; ++j) first = first && e.col[j] != col;
+        if (!first) continue;
+        float take = 0.0f;
+        for (int j = k; j < e.n; ++j)
+            if (e.col[j] == col)
+                take += row_grad * (j < a.k ? a.grad_kd * e.p[j] : a.grad_ce);
+        put(out + col, slope_at<CE>(g, e.s[k], c) - take);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void put_zeros(T* out, int64_t c0, int64_t c1)
+{
+    constexpr int N = kVec<T>;
+    const float z[N] = {};
+    const int64_t nv = (c1 - c0) / N;
+    for (int64_t v = threadIdx.x; v < nv; v += kDistillThreads) store_n<N>(out + c0 + v * N, z);
+    const int64_t e = c0 + nv * N + threadIdx.x;
+    if (e < c1) put(out + e, 0.0f);
+}
+
+// Loss, statistics and flag of a row, by one thread.
+__device__ __forceinline__ void put_loss(const DistillArgs& a, int64_t row, bool counts,
+                                         float loss, const Stat& st)
+{
+    if (threadIdx.x != 0) return;
+    a.loss[row] = counts ? loss : 0.0f;
+    a.counts[row] = counts;
+    if (a.lse_out) {
+        a.lse_out[2 * row] = counts ? st.m * a.inv_tau + logf(st.a) : 0.0f;
+        a.lse_out[2 * row + 1] = counts && a.ce ? st.m + logf(st.b) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ Slope slope_of(const DistillArgs& a, const Entries& e, const Stat& st,
+                                          float row_grad)
+{
+    return Slope{st.m, row_grad * a.grad_kd * e.mass / st.a, st.m,
+                 a.ce ? row_grad * a.grad_ce / st.b : 0.0f};
+}
+
+// One block per row: loss, and with GRAD the gradient.
+template <typename T, bool CE, bool GRAD>
+__global__ void __launch_bounds__(kDistillThreads)
+    k_distill_row(DistillArgs a, int64_t b0)
+{
+    extern __shared__ __align__(16) char lds[];
+    __shared__ float red[kDistillWaves * 3];
+    const int64_t row = b0 + blockIdx.x;
+    const float c = a.inv_tau * kLog2e;
+    const T* s = static_cast<const T*>(a.logits) + row * a.logits_pitch;
+    T* out = static_cast<T*>(a.grad) + row * a.grad_pitch;
+    const Entries e = load_targets(a, row, lds, red);
+    if (!e.counts) {
+        put_loss(a, row, false, 0.0f, Stat{});
+        if constexpr (GRAD) put_zeros(out, 0, a.vocab);
+        return;
+    }
+    const Stat st = block_join<CE>(scan<T, CE>(s, 0, a.vocab, c), c, red);
+    const float loss =
+        row_loss(a, e, st, [&](int k) { return widen(s[e.col[k]]); }, red);
+    put_loss(a, row, true, loss, st);
+    if constexpr (GRAD) {
+        const float rg = a.row_grad ? a.row_grad[row] : 1.0f;
+        // every thread's logits for the loss are read before any is overwritten
+        put_grad<T, CE>(a, e, slope_of(a, e, st, rg), rg, s, out, 0, a.vocab, c);
+    }
+}
+
+// One block per part of a row: the part's statistics; the first part's block
+// also picks the logits at the entries, for the loss.
+template <typename T, bool CE>
+__global__ void __launch_bounds__(kDistillThreads)
+    k_distill_parts(DistillArgs a, int64_t b0)
+{
+    __shared__ float red[kDistillWaves * 3];
+    const int64_t block = b0 + blockIdx.x, row = block / a.splits;
+    const int part = static_cast<int>(block - row * a.splits);
+    int label;
+    if (!row_counts(a, row, &label)) return;
+    const T* s = static_cast<const T*>(a.logits) + row * a.logits_pitch;
+    if (part == 0) {
+        for (int k = threadIdx.x; k < a.k + a.ce; k += kDistillThreads) {
+            const int col = k < a.k ? read_column(a.teacher_ids, a.id64, row * a.k + k, a.vocab)
+                                    : label;
+            if (col >= 0) a.picked[row * (a.k + 1) + k] = widen(s[col]);
+        }
+    }
+    const int64_t c0 = part * a.part_cols;
+    const int64_t c1 = c0 + a.part_cols < a.vocab ? c0 + a.part_cols : a.vocab;
+    const float c = a.inv_tau * kLog2e;
+    const Stat st = block_join<CE>(scan<T, CE>(s, c0, c1, c), c, red);
+    if (threadIdx.x == 0) {
+        float* o = a.parts + block * kDistillPart;
+        o[0] = st.m;
+        o[1] = st.a;
+        o[2] = st.b;
+    }
+}
+
+template <bool CE>
+__device__ __forceinline__ Stat join_parts(const DistillArgs& a, int64_t row, float c, float* red)
+{
+    Stat s = {kLowest, 0.0f, 0.0f};
+    for (int i = threadIdx.x; i < a.splits; i += kDistillThreads) {
+        const float* o = a.parts + (row * a.splits + i) * kDistillPart;
+        join<CE>(s, Stat{o[0], o[1], o[2]}, c);
+    }
+    return block_join<CE>(s, c, red);
+}
+
+// One block per part of a row.  FROM_LSE: the gradient from saved
+// statistics.  Otherwise they come from the parts' statistics, the first
+// part's block writes the row's loss, and with GRAD every block its part of
+// the gradient.
+template <typename T, bool CE, bool GRAD, bool FROM_LSE>
+__global__ void __launch_bounds__(kDistillThreads)
+    k_distill_finish(DistillArgs a, int64_t b0)
+{
+    extern __shared__ __align__(16) char lds[];
+    __shared__ float red[kDistillWaves * 3];
+    const int64_t block = b0 + blockIdx.x, row = GRAD ? block / a.splits : block;
+    const int part = GRAD ? static_cast<int>(block - row * a.splits) : 0;
+    const float c = a.inv_tau * kLog2e;
+    const T* s = static_cast<const T*>(a.logits) + row * a.logits_pitch;
+    T* out = static_cast<T*>(a.grad) + row * a.grad_pitch;
+    const int64_t c0 = part * a.part_cols;
+    const int64_t c1 = c0 + a.part_cols < a.vocab ? c0 + a.part_cols : a.vocab;
+    const Entries e = load_targets(a, row, lds, red);
+    if (!e.counts) {
+        if (!FROM_LSE && part == 0) put_loss(a, row, false, 0.0f, Stat{});
+        if constexpr (GRAD) put_zeros(out, c0, c1);
+        return;
+    }
+    const float rg = GRAD && a.row_grad ? a.row_grad[row] : 1.0f;
+    Slope g;
+    if constexpr (FROM_LSE) {
+        // exp(s/tau - lse) = exp((s - m)/tau) * exp(m/tau - lse) with
+        // m = tau * lse rounded: the second factor takes up the rounding
+        const float lse = a.lse_in[2 * row], m = lse / a.inv_tau;
+        const double rest = static_cast<double>(m) * a.inv_tau - lse;
+        g.m_kd = m;
+        g.g_kd = rg * a.grad_kd * e.mass * (1.0f + static_cast<float>(rest));
+        g.m_ce = a.lse_in[2 * row + 1];
+        g.g_ce = rg * a.grad_ce;
+    } else {
+        const Stat st = join_parts<CE>(a, row, c, red);
+        if (part == 0) {
+            const float* picked = a.picked + row * (a.k + 1);
+            const float loss = row_loss(a, e, st, [&](int k) { return picked[k]; }, red);
+            put_loss(a, row, true, loss, st);
+        }
+        g = slope_of(a, e, st, rg);
+    }
+    if constexpr (GRAD) put_grad<T, CE>(a, e, g, rg, s, out, c0, c1, c);
+}
+
+constexpr int kTotalThreads = 1024;
+
+// The sum of the row losses in fp64, in a fixed order, and the count.
+__global__ void __launch_bounds__(kTotalThreads) k_distill_total(DistillArgs a)
+{
+    __shared__ double sums[kTotalThreads / kWave];
+    __shared__ int64_t counts[kTotalThreads / kWave];
+    double s = 0.0;
+    int64_t n = 0;
+    for (int64_t r = threadIdx.x; r < a.rows; r += kTotalThreads) {
+        s += a.loss[r];
+        n += a.counts[r];
+    }
+    for (int o = kWave / 2; o > 0; o >>= 1) {
+        s += __shfl_xor(s, o);
+        n += __shfl_xor(n, o);
+    }
+    if (threadIdx.x % kWave == 0) {
+        sums[threadIdx.x / kWave] = s;
+        counts[threadIdx.x / kWave] = n;
+    }
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int w = 1; w < kTotalThreads / kWave; ++w) {
+        s += sums[w];
+        n += counts[w];
+    }
+    if (a.loss_sum) *a.loss_sum = static_cast<float>(a.accumulate ? *a.loss_sum + s : s);
+    if (a.counted) *a.counted = a.accumulate ? *a.counted + n : n;
+}
+
+// ---- launch helpers -------------------------------------------------------------------
+
+int launched() { return hipGetLastError() == hipSuccess ? ZS_OK : ZS_ELAUNCH; }
+
+// blocks of `threads` threads of kernel(args..., first block), in as many
+// launches as they need.
+template <typename K, typename... Args>
+int launch(K kernel, int64_t blocks, int threads, size_t lds, hipStream_t st, Args... args)
+{
+    const int64_t cap = max_blocks(threads);
+    for (int64_t b0 = 0; b0 < blocks; b0 += cap) {
+        const int64_t nb = blocks - b0 < cap ? blocks - b0 : cap;
+        hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(nb)), dim3(threads), lds, st, args...,
+                           b0);
+        const int rc = launched();
+        if (rc != ZS_OK) return rc;
+    }
+    return ZS_OK;
+}
+
+template <typename TT, typename AT, int N>
+int lookup(const EmbedArgs& a, hipStream_t st)
+{
+    const int shift = lane_shift(a.dim, N, 8);
+    const int64_t per = kEmbedThreads >> shift;
+    return launch(k_embed_lookup<TT, AT, N>, (a.tokens + per - 1) / per, kEmbedThreads, 0, st, a,
+                  shift);
+}
+
+template <typename AT, typename GT, bool ADD>
+int embed_sums(const EmbedArgs& a, SumPlan p, hipStream_t st)
+{
+    constexpr int N = 16 / sizeof(AT);      // one 16-byte load of activations a lane
+    p.shift = lane_shift(a.dim, N, 6);
+    p.zero_shift = lane_shift(a.dim, N, 8);
+    const int64_t cols = static_cast<int64_t>(N) << p.shift;
+    p.splits = (a.dim + cols - 1) / cols;
+    const int64_t per = kEmbedThreads >> p.shift, zero_per = kEmbedThreads >> p.zero_shift;
+    p.sum_blocks = (p.chunks * p.splits + per - 1) / per;
+    const int64_t zero_blocks = ADD ? 0 : (a.rows + zero_per - 1) / zero_per;
+    int rc = launch(k_embed_sum<AT, GT, N, ADD>, p.sum_blocks + zero_blocks, kEmbedThreads, 0, st,
+                    a, p);
+    if (rc != ZS_OK || p.chunks <= 1) return rc;
+    return launch(k_embed_join<GT, N, ADD>, p.chunks * p.splits, kEmbedThreads, 0, st, a, p);
+}
+
+template <typename AT, typename GT>
+int embed_sums(const EmbedArgs& a, const SumPlan& p, bool add, hipStream_t st)
+{
+    return add ? embed_sums<AT, GT, true>(a, p, st) : embed_sums<AT, GT, false>(a, p, st);
+}
+
+template <typename T, bool CE>
+int distill_loss_t(const DistillArgs& a, bool grad, hipStream_t st)
+{
+    const size_t lds = entry_bytes(a.k);
+    if (a.splits == 1)
+        return grad ? launch(k_distill_row<T, CE, true>, a.rows, kDistillThreads, lds, st, a)
+                    : launch(k_distill_row<T, CE, false>, a.rows, kDistillThreads, lds, st, a);
+    const int64_t parts = a.rows * a.splits;
+    const int rc = launch(k_distill_parts<T, CE>, parts, kDistillThreads, 0, st, a);
+    if (rc != ZS_OK) return rc;
+    return grad ? launch(k_distill_finish<T, CE, true, false>, parts, kDistillThreads, lds, st, a)
+                : launch(k_distill_finish<T, CE, false, false>, a.rows, kDistillThreads, lds, st,
+                         a);
+}
+
+template <typename T, bool CE>
+int distill_grad_t(const DistillArgs& a, hipStream_t st)
+{
+    return launch(k_distill_finish<T, CE, true, true>, a.rows * a.splits, kDistillThreads,
+                  entry_bytes(a.k), st, a);
+}
+
+// Parts of whole vectors (of either element type).
+int64_t part_columns(int64_t vocab, int32_t splits)
+{
+    const int64_t cols = (vocab + splits - 1) / splits;
+    return (cols + 7) / 8 * 8;
+}
+
+}  // namespace
+
+int prepare_vocab()
+{
+    // one kernel's attributes load the code object that holds them all
+    hipFuncAttributes f;
+    return hipFuncGetAttributes(&f, reinterpret_cast<const void*>(k_distill_total)) == hipSuccess
+               ? ZS_OK
+               : ZS_ELAUNCH;
+}
+
+int enqueue_embed_lookup(const EmbedArgs& a, void* stream)
+{
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    (void)hipGetLastError();
+    if (a.table_f32)
+        return a.act_f32 ? lookup<float, float, 4>(a, st) : lookup<float, uint16_t, 4>(a, st);
+    return a.act_f32 ? lookup<uint16_t, float, 4>(a, st) : lookup<uint16_t, uint16_t, 8>(a, st);
+}
+
+int enqueue_embed_grad(const EmbedArgs& a, bool accumulate, void* workspace, void* stream)
+{
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    (void)hipGetLastError();
+    const EmbedSpace w = embed_space(a.tokens, a.rows, a.dim);
+    char* base = static_cast<char*>(workspace);
+    int32_t* order = reinterpret_cast<int32_t*>(base + w.order);
+    int32_t* row_of = reinterpret_cast<int32_t*>(base + w.row_of);
+    int32_t* starts = reinterpret_cast<int32_t*>(base + w.starts);
+    const SortShape s = sort_shape(a.rows);
+    hipLaunchKernelGGL(k_embed_sort, dim3(static_cast<uint32_t>(s.buckets)), dim3(kSortThreads), 0,
+                       st, a, s, order, row_of, starts);
+    const int rc = launched();
+    if (rc != ZS_OK) return rc;
+    SumPlan p{};
+    p.order = order;
+    p.row_of = row_of;
+    p.starts = starts;
+    p.partials = reinterpret_cast<float*>(base + w.partials);
+    p.chunk = embed_chunk(a.tokens);
+    p.chunks = embed_chunks(a.tokens);
+    if (a.act_f32)
+        return a.table_f32 ? embed_sums<float, float>(a, p, accumulate, st)
+                           : embed_sums<float, uint16_t>(a, p, accumulate, st);
+    return a.table_f32 ? embed_sums<uint16_t, float>(a, p, accumulate, st)
+                       : embed_sums<uint16_t, uint16_t>(a, p, accumulate, st);
+}
+
+int enqueue_distill_loss(DistillArgs a, bool with_grad, void* stream)
+{
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    (void)hipGetLastError();
+    a.splits = distill_splits(a.rows, a.vocab);
+    a.part_cols = part_columns(a.vocab, a.splits);
+    int rc = ZS_OK;
+    if (a.rows > 0) {
+        if (a.f32)
+            rc = a.ce ? distill_loss_t<float, true>(a, with_grad, st)
+                      : distill_loss_t<float, false>(a, with_grad, st);
+        else
+            rc = a.ce ? distill_loss_t<uint16_t, true>(a, with_grad, st)
+                      : distill_loss_t<uint16_t, false>(a, with_grad, st);
+    }
+    if (rc != ZS_OK || (!a.loss_sum && !a.counted)) return rc;
+    hipLaunchKernelGGL(k_distill_total, dim3(1), dim3(kTotalThreads), 0, st, a);
+    return launched();
+}
+
+int enqueue_distill_grad(DistillArgs a, void* stream)
+{
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    (void)hipGetLastError();
+    if (a.rows == 0) return ZS_OK;
+    a.splits = distill_splits(a.rows, a.vocab);
+    a.part_cols = part_columns(a.vocab, a.splits);
+    if (a.f32) return a.ce ? distill_grad_t<float, true>(a, st) : distill_grad_t<float, false>(a, st);
+    return a.ce ? distill_grad_t<uint16_t, true>(a, st) : distill_grad_t<uint16_t, false>(a, st);
+}
+
+}  // namespace zs

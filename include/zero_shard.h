@@ -52,6 +52,9 @@
  *  - Outputs must not overlap inputs, except master/exp_avg/exp_avg_sq which
  *    are updated in place.  Calls that write the same buffers must not run
  *    concurrently on different streams.
+ *
+ * The calls on the vocabulary table (embed_*, distill_*) state their own
+ * conventions where they differ.
  */
 #ifndef ZERO_SHARD_H
 #define ZERO_SHARD_H
@@ -91,6 +94,10 @@ extern "C" {
 #define ZS_EINVAL_UNITS  (-14)   /* units < 1 */
 #define ZS_ESCRATCH      (-15)   /* shard_grad_sqnorm_noalloc: the shard needs
                                     more than ZS_SCRATCH_BYTES of workspace */
+#define ZS_EINVAL_EMBED  (-16)   /* zs_embed: a size, pitch, type or scale out of
+                                    range, or reserved != 0 */
+#define ZS_EINVAL_DISTILL (-17)  /* zs_distill: a size, pitch, type, temperature,
+                                    alpha or scale out of range */
 
 #define ZS_MAX_RANKS 64          /* gradient slices one call can reduce */
 /* Bytes of the per-device static scratch array of shard_grad_sqnorm_noalloc:
@@ -329,6 +336,152 @@ int shard_pack_gather(const zs_shard* s, const float* master, uint16_t* param_ou
 int shard_grad_sqnorm_noalloc(const zs_shard* s, const uint16_t* const* grad_slices,
                               float* mean_out, double* sqnorm_out, int32_t accumulate,
                               void* stream);
+
+/* ---- the vocabulary table: lookup and gradient, distillation ----------------------
+ *
+ * The operators at the two ends of a training step, whose parameter is the
+ * (often tied) vocabulary table of a sharded unit: embed_lookup reads rows of
+ * the vector the all-gather filled, embed_grad writes the gradient whose
+ * slices shard_grad_reduce reads, and the distillation loss counts the valid
+ * tokens that zs_reduce.rank_tokens weighs the ranks by.  All conventions
+ * above hold, except: the table, its gradient, activations, logits and their
+ * gradient need only the alignment of their element (rows of odd length and
+ * tables inside a flat vector are allowed), and fp32 sums here may use fused
+ * multiply-add. */
+
+/* Element types of these calls, and the types of ids. */
+#define ZS_BF16   0
+#define ZS_F32    1
+#define ZS_ID_I32 0
+#define ZS_ID_I64 1
+
+/* Tokens and table rows one embed_grad call takes at most, and the teacher
+ * entries of a row. */
+#define ZS_EMBED_MAX       ((int64_t)1 << 24)
+#define ZS_DISTILL_MAX_K   1024
+
+/* A call on a batch of token ids and `rows` consecutive rows of an embedding
+ * table (the whole table, or the rows a rank holds).  A token is here when
+ * first_row <= id < first_row + rows; any other id (padding, another rank's
+ * rows) reads a row of zeros and has no gradient. */
+typedef struct zs_embed {
+    int64_t tokens;        /* T >= 0 ids, and rows of activations */
+    int64_t rows;          /* R >= 1 table rows in the buffer */
+    int64_t first_row;     /* id of the first of them, >= 0 */
+    int64_t dim;           /* D >= 1 */
+    int64_t table_pitch;   /* elements from one table row to the next, >= D */
+    int64_t act_pitch;     /* elements from one activation row to the next, >= D */
+    int32_t id_dtype;      /* ZS_ID_I32 or ZS_ID_I64 */
+    int32_t table_dtype;   /* ZS_BF16 or ZS_F32: the table, or its gradient */
+    int32_t act_dtype;     /* ZS_BF16 or ZS_F32: activations, or their gradient */
+    int32_t reserved;      /* must be 0 */
+    double scale;          /* rounded once to fp32; finite */
+} zs_embed;
+
+/* out[t, :] = scale * table[ids[t] - first_row, :], the product in fp32 and
+ * rounded once to act_dtype; +0 for a token that is not here.
+ *   ids    device, T ids.     table  device, R rows.     out  device, T rows.
+ * Columns between D and the pitch are not read or written.
+ * Errors: ZS_ENULL, ZS_EINVAL_EMBED, ZS_EALIGN, ZS_ELAUNCH. */
+int embed_lookup(const zs_embed* e, const void* ids, const void* table, void* out, void* stream);
+
+/* Bytes of device workspace embed_grad needs: the token positions sorted by
+ * row (8 bytes a token), the row starts (4 bytes a row) and the partial sums
+ * of rows with many tokens (at most 1/4 of an fp32 activation batch).  0 for
+ * a NULL or invalid e.  Host only. */
+size_t zs_embed_workspace_bytes(const zs_embed* e);
+
+/* The gradient of embed_lookup with respect to the table, dense:
+ *   G_r = scale * (sum of grad_out[t, :] over the tokens with row r)
+ *   accumulate == 0: grad_table[r, :] = G_r for every row r (+0 without tokens)
+ *   accumulate != 0: grad_table[r, :] += G_r for the rows that have tokens;
+ *                    other rows are not read or written
+ * (micro-batches after the first, or a tied table whose head's gradient is
+ * there already).  Tokens are sorted by row, stably, and summed in fp32 in an
+ * order that depends on the sizes and ids alone (run-to-run deterministic:
+ * no floating-point atomics); the result is rounded once to table_dtype.
+ *   workspace  device, 16-byte aligned, >= zs_embed_workspace_bytes(e) bytes;
+ *              contents on entry are ignored.
+ * Errors: ZS_ENULL, ZS_EINVAL_EMBED, ZS_EALIGN, ZS_EUNSUPPORTED (more than
+ * ZS_EMBED_MAX tokens or rows), ZS_EWORKSPACE, ZS_ELAUNCH. */
+int embed_grad(const zs_embed* e, const void* ids, const void* grad_out, void* grad_table,
+               int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Distillation of student logits (T rows over a vocabulary of V) from the top
+ * logits of a teacher, optionally mixed with the cross entropy of labels. */
+typedef struct zs_distill {
+    int64_t rows;          /* T >= 0 */
+    int64_t vocab;         /* 1 <= V < 2^31 */
+    int64_t logits_pitch;  /* elements from one row of logits to the next, >= V */
+    int64_t grad_pitch;    /* the same of the logits' gradient */
+    int32_t k;             /* teacher entries a row, 0..ZS_DISTILL_MAX_K */
+    int32_t logits_dtype;  /* ZS_BF16 or ZS_F32: logits and their gradient */
+    int32_t teacher_dtype; /* ZS_BF16 or ZS_F32: the teacher's logits */
+    int32_t id_dtype;      /* ZS_ID_I32 or ZS_ID_I64: teacher ids and labels */
+    double temperature;    /* tau > 0 */
+    double alpha;          /* weight of the distillation, 0..1; the labels' cross
+                              entropy has 1 - alpha */
+    double scale;          /* of the gradient (not of the loss), finite */
+} zs_distill;
+
+/* What the student is held to.  Device pointers, rows contiguous. */
+typedef struct zs_targets {
+    const void* teacher_ids;     /* [T, k] columns; an id outside [0, V) is no entry */
+    const void* teacher_logits;  /* [T, k] u, before the temperature; -Inf is no entry */
+    const float* teacher_lse;    /* [T] or NULL: log(sum exp(u / tau)) over the teacher's
+                                    whole vocabulary; NULL: the entries are all of it */
+    const void* labels;          /* [T] or NULL: columns; a label outside [0, V) (-100)
+                                    masks its row out of loss and gradient */
+} zs_targets;
+
+/* Bytes of device workspace distill_loss and distill_loss_grad need: a flag
+ * per row, and, where there are too few rows to fill the GPU, the partial
+ * statistics of the parts each row is cut into.  0 for a NULL or invalid d.
+ * Host only. */
+size_t zs_distill_workspace_bytes(const zs_distill* d);
+
+/* Row losses.  With s a row's logits, K its teacher entries, in fp32:
+ *   lse_tau = log(sum over v of exp(s_v / tau)),  log q_v = s_v / tau - lse_tau
+ *   log p_k = u_k / tau - (teacher_lse, or log(sum over K of exp(u / tau)))
+ *   KD = sum over K of p_k (log p_k - log q_{id_k});   CE = lse_1 - s_label
+ *   loss_out[t] = alpha tau^2 KD + (1 - alpha) CE
+ * A row counts when its label (where labels are given) is in [0, V) and, if
+ * alpha == 1, it has a teacher entry.  Any other row has loss 0, and its
+ * logits are not read.  An entry with p_k = 0 adds nothing; the same id twice
+ * is two entries.  alpha < 1 needs labels; alpha == 0 reads no teacher.  NaN
+ * and +Inf in a row that counts propagate; a logit of -Inf has probability 0.
+ *   loss_out   fp32[T].
+ *   lse_out    fp32[T, 2] or NULL (required by distill_loss): lse_tau and
+ *              lse_1 (0 if alpha == 1); both 0 for a row that does not count.
+ *   loss_sum   one fp32 or NULL: the sum of loss_out, taken in fp64 in a fixed
+ *              order and rounded once.   counted  one int64 or NULL: how many
+ *              rows count.  accumulate != 0 adds to what they hold.
+ *   workspace  16-byte aligned, >= zs_distill_workspace_bytes(d) bytes.
+ * Errors: ZS_ENULL, ZS_EINVAL_DISTILL, ZS_EALIGN, ZS_EWORKSPACE, ZS_ELAUNCH. */
+int distill_loss(const zs_distill* d, const void* logits, const zs_targets* t, float* loss_out,
+                 float* lse_out, float* loss_sum, int64_t* counted, int32_t accumulate,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gradient of the row losses, from the statistics distill_loss left:
+ *   grad_out[t, v] = scale * row_grad[t] * (alpha tau (M q_v - sum of p_k with id_k = v)
+ *                    + (1 - alpha) (exp(s_v - lse_1) - [v = label])),  M = sum of p_k
+ * (M is 1 without teacher_lse), rounded once to logits_dtype; +0 in rows that
+ * do not count.
+ *   row_grad  fp32[T] or NULL (1): the gradient each row's loss receives.
+ *   grad_out  T rows; may be the logits themselves (then of the same pitch).
+ * Errors: ZS_ENULL, ZS_EINVAL_DISTILL (also: in place with another pitch),
+ * ZS_EALIGN, ZS_ELAUNCH. */
+int distill_grad(const zs_distill* d, const void* logits, const zs_targets* t,
+                 const float* lse_in, const float* row_grad, void* grad_out, void* stream);
+
+/* Both in one call, reading the logits once where a row's part fits the
+ * registers: the loss is usually the last operator of the forward pass, so
+ * its gradient can be taken there.  Arguments and errors as above; lse_out
+ * may be NULL. */
+int distill_loss_grad(const zs_distill* d, const void* logits, const zs_targets* t,
+                      float* loss_out, float* lse_out, const float* row_grad, void* grad_out,
+                      float* loss_sum, int64_t* counted, int32_t accumulate, void* workspace,
+                      size_t workspace_bytes, void* stream);
 
 /* Per-device set-up for the current HIP device: queries its LDS size, raises
  * the kernels' dynamic-LDS limits and takes the address of the static

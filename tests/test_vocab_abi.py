@@ -1,0 +1,185 @@
+"""Host-side checks of the vocabulary-table calls (no GPU needed): every
+documented argument error is reported before anything is enqueued.  Fake
+device addresses are used, so these run only where no GPU is visible."""
+import ctypes as C
+
+import pytest
+import torch
+
+import fsdp_sharded_optimizer_zero_amd as Z
+
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(),
+                            reason="fake-address error paths run only without a GPU")
+FAKE = 0x7F0000000000
+
+
+def _embed(**kw):
+    e = Z.make_embed(10, 20, 8)
+    for k, v in kw.items():
+        setattr(e, k, v)
+    return e
+
+
+def _lookup(e, ids=FAKE, table=FAKE, out=FAKE):
+    return Z.lib().embed_lookup(None if e is None else C.byref(e), ids, table, out, None)
+
+
+def _grad(e, ids=FAKE, act=FAKE, table=FAKE, acc=0, ws=FAKE, nbytes=None):
+    if nbytes is None:
+        nbytes = Z.zs_embed_workspace_bytes(e)
+    return Z.lib().embed_grad(C.byref(e), ids, act, table, acc, ws, nbytes, None)
+
+
+BAD_EMBED = [dict(tokens=-1), dict(rows=0), dict(rows=-1), dict(first_row=-1), dict(dim=0),
+             dict(table_pitch=7), dict(act_pitch=7), dict(id_dtype=2), dict(table_dtype=-1),
+             dict(act_dtype=2), dict(reserved=1), dict(scale=float("nan")),
+             dict(scale=float("inf")), dict(scale=1e39), dict(tokens=1 << 62),
+             dict(rows=1 << 41), dict(first_row=(1 << 63) - 1), dict(table_pitch=1 << 60)]
+
+
+@no_gpu
+@pytest.mark.parametrize("bad", BAD_EMBED)
+def test_embed_struct_is_refused(bad):
+    e = _embed(**bad)
+    assert _lookup(e) == Z.ZS_EINVAL_EMBED
+    assert _grad(e, nbytes=1 << 60) == Z.ZS_EINVAL_EMBED
+    assert Z.zs_embed_workspace_bytes(e) == 0
+
+
+@no_gpu
+def test_embed_pointers_are_refused():
+    e = _embed()
+    assert _lookup(None) == Z.ZS_ENULL
+    for name in ("ids", "table", "out"):
+        assert _lookup(e, **{name: None}) == Z.ZS_ENULL
+        assert _lookup(e, **{name: FAKE + 1}) == Z.ZS_EALIGN
+    assert _lookup(e, ids=FAKE + 4) == Z.ZS_EALIGN            # int64 ids
+    assert _lookup(_embed(table_dtype=Z.ZS_F32), table=FAKE + 2) == Z.ZS_EALIGN
+    for name in ("ids", "act", "table", "ws"):
+        assert _grad(e, **{name: None}) == Z.ZS_ENULL
+        assert _grad(e, **{name: FAKE + 1}) == Z.ZS_EALIGN
+    assert _grad(e, ws=FAKE + 8) == Z.ZS_EALIGN
+    assert _grad(e, nbytes=Z.zs_embed_workspace_bytes(e) - 1) == Z.ZS_EWORKSPACE
+    assert _grad(_embed(tokens=Z.ZS_EMBED_MAX + 1), nbytes=1 << 60) == Z.ZS_EUNSUPPORTED
+    assert _grad(_embed(rows=Z.ZS_EMBED_MAX + 1), nbytes=1 << 60) == Z.ZS_EUNSUPPORTED
+    # nothing to do: no launch
+    none = _embed(tokens=0)
+    assert _lookup(none, ids=None, out=None) == Z.ZS_OK
+    assert _grad(none, ids=None, act=None, acc=1) == Z.ZS_OK
+    assert _grad(none, ids=None, act=None, table=None) == Z.ZS_ENULL
+
+
+def test_embed_workspace_covers_its_parts():
+    for tokens in (0, 1, 8, 9, 1000, 8192, 8193, 65536, 65537, 1 << 24):
+        for rows in (1, 255, 128256):
+            for dim in (1, 771, 4096):
+                n = Z.zs_embed_workspace_bytes(Z.make_embed(tokens, rows, dim))
+                chunk = 8
+                while chunk < 64 and tokens > 1024 * chunk:
+                    chunk *= 2
+                chunks = -(-tokens // chunk)
+                least = 8 * tokens + 4 * (rows + 1) + (8 * chunks * dim if chunks > 1 else 0)
+                assert least <= n <= least + 4 * 256
+                assert n <= 8 * tokens + 4 * rows + tokens * dim + 8 * dim + 2048
+
+
+def _distill(**kw):
+    d = Z.make_distill(6, 100, 4, alpha=0.5)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def _t(**kw):
+    t = Z.zs_targets(FAKE, FAKE, None, FAKE)
+    for k, v in kw.items():
+        setattr(t, k, v)
+    return t
+
+
+def _loss(d, logits=FAKE, t=None, loss=FAKE, lse=FAKE, total=None, count=None, ws=FAKE,
+          nbytes=None):
+    t = _t() if t is None else t
+    if nbytes is None:
+        nbytes = Z.zs_distill_workspace_bytes(d)
+    return Z.lib().distill_loss(C.byref(d), logits, C.byref(t), loss, lse, total, count, 0, ws,
+                                nbytes, None)
+
+
+def _dgrad(d, logits=FAKE, t=None, lse=FAKE, rg=None, grad=FAKE):
+    t = _t() if t is None else t
+    return Z.lib().distill_grad(C.byref(d), logits, C.byref(t), lse, rg, grad, None)
+
+
+def _both(d, logits=FAKE, t=None, loss=FAKE, lse=None, rg=None, grad=FAKE, total=None, count=None,
+          ws=FAKE, nbytes=None):
+    t = _t() if t is None else t
+    if nbytes is None:
+        nbytes = Z.zs_distill_workspace_bytes(d)
+    return Z.lib().distill_loss_grad(C.byref(d), logits, C.byref(t), loss, lse, rg, grad, total,
+                                     count, 0, ws, nbytes, None)
+
+
+BAD_DISTILL = [dict(rows=-1), dict(rows=1 << 31), dict(vocab=0), dict(vocab=1 << 31),
+               dict(logits_pitch=99), dict(grad_pitch=99), dict(k=-1),
+               dict(k=Z.ZS_DISTILL_MAX_K + 1), dict(logits_dtype=2), dict(teacher_dtype=-1),
+               dict(id_dtype=5), dict(temperature=0.0), dict(temperature=-1.0),
+               dict(temperature=float("nan")), dict(temperature=float("inf")),
+               dict(temperature=1e7), dict(alpha=-0.1), dict(alpha=1.1), dict(alpha=float("nan")),
+               dict(scale=float("inf")), dict(scale=1e39), dict(logits_pitch=1 << 60)]
+
+
+@no_gpu
+@pytest.mark.parametrize("bad", BAD_DISTILL)
+def test_distill_struct_is_refused(bad):
+    d = _distill(**bad)
+    assert _loss(d, nbytes=1 << 60) == Z.ZS_EINVAL_DISTILL
+    assert _dgrad(d) == Z.ZS_EINVAL_DISTILL
+    assert _both(d, nbytes=1 << 60) == Z.ZS_EINVAL_DISTILL
+    assert Z.zs_distill_workspace_bytes(d) == 0
+
+
+@no_gpu
+def test_distill_pointers_are_refused():
+    d = _distill()
+    for call in (_loss, _dgrad, _both):
+        assert call(d, logits=None) == Z.ZS_ENULL
+        assert call(d, logits=FAKE + 1) == Z.ZS_EALIGN
+        for name in ("teacher_ids", "teacher_logits", "labels"):
+            assert call(d, t=_t(**{name: None})) == Z.ZS_ENULL
+            assert call(d, t=_t(**{name: FAKE + 1})) == Z.ZS_EALIGN
+        assert call(d, t=_t(teacher_lse=FAKE + 2)) == Z.ZS_EALIGN
+    assert Z.lib().distill_loss(C.byref(d), FAKE, None, FAKE, FAKE, None, None, 0, FAKE, 1 << 20,
+                                None) == Z.ZS_ENULL
+    assert Z.lib().distill_grad(None, FAKE, C.byref(_t()), FAKE, None, FAKE, None) == Z.ZS_ENULL
+    for call in (_loss, _both):
+        assert call(d, loss=None) == Z.ZS_ENULL
+        assert call(d, ws=None) == Z.ZS_ENULL
+        assert call(d, ws=FAKE + 8) == Z.ZS_EALIGN
+        assert call(d, loss=FAKE + 2) == Z.ZS_EALIGN
+        assert call(d, lse=FAKE + 2) == Z.ZS_EALIGN
+        assert call(d, total=FAKE + 2) == Z.ZS_EALIGN
+        assert call(d, count=FAKE + 4) == Z.ZS_EALIGN
+        assert call(d, nbytes=Z.zs_distill_workspace_bytes(d) - 1) == Z.ZS_EWORKSPACE
+    assert _loss(d, lse=None) == Z.ZS_ENULL
+    for call in (_dgrad, _both):
+        assert call(d, grad=None) == Z.ZS_ENULL
+        assert call(d, grad=FAKE + 1) == Z.ZS_EALIGN
+        assert call(d, rg=FAKE + 2) == Z.ZS_EALIGN
+        # in place needs the same pitch
+        assert call(_distill(grad_pitch=104)) == Z.ZS_EINVAL_DISTILL
+    assert _dgrad(d, lse=None) == Z.ZS_ENULL
+    # no teacher is needed at alpha = 0, no labels at alpha = 1, nothing for no rows
+    none = Z.zs_targets(None, None, None, None)
+    assert _dgrad(_distill(rows=0), logits=None, t=none, lse=None, grad=None) == Z.ZS_OK
+    assert _dgrad(_distill(alpha=0.0), t=_t(teacher_ids=None, labels=None)) == Z.ZS_ENULL
+    assert _dgrad(_distill(alpha=1.0), t=_t(labels=None), lse=None) == Z.ZS_ENULL
+
+
+def test_distill_workspace_grows_with_rows_until_they_fill_the_gpu():
+    for rows in (0, 1, 2, 100, 511, 512, 8192):
+        for vocab in (1, 4096, 4097, 128256):
+            n = Z.zs_distill_workspace_bytes(Z.make_distill(rows, vocab, 64))
+            assert n >= max(256, 4 * rows) and n % 256 == 0
+            if rows >= 512:
+                assert n <= 4 * rows + 512
