@@ -15,6 +15,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "zs_internal.h"
 
@@ -39,16 +40,13 @@ typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(2)));
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 
-// fp32 -> bf16, round to nearest even, any NaN to 0x7FC0 (as the pack does).
-__device__ __forceinline__ uint32_t bf16_rne(float f)
-{
-    const uint32_t u = __float_as_uint(f);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0x7FC0u;
-    return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-}
+// fp32 -> bf16 by the hardware's conversion: round to nearest even,
+// subnormals kept, NaN stays NaN.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
 {
-    return bf16_rne(lo) | (bf16_rne(hi) << 16);
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), b16x2));
 }
 
 __device__ __forceinline__ float widen(uint16_t x)
@@ -56,7 +54,7 @@ __device__ __forceinline__ float widen(uint16_t x)
     return __uint_as_float(static_cast<uint32_t>(x) << 16);
 }
 __device__ __forceinline__ float widen(float x) { return x; }
-__device__ __forceinline__ void put(uint16_t* p, float v) { *p = static_cast<uint16_t>(bf16_rne(v)); }
+__device__ __forceinline__ void put(uint16_t* p, float v) { *p = static_cast<uint16_t>(pack_bf16x2(v, 0.0f)); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 
 // N consecutive elements from any element address.
@@ -463,140 +461,196 @@ __global__ void __launch_bounds__(kEmbedThreads)
 }
 
 // ---- distillation -------------------------------------------------------------------
+//
+// One row is one softmax (two with labels at another temperature) over the
+// vocabulary plus K entries to look at.  The logits are what costs: HBM moves
+// them, and each takes about ten vector instructions and an exponential (four
+// issue slots) in each of the two passes, so the arithmetic is kept near half
+// of the time the bytes take:
+//  - exponentials are the hardware's base-2 one (1 ulp), arguments
+//    (s - m) * log2(e)/tau with the difference taken first, so that an error
+//    grows with the distance from the maximum, where the value is small;
+//  - the teacher's entries are one wave's work, beside the others' loads.
 
-constexpr int kDistillThreads = 512;
-constexpr int kDistillWaves = kDistillThreads / kWave;
+constexpr int kWaves(int threads) { return threads / kWave; }
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Running statistics of a softmax: the maximum so far and the sums of
-// exp((s - m)/tau) and (CE) exp(s - m).  The maximum starts at the lowest
-// finite value, so that -Inf logits have weight 0 and no Inf - Inf occurs.
+__device__ __forceinline__ float wave_sum(float x)
+{
+    for (int o = kWave / 2; o > 0; o >>= 1) x += __shfl_xor(x, o);
+    return x;
+}
+__device__ __forceinline__ float wave_max(float x)
+{
+    for (int o = kWave / 2; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o));
+    return x;
+}
+
+// Statistics of a softmax: the maximum and the sums of exp((s - m)/tau) and
+// (CE) exp(s - m).  The maximum starts at the lowest finite value, so that
+// -Inf logits have weight 0 and no Inf - Inf occurs.
 struct Stat {
     float m, a, b;
 };
 
-template <bool CE>
+// At tau = 1 both sums are one: SAME takes the exponentials once.
+enum Terms { kKd = 0, kKdCe = 1, kSame = 2 };
+
+template <Terms TM>
 __device__ __forceinline__ void rescale(Stat& s, float m, float c)
 {
     s.a *= exp2_hw((s.m - m) * c);
-    if constexpr (CE) s.b *= exp2_hw((s.m - m) * kLog2e);
+    if constexpr (TM == kKdCe) s.b *= exp2_hw((s.m - m) * kLog2e);
     s.m = m;
 }
 
-template <bool CE>
+template <Terms TM>
 __device__ __forceinline__ void join(Stat& s, Stat o, float c)
 {
     const float m = fmaxf(s.m, o.m);
-    rescale<CE>(s, m, c);
-    rescale<CE>(o, m, c);
+    rescale<TM>(s, m, c);
+    rescale<TM>(o, m, c);
     s.a += o.a;
-    if constexpr (CE) s.b += o.b;
+    if constexpr (TM == kKdCe) s.b += o.b;
 }
 
-template <bool CE>
-__device__ __forceinline__ Stat wave_join(Stat s, float c)
+// Over groups of `lanes` lanes (a power of two); all lanes get the result.
+template <Terms TM>
+__device__ __forceinline__ Stat lanes_join(Stat s, float c, int lanes)
 {
-    for (int o = kWave / 2; o > 0; o >>= 1) {
+    for (int o = lanes / 2; o > 0; o >>= 1) {
         Stat t;
         t.m = __shfl_xor(s.m, o);
         t.a = __shfl_xor(s.a, o);
-        t.b = CE ? __shfl_xor(s.b, o) : 0.0f;
-        join<CE>(s, t, c);
+        t.b = TM == kKdCe ? __shfl_xor(s.b, o) : 0.0f;
+        join<TM>(s, t, c);
     }
     return s;
 }
 
-template <bool CE>
-__device__ __forceinline__ Stat block_join(Stat s, float c, float* lds)
+// Over the block, with its one barrier.
+template <Terms TM, int THREADS>
+__device__ __forceinline__ Stat block_join(Stat s, float c, float* red)
 {
-    const int wave = threadIdx.x / kWave;
-    s = wave_join<CE>(s, c);
-    __syncthreads();
-    if (threadIdx.x % kWave == 0) {
-        lds[wave * 3] = s.m;
-        lds[wave * 3 + 1] = s.a;
-        lds[wave * 3 + 2] = s.b;
+    s = lanes_join<TM>(s, c, kWave);
+    const int lane = threadIdx.x % kWave;
+    if (lane == 0) {
+        float* r = red + threadIdx.x / kWave * 3;
+        r[0] = s.m;
+        r[1] = s.a;
+        r[2] = s.b;
     }
     __syncthreads();
-    Stat r = {lds[0], lds[1], lds[2]};
-    for (int w = 1; w < kDistillWaves; ++w)
-        join<CE>(r, Stat{lds[w * 3], lds[w * 3 + 1], lds[w * 3 + 2]}, c);
-    return r;
+    const float* r = red + lane % kWaves(THREADS) * 3;
+    s = lanes_join<TM>(Stat{r[0], r[1], r[2]}, c, kWaves(THREADS));
+    if constexpr (TM == kSame) s.b = s.a;
+    return s;
 }
 
-__device__ __forceinline__ float block_sum(float x, float* lds)
-{
-    for (int o = kWave / 2; o > 0; o >>= 1) x += __shfl_xor(x, o);
-    __syncthreads();
-    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = x;
-    __syncthreads();
-    float r = lds[0];
-    for (int w = 1; w < kDistillWaves; ++w) r += lds[w];
-    return r;
-}
-
-__device__ __forceinline__ float block_max(float x, float* lds)
-{
-    for (int o = kWave / 2; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o));
-    __syncthreads();
-    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = x;
-    __syncthreads();
-    float r = lds[0];
-    for (int w = 1; w < kDistillWaves; ++w) r = fmaxf(r, lds[w]);
-    return r;
-}
-
-// Elements of one 16-byte vector of logits.
+// A 16-byte vector of logits, and its elements.
 template <typename T>
-constexpr int kVec = 16 / sizeof(T);
-
-// The statistics of columns [c0, c1) of a row, over the block's threads.
-template <typename T, bool CE>
-__device__ __forceinline__ Stat scan(const T* row, int64_t c0, int64_t c1, float c)
-{
-    constexpr int N = kVec<T>;
-    Stat s = {kLowest, 0.0f, 0.0f};
-    const int64_t nv = (c1 - c0) / N;
-    for (int64_t v = threadIdx.x; v < nv; v += kDistillThreads) {
-        float x[N];
-        load_n<N>(row + c0 + v * N, x);
-        float m = x[0];
-#pragma unroll
-        for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
-        if (m > s.m) rescale<CE>(s, m, c);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            s.a += exp2_hw((x[i] - s.m) * c);
-            if constexpr (CE) s.b += exp2_hw((x[i] - s.m) * kLog2e);
-        }
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+    static constexpr int N = 8;
+    using V = u32x4_u;
+    static __device__ __forceinline__ V lowest() { return V{kNegInf2, kNegInf2, kNegInf2, kNegInf2}; }
+    static __device__ __forceinline__ void widen(const V& b, float v[8])
+    {
+        v[0] = bf16_lo(b.x); v[1] = bf16_hi(b.x);
+        v[2] = bf16_lo(b.y); v[3] = bf16_hi(b.y);
+        v[4] = bf16_lo(b.z); v[5] = bf16_hi(b.z);
+        v[6] = bf16_lo(b.w); v[7] = bf16_hi(b.w);
     }
-    const int64_t e = c0 + nv * N + threadIdx.x;
+    static constexpr uint32_t kNegInf2 = 0xFF80FF80u;
+};
+template <>
+struct Raw<float> {
+    static constexpr int N = 4;
+    using V = f32x4_u;
+    static __device__ __forceinline__ V lowest()
+    {
+        return V{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    }
+    static __device__ __forceinline__ void widen(const V& b, float v[4])
+    {
+        v[0] = b.x; v[1] = b.y; v[2] = b.z; v[3] = b.w;
+    }
+};
+
+template <int N>
+__device__ __forceinline__ float max_n(const float x[N], float m)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = fmaxf(m, x[i]);
+    return m;
+}
+
+// exp((x - m)/tau) of N elements, added in pairs to s.
+template <Terms TM, int N>
+__device__ __forceinline__ void add_exp(Stat& s, const float x[N], float c)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float d = x[i] - s.m;
+        s.a += exp2_hw(d * c);
+        if constexpr (TM == kKdCe) s.b += exp2_hw(d * kLog2e);
+    }
+}
+
+// The statistics of columns [c0, c1) of a row, over the block's threads, in
+// one pass with the running maximum.
+template <typename T, Terms TM, int THREADS>
+__device__ __forceinline__ Stat scan(Stat s, const T* row, int64_t c0, int64_t c1, float c)
+{
+    constexpr int N = Raw<T>::N;
+    const int nv = static_cast<int>((c1 - c0) / N);
+    const typename Raw<T>::V* p = reinterpret_cast<const typename Raw<T>::V*>(row + c0);
+#pragma unroll 4
+    for (int v = threadIdx.x; v < nv; v += THREADS) {
+        float x[N];
+        Raw<T>::widen(p[v], x);
+        const float m = max_n<N>(x, s.m);
+        if (m > s.m) rescale<TM>(s, m, c);
+        add_exp<TM, N>(s, x, c);
+    }
+    const int64_t e = c0 + static_cast<int64_t>(nv) * N + threadIdx.x;
     if (e < c1) {
         const float x = widen(row[e]);
-        if (x > s.m) rescale<CE>(s, x, c);
-        s.a += exp2_hw((x - s.m) * c);
-        if constexpr (CE) s.b += exp2_hw((x - s.m) * kLog2e);
+        if (x > s.m) rescale<TM>(s, x, c);
+        add_exp<TM, 1>(s, &x, c);
     }
     return s;
 }
 
-// A row's targets in LDS: entry k's column (-1: no entry), its log p and p
-// (the label, with CE, is entry K), and the logit at each.
+// A row's targets in LDS: entry k's column (-1: no entry), its log p and p,
+// and the logit at it; with labels at alpha < 1 the label is entry K.
 struct Entries {
     int32_t* col;
     float* logp;
     float* p;
     float* s;
+    float* mass;    // sum of p
     int n;          // K, or K + 1 with the label
-    int label;
-    float mass;     // sum of p
-    bool counts;
 };
 
-// Entries a row can hold, a multiple of 4 (col is searched four at a time).
+// Entries a row can hold, a multiple of 4.
 __host__ __device__ constexpr int entry_slots(int k) { return (k + 1 + 3) / 4 * 4; }
-size_t entry_bytes(int k) { return static_cast<size_t>(entry_slots(k)) * 16; }
+size_t entry_bytes(int k) { return static_cast<size_t>(entry_slots(k)) * 16 + 16; }
+
+__device__ __forceinline__ Entries entries_at(char* lds, const DistillArgs& a)
+{
+    const int slots = entry_slots(a.k);
+    Entries e;
+    e.col = reinterpret_cast<int32_t*>(lds);
+    e.logp = reinterpret_cast<float*>(lds + slots * 4);
+    e.p = e.logp + slots;
+    e.s = e.p + slots;
+    e.mass = e.s + slots;
+    e.n = a.k + a.ce;
+    return e;
+}
 
 __device__ __forceinline__ int read_column(const void* ids, int id64, int64_t i, int64_t vocab)
 {
@@ -604,7 +658,17 @@ __device__ __forceinline__ int read_column(const void* ids, int id64, int64_t i,
     return id >= 0 && id < vocab ? static_cast<int>(id) : -1;
 }
 
-// Whether the row counts, and its label (-1: none).
+// Entry `at` of the teacher: its column and value.
+__device__ __forceinline__ int read_entry(const DistillArgs& a, int64_t at, float* u)
+{
+    *u = a.teacher_f32 ? static_cast<const float*>(a.teacher_logits)[at]
+                       : widen(static_cast<const uint16_t*>(a.teacher_logits)[at]);
+    const int col = read_column(a.teacher_ids, a.id64, at, a.vocab);
+    return *u == -INFINITY ? -1 : col;
+}
+
+// Whether the row counts, and its label (-1: none).  Every wave finds out by
+// itself: no barrier, and the loads hit the cache after the first wave's.
 __device__ __forceinline__ bool row_counts(const DistillArgs& a, int64_t row, int* label)
 {
     *label = -1;
@@ -613,223 +677,276 @@ __device__ __forceinline__ bool row_counts(const DistillArgs& a, int64_t row, in
         if (*label < 0) return false;
     }
     if (a.ce) return true;
-    int any = 0;
-    for (int k = threadIdx.x; k < a.k; k += kDistillThreads) {
-        const int64_t at = row * a.k + k;
-        const float u = a.teacher_f32 ? static_cast<const float*>(a.teacher_logits)[at]
-                                      : widen(static_cast<const uint16_t*>(a.teacher_logits)[at]);
-        any |= read_column(a.teacher_ids, a.id64, at, a.vocab) >= 0 && !(u == -INFINITY);
+    for (int k = threadIdx.x % kWave; k - static_cast<int>(threadIdx.x % kWave) < a.k; k += kWave) {
+        float u;
+        if (__ballot(k < a.k && read_entry(a, row * a.k + k, &u) >= 0)) return true;
     }
-    return __syncthreads_or(any) != 0;
+    return false;
 }
 
-__device__ __forceinline__ Entries load_targets(const DistillArgs& a, int64_t row, char* lds,
-                                                float* red)
+// One wave's work: the row's entries into LDS, and with PICK the logits at
+// those in columns [c0, c1).  The block's next barrier publishes them.
+template <typename T, bool PICK>
+__device__ __forceinline__ void load_entries(const DistillArgs& a, const Entries& e, int64_t row,
+                                             int label, const T* s, int64_t c0, int64_t c1)
 {
-    const int slots = entry_slots(a.k);
-    Entries e;
-    e.col = reinterpret_cast<int32_t*>(lds);
-    e.logp = reinterpret_cast<float*>(lds + slots * 4);
-    e.p = e.logp + slots;
-    e.s = e.p + slots;
-    e.n = a.k + a.ce;
-    e.counts = row_counts(a, row, &e.label);
-    e.mass = 0.0f;
-    if (!e.counts) return e;
+    const int lane = threadIdx.x % kWave;
     float top = kLowest;
-    for (int k = threadIdx.x; k < slots; k += kDistillThreads) {
+    for (int k = lane; k < entry_slots(a.k); k += kWave) {
         int col = -1;
         float u = 0.0f;
         if (k < a.k) {
-            const int64_t at = row * a.k + k;
-            col = read_column(a.teacher_ids, a.id64, at, a.vocab);
-            u = a.teacher_f32 ? static_cast<const float*>(a.teacher_logits)[at]
-                              : widen(static_cast<const uint16_t*>(a.teacher_logits)[at]);
-            if (u == -INFINITY) col = -1;
+            col = read_entry(a, row * a.k + k, &u);
             u *= a.inv_tau;
             if (col >= 0) top = fmaxf(top, u);
         } else if (k == a.k && a.ce) {
-            col = e.label;
+            col = label;
         }
         e.col[k] = col;
         e.logp[k] = u;
-    }
-    if (a.k == 0) {
-        __syncthreads();
-        return e;
-    }
-    float norm;
-    if (a.teacher_lse) {
-        norm = a.teacher_lse[row];
-    } else {
-        top = block_max(top, red);
-        float sum = 0.0f;
-        for (int k = threadIdx.x; k < a.k; k += kDistillThreads)
-            if (e.col[k] >= 0) sum += expf(e.logp[k] - top);
-        norm = top + logf(block_sum(sum, red));
+        if (PICK && col >= c0 && col < c1) e.s[k] = widen(s[col]);
     }
     float mass = 0.0f;
-    for (int k = threadIdx.x; k < a.k; k += kDistillThreads) {
-        const float logp = e.logp[k] - norm;
-        const float p = e.col[k] >= 0 ? expf(logp) : 0.0f;
-        e.logp[k] = logp;
-        e.p[k] = p;
-        mass += p;
+    if (a.k > 0) {
+        float norm;
+        if (a.teacher_lse) {
+            norm = a.teacher_lse[row];
+        } else {
+            top = wave_max(top);
+            float sum = 0.0f;
+            for (int k = lane; k < a.k; k += kWave)
+                if (e.col[k] >= 0) sum += expf(e.logp[k] - top);
+            norm = top + logf(wave_sum(sum));
+        }
+        for (int k = lane; k < a.k; k += kWave) {
+            const float logp = e.logp[k] - norm;
+            const float p = e.col[k] >= 0 ? expf(logp) : 0.0f;
+            e.logp[k] = logp;
+            e.p[k] = p;
+            mass += p;
+        }
+        mass = wave_sum(mass);
     }
-    e.mass = block_sum(mass, red);
-    return e;
+    if (lane == 0) *e.mass = mass;
 }
 
-// The row's loss from its statistics (all threads get it).
-template <typename LogitAt>
-__device__ __forceinline__ float row_loss(const DistillArgs& a, const Entries& e, const Stat& st,
-                                          LogitAt logit, float* red)
+// Loss, statistics and flag of a row that counts, by one wave.
+__device__ __forceinline__ void put_loss(const DistillArgs& a, const Entries& e, int64_t row,
+                                         const Stat& st, const float* logit)
 {
-    float kd = 0.0f;
+    const int lane = threadIdx.x % kWave;
     const float log_a = logf(st.a);
-    for (int k = threadIdx.x; k < a.k; k += kDistillThreads)
-        if (e.col[k] >= 0 && e.p[k] != 0.0f)
-            kd += e.p[k] * (e.logp[k] - ((logit(k) - st.m) * a.inv_tau - log_a));
-    float loss = a.kd ? a.loss_kd * block_sum(kd, red) : 0.0f;
-    if (a.ce) loss += a.loss_ce * (logf(st.b) - (logit(a.k) - st.m));
-    return loss;
+    float loss = 0.0f;
+    if (a.kd) {
+        for (int k = lane; k < a.k; k += kWave)
+            if (e.col[k] >= 0 && e.p[k] != 0.0f)
+                loss += e.p[k] * (e.logp[k] - ((logit[k] - st.m) * a.inv_tau - log_a));
+        loss = a.loss_kd * wave_sum(loss);
+    }
+    const float log_b = a.ce ? logf(st.b) : 0.0f;
+    if (a.ce) loss += a.loss_ce * (log_b - (logit[a.k] - st.m));
+    if (lane != 0) return;
+    a.loss[row] = loss;
+    a.counts[row] = 1;
+    if (a.lse_out) {
+        a.lse_out[2 * row] = st.m * a.inv_tau + log_a;
+        a.lse_out[2 * row + 1] = a.ce ? st.m + log_b : 0.0f;
+    }
 }
 
-// A softmax as the gradient needs it: value * exp2((s - m) * c).
+// A row that does not count.
+__device__ __forceinline__ void put_no_loss(const DistillArgs& a, int64_t row)
+{
+    if (threadIdx.x != 0) return;
+    a.loss[row] = 0.0f;
+    a.counts[row] = 0;
+    if (a.lse_out) a.lse_out[2 * row] = a.lse_out[2 * row + 1] = 0.0f;
+}
+
+// A softmax's share of the gradient: g * exp2((s - m) * c), for both.
 struct Slope {
     float m_kd, g_kd, m_ce, g_ce;
 };
 
-template <bool CE>
+template <Terms TM>
 __device__ __forceinline__ float slope_at(const Slope& g, float x, float c)
 {
     float v = g.g_kd * exp2_hw((x - g.m_kd) * c);
-    if constexpr (CE) v += g.g_ce * exp2_hw((x - g.m_ce) * kLog2e);
+    if constexpr (TM == kKdCe) v += g.g_ce * exp2_hw((x - g.m_ce) * kLog2e);
     return v;
 }
 
-// The gradient of columns [c0, c1) of a row.  The entries' columns are
-// written a second time, after a barrier, with their share taken off before
-// the one rounding: the first entry of a column adds up all of that column's.
-template <typename T, bool CE>
-__device__ __forceinline__ void put_grad(const DistillArgs& a, const Entries& e, const Slope& g,
-                                         float row_grad, const T* row, T* out, int64_t c0,
-                                         int64_t c1, float c)
+__device__ __forceinline__ Slope slope_of(const DistillArgs& a, float mass, const Stat& st,
+                                          float row_grad, bool same)
 {
-    constexpr int N = kVec<T>;
-    // the logits at the entries, before they may be overwritten
-    for (int k = threadIdx.x; k < e.n; k += kDistillThreads) {
-        const int col = e.col[k];
-        if (col >= c0 && col < c1) e.s[k] = widen(row[col]);
-    }
-    __syncthreads();
-    const int64_t nv = (c1 - c0) / N;
-    for (int64_t v = threadIdx.x; v < nv; v += kDistillThreads) {
-        float x[N];
-        load_n<N>(row + c0 + v * N, x);
+    Slope g = {st.m, row_grad * a.grad_kd * mass / st.a, st.m,
+               a.ce ? row_grad * a.grad_ce / st.b : 0.0f};
+    if (same) g.g_kd += g.g_ce;
+    return g;
+}
+
+template <typename T, Terms TM>
+__device__ __forceinline__ void put_slopes(T* out, const typename Raw<T>::V& raw, const Slope& g,
+                                           float c)
+{
+    constexpr int N = Raw<T>::N;
+    float x[N];
+    Raw<T>::widen(raw, x);
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = slope_at<CE>(g, x[i], c);
-        store_n<N>(out + c0 + v * N, x);
-    }
-    const int64_t at = c0 + nv * N + threadIdx.x;
-    if (at < c1) put(out + at, slope_at<CE>(g, widen(row[at]), c));
-    __syncthreads();
-    for (int k = threadIdx.x; k < e.n; k += kDistillThreads) {
+    for (int i = 0; i < N; ++i) x[i] = slope_at<TM>(g, x[i], c);
+    store_n<N>(out, x);
+}
+
+// The gradient of vectors [v0, nv) of the columns [c0, c1), and of the
+// elements behind the last vector.
+template <typename T, Terms TM, int THREADS>
+__device__ __forceinline__ void put_columns(const Slope& g, const T* row, T* out, int64_t c0,
+                                            int64_t c1, int v0, float c)
+{
+    constexpr int N = Raw<T>::N;
+    const int nv = static_cast<int>((c1 - c0) / N);
+    const typename Raw<T>::V* p = reinterpret_cast<const typename Raw<T>::V*>(row + c0);
+#pragma unroll 4
+    for (int v = v0 + threadIdx.x; v < nv; v += THREADS)
+        put_slopes<T, TM>(out + c0 + static_cast<int64_t>(v) * N, p[v], g, c);
+    const int64_t e = c0 + static_cast<int64_t>(nv) * N + threadIdx.x;
+    if (e < c1) put(out + e, slope_at<TM>(g, widen(row[e]), c));
+}
+
+// After a barrier behind the columns: the entries' columns once more, with
+// their share taken off before the one rounding.  The first entry of a column
+// takes off all of that column's, in their order.
+template <typename T, Terms TM, int THREADS>
+__device__ __forceinline__ void put_entries(const DistillArgs& a, const Entries& e, const Slope& g,
+                                            float row_grad, T* out, int64_t c0, int64_t c1, float c)
+{
+    for (int k = threadIdx.x; k < e.n; k += THREADS) {
         const int col = e.col[k];
         if (col < c0 || col >= c1) continue;
-        bool first = true;
-        for (int j = 0; j < k; ++j) first = first && e.col[j] != col;
-        if (!first) continue;
         float take = 0.0f;
-        for (int j = k; j < e.n; ++j)
-            if (e.col[j] == col)
-                take += row_grad * (j < a.k ? a.grad_kd * e.p[j] : a.grad_ce);
-        put(out + col, slope_at<CE>(g, e.s[k], c) - take);
+        bool first = true;
+        for (int j = 0; j < e.n; j += 4) {
+            const int4 other = *reinterpret_cast<const int4*>(e.col + j);
+            const int o[4] = {other.x, other.y, other.z, other.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (o[i] != col) continue;
+                if (j + i < k) first = false;
+                take += row_grad * (j + i < a.k ? a.grad_kd * e.p[j + i] : a.grad_ce);
+            }
+        }
+        if (first) put(out + col, slope_at<TM>(g, e.s[k], c) - take);
     }
 }
 
-template <typename T>
+template <typename T, int THREADS>
 __device__ __forceinline__ void put_zeros(T* out, int64_t c0, int64_t c1)
 {
-    constexpr int N = kVec<T>;
+    constexpr int N = Raw<T>::N;
     const float z[N] = {};
-    const int64_t nv = (c1 - c0) / N;
-    for (int64_t v = threadIdx.x; v < nv; v += kDistillThreads) store_n<N>(out + c0 + v * N, z);
-    const int64_t e = c0 + nv * N + threadIdx.x;
+    const int nv = static_cast<int>((c1 - c0) / N);
+    for (int v = threadIdx.x; v < nv; v += THREADS)
+        store_n<N>(out + c0 + static_cast<int64_t>(v) * N, z);
+    const int64_t e = c0 + static_cast<int64_t>(nv) * N + threadIdx.x;
     if (e < c1) put(out + e, 0.0f);
 }
 
-// Loss, statistics and flag of a row, by one thread.
-__device__ __forceinline__ void put_loss(const DistillArgs& a, int64_t row, bool counts,
-                                         float loss, const Stat& st)
-{
-    if (threadIdx.x != 0) return;
-    a.loss[row] = counts ? loss : 0.0f;
-    a.counts[row] = counts;
-    if (a.lse_out) {
-        a.lse_out[2 * row] = counts ? st.m * a.inv_tau + logf(st.a) : 0.0f;
-        a.lse_out[2 * row + 1] = counts && a.ce ? st.m + logf(st.b) : 0.0f;
-    }
-}
+// Vectors of a row each thread keeps in registers between the two passes:
+// 64 registers, which with the rest stays under the 128 that 16 waves on a CU
+// have each.  A block of 1024 threads so keeps 131072 bf16 (65536 fp32)
+// logits; what a longer row has beyond that is read again.
+constexpr int kHold = 16;
 
-__device__ __forceinline__ Slope slope_of(const DistillArgs& a, const Entries& e, const Stat& st,
-                                          float row_grad)
-{
-    return Slope{st.m, row_grad * a.grad_kd * e.mass / st.a, st.m,
-                 a.ce ? row_grad * a.grad_ce / st.b : 0.0f};
-}
-
-// One block per row: loss, and with GRAD the gradient.
-template <typename T, bool CE, bool GRAD>
-__global__ void __launch_bounds__(kDistillThreads)
-    k_distill_row(DistillArgs a, int64_t b0)
+// One block per row: the loss, and with GRAD the gradient, the row read once.
+template <typename T, Terms TM, bool GRAD, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_distill_row(DistillArgs a, int64_t b0)
 {
     extern __shared__ __align__(16) char lds[];
-    __shared__ float red[kDistillWaves * 3];
+    __shared__ float red[kWaves(THREADS) * 3];
+    constexpr int N = Raw<T>::N;
     const int64_t row = b0 + blockIdx.x;
     const float c = a.inv_tau * kLog2e;
     const T* s = static_cast<const T*>(a.logits) + row * a.logits_pitch;
     T* out = static_cast<T*>(a.grad) + row * a.grad_pitch;
-    const Entries e = load_targets(a, row, lds, red);
-    if (!e.counts) {
-        put_loss(a, row, false, 0.0f, Stat{});
-        if constexpr (GRAD) put_zeros(out, 0, a.vocab);
+    int label;
+    if (!row_counts(a, row, &label)) {
+        put_no_loss(a, row);
+        if constexpr (GRAD) put_zeros<T, THREADS>(out, 0, a.vocab);
         return;
     }
-    const Stat st = block_join<CE>(scan<T, CE>(s, 0, a.vocab, c), c, red);
-    const float loss =
-        row_loss(a, e, st, [&](int k) { return widen(s[e.col[k]]); }, red);
-    put_loss(a, row, true, loss, st);
-    if constexpr (GRAD) {
-        const float rg = a.row_grad ? a.row_grad[row] : 1.0f;
-        // every thread's logits for the loss are read before any is overwritten
-        put_grad<T, CE>(a, e, slope_of(a, e, st, rg), rg, s, out, 0, a.vocab, c);
+    const int nv = static_cast<int>(a.vocab / N);
+    const int held = (nv < kHold * THREADS ? nv : kHold * THREADS);
+    const int turns = (held + THREADS - 1) / THREADS;
+    const typename Raw<T>::V* p = reinterpret_cast<const typename Raw<T>::V*>(s);
+    typename Raw<T>::V raw[kHold];
+#pragma unroll
+    for (int j = 0; j < kHold; ++j) {
+        if (j >= turns) continue;
+        const int v = threadIdx.x + j * THREADS;
+        raw[j] = v < held ? p[v] : Raw<T>::lowest();
     }
+    const Entries e = entries_at(lds, a);
+    if (threadIdx.x < kWave) load_entries<T, true>(a, e, row, label, s, 0, a.vocab);
+
+    Stat st = {kLowest, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < kHold; ++j) {
+        if (j >= turns) continue;
+        float x[N];
+        Raw<T>::widen(raw[j], x);
+        st.m = max_n<N>(x, st.m);
+    }
+#pragma unroll
+    for (int j = 0; j < kHold; ++j) {
+        if (j >= turns) continue;
+        float x[N];
+        Raw<T>::widen(raw[j], x);
+        add_exp<TM, N>(st, x, c);
+    }
+    st = scan<T, TM, THREADS>(st, s, static_cast<int64_t>(held) * N, a.vocab, c);
+    st = block_join<TM, THREADS>(st, c, red);
+    if constexpr (!GRAD) {
+        if (threadIdx.x < kWave) put_loss(a, e, row, st, e.s);
+        return;
+    }
+
+    const float rg = a.row_grad ? a.row_grad[row] : 1.0f;
+    const Slope g = slope_of(a, *e.mass, st, rg, TM == kSame);
+#pragma unroll
+    for (int j = 0; j < kHold; ++j) {
+        if (j >= turns) continue;
+        const int v = threadIdx.x + j * THREADS;
+        if (v < held) put_slopes<T, TM>(out + static_cast<int64_t>(v) * N, raw[j], g, c);
+    }
+    put_columns<T, TM, THREADS>(g, s, out, static_cast<int64_t>(held) * N, a.vocab, 0, c);
+    if (threadIdx.x < kWave) put_loss(a, e, row, st, e.s);
+    __syncthreads();
+    put_entries<T, TM, THREADS>(a, e, g, rg, out, 0, a.vocab, c);
 }
 
-// One block per part of a row: the part's statistics; the first part's block
-// also picks the logits at the entries, for the loss.
-template <typename T, bool CE>
-__global__ void __launch_bounds__(kDistillThreads)
-    k_distill_parts(DistillArgs a, int64_t b0)
+constexpr int kPartThreads = 512;
+
+// One block per part of a row: the part's statistics, and the logits at the
+// entries in it, for the loss.
+template <typename T, Terms TM>
+__global__ void __launch_bounds__(kPartThreads) k_distill_parts(DistillArgs a, int64_t b0)
 {
-    __shared__ float red[kDistillWaves * 3];
+    __shared__ float red[kWaves(kPartThreads) * 3];
     const int64_t block = b0 + blockIdx.x, row = block / a.splits;
     const int part = static_cast<int>(block - row * a.splits);
     int label;
     if (!row_counts(a, row, &label)) return;
     const T* s = static_cast<const T*>(a.logits) + row * a.logits_pitch;
-    if (part == 0) {
-        for (int k = threadIdx.x; k < a.k + a.ce; k += kDistillThreads) {
-            const int col = k < a.k ? read_column(a.teacher_ids, a.id64, row * a.k + k, a.vocab)
-                                    : label;
-            if (col >= 0) a.picked[row * (a.k + 1) + k] = widen(s[col]);
-        }
-    }
     const int64_t c0 = part * a.part_cols;
     const int64_t c1 = c0 + a.part_cols < a.vocab ? c0 + a.part_cols : a.vocab;
     const float c = a.inv_tau * kLog2e;
-    const Stat st = block_join<CE>(scan<T, CE>(s, c0, c1, c), c, red);
+    for (int k = threadIdx.x; k < a.k + a.ce; k += kPartThreads) {
+        float u;
+        const int col = k < a.k ? read_entry(a, row * a.k + k, &u) : label;
+        if (col >= c0 && col < c1) a.picked[row * (a.k + 1) + k] = widen(s[col]);
+    }
+    Stat st = scan<T, TM, kPartThreads>(Stat{kLowest, 0.0f, 0.0f}, s, c0, c1, c);
+    st = block_join<TM, kPartThreads>(st, c, red);
     if (threadIdx.x == 0) {
         float* o = a.parts + block * kDistillPart;
         o[0] = st.m;
@@ -838,61 +955,82 @@ __global__ void __launch_bounds__(kDistillThreads)
     }
 }
 
-template <bool CE>
-__device__ __forceinline__ Stat join_parts(const DistillArgs& a, int64_t row, float c, float* red)
+// A row's statistics from its parts', by every wave for itself.
+template <Terms TM>
+__device__ __forceinline__ Stat join_parts(const DistillArgs& a, int64_t row, float c)
 {
     Stat s = {kLowest, 0.0f, 0.0f};
-    for (int i = threadIdx.x; i < a.splits; i += kDistillThreads) {
+    for (int i = threadIdx.x % kWave; i < a.splits; i += kWave) {
         const float* o = a.parts + (row * a.splits + i) * kDistillPart;
-        join<CE>(s, Stat{o[0], o[1], o[2]}, c);
+        join<TM>(s, Stat{o[0], o[1], o[2]}, c);
     }
-    return block_join<CE>(s, c, red);
+    s = lanes_join<TM>(s, c, kWave);
+    if constexpr (TM == kSame) s.b = s.a;
+    return s;
 }
 
-// One block per part of a row.  FROM_LSE: the gradient from saved
-// statistics.  Otherwise they come from the parts' statistics, the first
-// part's block writes the row's loss, and with GRAD every block its part of
-// the gradient.
-template <typename T, bool CE, bool GRAD, bool FROM_LSE>
-__global__ void __launch_bounds__(kDistillThreads)
-    k_distill_finish(DistillArgs a, int64_t b0)
+// Rows cut into parts, once the parts' statistics are there: one wave per
+// row for its loss.
+template <Terms TM>
+__global__ void __launch_bounds__(kWave) k_distill_loss(DistillArgs a, int64_t b0)
 {
     extern __shared__ __align__(16) char lds[];
-    __shared__ float red[kDistillWaves * 3];
-    const int64_t block = b0 + blockIdx.x, row = GRAD ? block / a.splits : block;
-    const int part = GRAD ? static_cast<int>(block - row * a.splits) : 0;
+    const int64_t row = b0 + blockIdx.x;
+    int label;
+    if (!row_counts(a, row, &label)) {
+        put_no_loss(a, row);
+        return;
+    }
+    const Entries e = entries_at(lds, a);
+    load_entries<float, false>(a, e, row, label, nullptr, 0, 0);
+    put_loss(a, e, row, join_parts<TM>(a, row, a.inv_tau * kLog2e), a.picked + row * (a.k + 1));
+}
+
+// One block per part of a row: its gradient, from the parts' statistics (the
+// first part's block writes the row's loss) or FROM_LSE, from saved ones.
+template <typename T, Terms TM, bool FROM_LSE>
+__global__ void __launch_bounds__(kPartThreads) k_distill_grad(DistillArgs a, int64_t b0)
+{
+    extern __shared__ __align__(16) char lds[];
+    const int64_t block = b0 + blockIdx.x, row = block / a.splits;
+    const int part = static_cast<int>(block - row * a.splits);
     const float c = a.inv_tau * kLog2e;
     const T* s = static_cast<const T*>(a.logits) + row * a.logits_pitch;
     T* out = static_cast<T*>(a.grad) + row * a.grad_pitch;
     const int64_t c0 = part * a.part_cols;
     const int64_t c1 = c0 + a.part_cols < a.vocab ? c0 + a.part_cols : a.vocab;
-    const Entries e = load_targets(a, row, lds, red);
-    if (!e.counts) {
-        if (!FROM_LSE && part == 0) put_loss(a, row, false, 0.0f, Stat{});
-        if constexpr (GRAD) put_zeros(out, c0, c1);
+    int label;
+    if (!row_counts(a, row, &label)) {
+        if (!FROM_LSE && part == 0) put_no_loss(a, row);
+        put_zeros<T, kPartThreads>(out, c0, c1);
         return;
     }
-    const float rg = GRAD && a.row_grad ? a.row_grad[row] : 1.0f;
+    const Entries e = entries_at(lds, a);
+    if (threadIdx.x < kWave) load_entries<T, true>(a, e, row, label, s, c0, c1);
+    const float rg = a.row_grad ? a.row_grad[row] : 1.0f;
+    Stat st = {};
+    if constexpr (!FROM_LSE) st = join_parts<TM>(a, row, c);
+    __syncthreads();
     Slope g;
     if constexpr (FROM_LSE) {
         // exp(s/tau - lse) = exp((s - m)/tau) * exp(m/tau - lse) with
-        // m = tau * lse rounded: the second factor takes up the rounding
+        // m = tau * lse rounded: the second factor, near 1, takes up the
+        // rounding
         const float lse = a.lse_in[2 * row], m = lse / a.inv_tau;
         const double rest = static_cast<double>(m) * a.inv_tau - lse;
         g.m_kd = m;
-        g.g_kd = rg * a.grad_kd * e.mass * (1.0f + static_cast<float>(rest));
+        g.g_kd = rg * a.grad_kd * *e.mass * (1.0f + static_cast<float>(rest));
         g.m_ce = a.lse_in[2 * row + 1];
         g.g_ce = rg * a.grad_ce;
+        if constexpr (TM == kSame) g.g_kd += g.g_ce;
     } else {
-        const Stat st = join_parts<CE>(a, row, c, red);
-        if (part == 0) {
-            const float* picked = a.picked + row * (a.k + 1);
-            const float loss = row_loss(a, e, st, [&](int k) { return picked[k]; }, red);
-            put_loss(a, row, true, loss, st);
-        }
-        g = slope_of(a, e, st, rg);
+        g = slope_of(a, *e.mass, st, rg, TM == kSame);
     }
-    if constexpr (GRAD) put_grad<T, CE>(a, e, g, rg, s, out, c0, c1, c);
+    put_columns<T, TM, kPartThreads>(g, s, out, c0, c1, 0, c);
+    if (!FROM_LSE && part == 0 && threadIdx.x < kWave)
+        put_loss(a, e, row, st, a.picked + row * (a.k + 1));
+    __syncthreads();
+    put_entries<T, TM, kPartThreads>(a, e, g, rg, out, c0, c1, c);
 }
 
 constexpr int kTotalThreads = 1024;
@@ -978,26 +1116,54 @@ int embed_sums(const EmbedArgs& a, const SumPlan& p, bool add, hipStream_t st)
     return add ? embed_sums<AT, GT, true>(a, p, st) : embed_sums<AT, GT, false>(a, p, st);
 }
 
-template <typename T, bool CE>
+// Rows of up to kHold vectors a thread of 256, 512 or 1024 threads: the
+// smallest block that holds the row, so that 16 waves are on a CU at any
+// length.
+template <typename T, Terms TM, bool GRAD>
+int distill_rows(const DistillArgs& a, hipStream_t st)
+{
+    const size_t lds = entry_bytes(a.k);
+    const int64_t vectors = a.vocab / Raw<T>::N;
+    if (vectors <= kHold * 256)
+        return launch(k_distill_row<T, TM, GRAD, 256>, a.rows, 256, lds, st, a);
+    if (vectors <= kHold * 512)
+        return launch(k_distill_row<T, TM, GRAD, 512>, a.rows, 512, lds, st, a);
+    return launch(k_distill_row<T, TM, GRAD, 1024>, a.rows, 1024, lds, st, a);
+}
+
+template <typename T, Terms TM>
 int distill_loss_t(const DistillArgs& a, bool grad, hipStream_t st)
 {
     const size_t lds = entry_bytes(a.k);
     if (a.splits == 1)
-        return grad ? launch(k_distill_row<T, CE, true>, a.rows, kDistillThreads, lds, st, a)
-                    : launch(k_distill_row<T, CE, false>, a.rows, kDistillThreads, lds, st, a);
+        return grad ? distill_rows<T, TM, true>(a, st) : distill_rows<T, TM, false>(a, st);
     const int64_t parts = a.rows * a.splits;
-    const int rc = launch(k_distill_parts<T, CE>, parts, kDistillThreads, 0, st, a);
+    const int rc = launch(k_distill_parts<T, TM>, parts, kPartThreads, 0, st, a);
     if (rc != ZS_OK) return rc;
-    return grad ? launch(k_distill_finish<T, CE, true, false>, parts, kDistillThreads, lds, st, a)
-                : launch(k_distill_finish<T, CE, false, false>, a.rows, kDistillThreads, lds, st,
-                         a);
+    return grad ? launch(k_distill_grad<T, TM, false>, parts, kPartThreads, lds, st, a)
+                : launch(k_distill_loss<TM>, a.rows, kWave, lds, st, a);
 }
 
-template <typename T, bool CE>
+template <typename T, Terms TM>
 int distill_grad_t(const DistillArgs& a, hipStream_t st)
 {
-    return launch(k_distill_finish<T, CE, true, true>, a.rows * a.splits, kDistillThreads,
-                  entry_bytes(a.k), st, a);
+    return launch(k_distill_grad<T, TM, true>, a.rows * a.splits, kPartThreads, entry_bytes(a.k),
+                  st, a);
+}
+
+// f(type tag, terms) for the call's element type and softmaxes.
+template <typename F>
+int by_type(const DistillArgs& a, F f)
+{
+    const Terms terms = !a.ce ? kKd : (a.inv_tau == 1.0f ? kSame : kKdCe);
+    auto typed = [&](auto tag) {
+        switch (terms) {
+        case kKd: return f(tag, std::integral_constant<Terms, kKd>{});
+        case kKdCe: return f(tag, std::integral_constant<Terms, kKdCe>{});
+        default: return f(tag, std::integral_constant<Terms, kSame>{});
+        }
+    };
+    return a.f32 ? typed(float{}) : typed(uint16_t{});
 }
 
 // Parts of whole vectors (of either element type).
@@ -1062,14 +1228,10 @@ int enqueue_distill_loss(DistillArgs a, bool with_grad, void* stream)
     a.splits = distill_splits(a.rows, a.vocab);
     a.part_cols = part_columns(a.vocab, a.splits);
     int rc = ZS_OK;
-    if (a.rows > 0) {
-        if (a.f32)
-            rc = a.ce ? distill_loss_t<float, true>(a, with_grad, st)
-                      : distill_loss_t<float, false>(a, with_grad, st);
-        else
-            rc = a.ce ? distill_loss_t<uint16_t, true>(a, with_grad, st)
-                      : distill_loss_t<uint16_t, false>(a, with_grad, st);
-    }
+    if (a.rows > 0)
+        rc = by_type(a, [&](auto tag, auto terms) {
+            return distill_loss_t<decltype(tag), decltype(terms)::value>(a, with_grad, st);
+        });
     if (rc != ZS_OK || (!a.loss_sum && !a.counted)) return rc;
     hipLaunchKernelGGL(k_distill_total, dim3(1), dim3(kTotalThreads), 0, st, a);
     return launched();
@@ -1082,8 +1244,9 @@ int enqueue_distill_grad(DistillArgs a, void* stream)
     if (a.rows == 0) return ZS_OK;
     a.splits = distill_splits(a.rows, a.vocab);
     a.part_cols = part_columns(a.vocab, a.splits);
-    if (a.f32) return a.ce ? distill_grad_t<float, true>(a, st) : distill_grad_t<float, false>(a, st);
-    return a.ce ? distill_grad_t<uint16_t, true>(a, st) : distill_grad_t<uint16_t, false>(a, st);
+    return by_type(a, [&](auto tag, auto terms) {
+        return distill_grad_t<decltype(tag), decltype(terms)::value>(a, st);
+    });
 }
 
 }  // namespace zs

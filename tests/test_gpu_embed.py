@@ -75,6 +75,24 @@ def test_lookup_values_pass_through():
     assert bool((out[1:].view(torch.int32) == 0).all())
 
 
+def test_every_bf16_rounding():
+    """fp32 -> bf16 at every kept half (subnormals, infinities, NaN) and the
+    dropped halves around the middle: torch's CPU cast, NaN as a class."""
+    hi = torch.arange(1 << 16, dtype=torch.int64) << 16
+    low = torch.tensor([0, 1, 0x7FFF, 0x8000, 0x8001, 0xFFFF])
+    bits = (hi[:, None] | low).to(torch.int64)
+    bits = torch.where(bits >= 1 << 31, bits - (1 << 32), bits).to(torch.int32).flatten()
+    x = bits.view(F32).reshape(-1, 1024)
+    n = x.shape[0]
+    out = torch.empty((n, 1024), dtype=BF16, device="cuda")
+    e = Z.make_embed(n, n, 1024, table_dtype=Z.ZS_F32)
+    Z.embed_lookup(e, torch.arange(n).cuda(), x.cuda(), out)
+    want, got = x.to(BF16), out.cpu()
+    nan = torch.isnan(x)
+    assert bool((torch.isnan(got) == nan).all())
+    assert torch.equal(got.view(torch.int16)[~nan], want.view(torch.int16)[~nan])
+
+
 def test_extreme_ids_are_not_here():
     lim = torch.iinfo(torch.int64)
     ids = torch.tensor([lim.min, lim.max, -1, 10, 14, 2 ** 32 + 10, lim.min + 10]).cuda()
