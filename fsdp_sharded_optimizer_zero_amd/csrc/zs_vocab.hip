@@ -33,6 +33,8 @@ constexpr float kLowest = -3.402823466e38f;
 
 // ---- elements ------------------------------------------------------------------
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(2)));
@@ -554,9 +556,15 @@ struct Raw;
 template <>
 struct Raw<uint16_t> {
     static constexpr int N = 8;
-    using V = u32x4_u;
+    using M = u32x4_u;  // in memory
+    using V = u32x4;    // in registers
     static __device__ __forceinline__ V lowest() { return V{kNegInf2, kNegInf2, kNegInf2, kNegInf2}; }
-    static __device__ __forceinline__ void widen(const V& b, float v[8])
+    static __device__ __forceinline__ V pack(const float v[8])
+    {
+        return V{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                 pack_bf16x2(v[6], v[7])};
+    }
+    static __device__ __forceinline__ void widen(V b, float v[8])
     {
         v[0] = bf16_lo(b.x); v[1] = bf16_hi(b.x);
         v[2] = bf16_lo(b.y); v[3] = bf16_hi(b.y);
@@ -568,12 +576,14 @@ struct Raw<uint16_t> {
 template <>
 struct Raw<float> {
     static constexpr int N = 4;
-    using V = f32x4_u;
+    using M = f32x4_u;
+    using V = f32x4;
+    static __device__ __forceinline__ V pack(const float v[4]) { return V{v[0], v[1], v[2], v[3]}; }
     static __device__ __forceinline__ V lowest()
     {
         return V{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     }
-    static __device__ __forceinline__ void widen(const V& b, float v[4])
+    static __device__ __forceinline__ void widen(V b, float v[4])
     {
         v[0] = b.x; v[1] = b.y; v[2] = b.z; v[3] = b.w;
     }
@@ -587,7 +597,7 @@ __device__ __forceinline__ float max_n(const float x[N], float m)
     return m;
 }
 
-// exp((x - m)/tau) of N elements, added in pairs to s.
+// exp((x - m)/tau) of N elements, added to s.
 template <Terms TM, int N>
 __device__ __forceinline__ void add_exp(Stat& s, const float x[N], float c)
 {
@@ -599,15 +609,93 @@ __device__ __forceinline__ void add_exp(Stat& s, const float x[N], float c)
     }
 }
 
+// Vector v of the nv at a scalar address (held opaque, so that it stays one)
+// and one 32-bit offset; beyond the last: the last, whose value is not used.
+template <typename T>
+__device__ __forceinline__ typename Raw<T>::V held_vector(uint64_t base, int v, int nv)
+{
+    v = v < nv ? v : nv - 1;
+    using P = const __attribute__((address_space(1))) typename Raw<T>::M*;
+    asm("" : "+s"(base));
+    return __builtin_nontemporal_load((P)(base + static_cast<uint32_t>(v) * 16u));
+}
+
+template <typename T>
+__device__ __forceinline__ void put_held(uint64_t base, int v, const float x[Raw<T>::N])
+{
+    using P = __attribute__((address_space(1))) typename Raw<T>::M*;
+    asm("" : "+s"(base));
+    const typename Raw<T>::M m = Raw<T>::pack(x);
+    __builtin_nontemporal_store(m, (P)(base + static_cast<uint32_t>(v) * 16u));
+}
+
+// Keeps what was computed from v before out of what is computed after: the
+// widened elements of a whole row would not fit the registers.
+template <typename V>
+__device__ __forceinline__ void forget(V& v)
+{
+    asm("" : "+v"(v));
+}
+
+// Below this |m c| an exponent may be taken as fma(x, c, -r), r = m c rounded:
+// one instruction for two, and exact but for its own rounding and for what r
+// was rounded by, at most 2^-8, which `rounded_by` gives back as a factor.
+// Beyond it (and for a row of -Inf alone) the difference is taken first.
+constexpr float kFmaLimit = 65536.0f;
+
+__device__ __forceinline__ bool fma_range(float m, float c) { return fabsf(m * c) <= kFmaLimit; }
+__device__ __forceinline__ float rounded_by(float m, float c)
+{
+    return exp2_hw(-__builtin_fmaf(m, c, -(m * c)));
+}
+
+// The statistics of the vectors raw[0..HOLD) of each thread, of which `own`
+// are real: the maximum, and the sums where every |m c| allows the fma form
+// (otherwise false is returned, for all lanes of the wave).
+template <typename T, Terms TM, int HOLD, typename Own>
+__device__ __forceinline__ bool held_stats(typename Raw<T>::V (&raw)[HOLD], Own own, float c,
+                                           Stat& st)
+{
+    constexpr int N = Raw<T>::N;
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < HOLD; ++j) {
+        if (!own(j)) raw[j] = Raw<T>::lowest();
+        float x[N];
+        Raw<T>::widen(raw[j], x);
+        m = max_n<N>(x, m);
+    }
+    const bool none = m == -INFINITY;
+    const float ref = none ? 0.0f : m;
+    if (!__all(fma_range(ref, c) && (TM != kKdCe || fma_range(ref, kLog2e)))) return false;
+    const float r = ref * c, r1 = ref * kLog2e;
+    float a = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int j = 0; j < HOLD; ++j) {
+        float x[N];
+        forget(raw[j]);
+        Raw<T>::widen(raw[j], x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            a += exp2_hw(__builtin_fmaf(x[i], c, -r));
+            if constexpr (TM == kKdCe) b += exp2_hw(__builtin_fmaf(x[i], kLog2e, -r1));
+        }
+    }
+    st.m = none ? kLowest : m;
+    st.a = none ? a : a * rounded_by(ref, c);
+    st.b = TM == kKdCe && !none ? b * rounded_by(ref, kLog2e) : b;
+    return true;
+}
+
 // The statistics of columns [c0, c1) of a row, over the block's threads, in
 // one pass with the running maximum.
-template <typename T, Terms TM, int THREADS>
+template <typename T, Terms TM, int THREADS, int UNROLL>
 __device__ __forceinline__ Stat scan(Stat s, const T* row, int64_t c0, int64_t c1, float c)
 {
     constexpr int N = Raw<T>::N;
     const int nv = static_cast<int>((c1 - c0) / N);
-    const typename Raw<T>::V* p = reinterpret_cast<const typename Raw<T>::V*>(row + c0);
-#pragma unroll 4
+    const typename Raw<T>::M* p = reinterpret_cast<const typename Raw<T>::M*>(row + c0);
+#pragma unroll UNROLL
     for (int v = threadIdx.x; v < nv; v += THREADS) {
         float x[N];
         Raw<T>::widen(p[v], x);
@@ -631,7 +719,7 @@ struct Entries {
     float* logp;
     float* p;
     float* s;
-    float* mass;    // sum of p
+    float* mass;    // sum of p, and behind it 1 if the row counts, else 0
     int n;          // K, or K + 1 with the label
 };
 
@@ -667,21 +755,32 @@ __device__ __forceinline__ int read_entry(const DistillArgs& a, int64_t at, floa
     return *u == -INFINITY ? -1 : col;
 }
 
-// Whether the row counts, and its label (-1: none).  Every wave finds out by
-// itself: no barrier, and the loads hit the cache after the first wave's.
-__device__ __forceinline__ bool row_counts(const DistillArgs& a, int64_t row, int* label)
+// A value all lanes of the wave hold, in a scalar register.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ uint64_t uniform(uint64_t x)
 {
-    *label = -1;
-    if (a.labels) {
-        *label = read_column(a.labels, a.id64, row, a.vocab);
-        if (*label < 0) return false;
+    const uint64_t lo = static_cast<uint32_t>(uniform(static_cast<int>(x)));
+    const uint64_t hi = static_cast<uint32_t>(uniform(static_cast<int>(x >> 32)));
+    return hi << 32 | lo;
+}
+
+// Whether the row's label lets it count (it may still have no entry), and the
+// label (0 without labels).  `row` is uniform; the label comes through the
+// scalar cache and does not wait for the vector loads under way.
+__device__ __forceinline__ bool label_counts(const DistillArgs& a, int64_t row, int* label)
+{
+    *label = 0;
+    if (!a.labels) return true;
+    int64_t id;
+    if (a.id64) {
+        using P = const __attribute__((address_space(4))) int64_t*;
+        id = ((P)reinterpret_cast<uint64_t>(a.labels))[row];
+    } else {
+        using P = const __attribute__((address_space(4))) int32_t*;
+        id = ((P)reinterpret_cast<uint64_t>(a.labels))[row];
     }
-    if (a.ce) return true;
-    for (int k = threadIdx.x % kWave; k - static_cast<int>(threadIdx.x % kWave) < a.k; k += kWave) {
-        float u;
-        if (__ballot(k < a.k && read_entry(a, row * a.k + k, &u) >= 0)) return true;
-    }
-    return false;
+    *label = static_cast<int>(id);
+    return id >= 0 && id < a.vocab;
 }
 
 // One wave's work: the row's entries into LDS, and with PICK the logits at
@@ -692,13 +791,17 @@ __device__ __forceinline__ void load_entries(const DistillArgs& a, const Entries
 {
     const int lane = threadIdx.x % kWave;
     float top = kLowest;
+    bool found = false;
     for (int k = lane; k < entry_slots(a.k); k += kWave) {
         int col = -1;
         float u = 0.0f;
         if (k < a.k) {
             col = read_entry(a, row * a.k + k, &u);
             u *= a.inv_tau;
-            if (col >= 0) top = fmaxf(top, u);
+            if (col >= 0) {
+                top = fmaxf(top, u);
+                found = true;
+            }
         } else if (k == a.k && a.ce) {
             col = label;
         }
@@ -707,6 +810,7 @@ __device__ __forceinline__ void load_entries(const DistillArgs& a, const Entries
         if (PICK && col >= c0 && col < c1) e.s[k] = widen(s[col]);
     }
     float mass = 0.0f;
+    const bool any = a.ce || __ballot(found) != 0;
     if (a.k > 0) {
         float norm;
         if (a.teacher_lse) {
@@ -727,10 +831,13 @@ __device__ __forceinline__ void load_entries(const DistillArgs& a, const Entries
         }
         mass = wave_sum(mass);
     }
-    if (lane == 0) *e.mass = mass;
+    if (lane == 0) {
+        e.mass[0] = mass;
+        e.mass[1] = any ? 1.0f : 0.0f;
+    }
 }
 
-// Loss, statistics and flag of a row that counts, by one wave.
+// Loss, statistics and flag of a row whose label lets it count, by one wave.
 __device__ __forceinline__ void put_loss(const DistillArgs& a, const Entries& e, int64_t row,
                                          const Stat& st, const float* logit)
 {
@@ -746,15 +853,16 @@ __device__ __forceinline__ void put_loss(const DistillArgs& a, const Entries& e,
     const float log_b = a.ce ? logf(st.b) : 0.0f;
     if (a.ce) loss += a.loss_ce * (log_b - (logit[a.k] - st.m));
     if (lane != 0) return;
-    a.loss[row] = loss;
-    a.counts[row] = 1;
+    const bool counts = e.mass[1] != 0.0f;
+    a.loss[row] = counts ? loss : 0.0f;
+    a.counts[row] = counts;
     if (a.lse_out) {
-        a.lse_out[2 * row] = st.m * a.inv_tau + log_a;
+        a.lse_out[2 * row] = counts ? st.m * a.inv_tau + log_a : 0.0f;
         a.lse_out[2 * row + 1] = a.ce ? st.m + log_b : 0.0f;
     }
 }
 
-// A row that does not count.
+// A row whose label masks it.
 __device__ __forceinline__ void put_no_loss(const DistillArgs& a, int64_t row)
 {
     if (threadIdx.x != 0) return;
@@ -785,8 +893,49 @@ __device__ __forceinline__ Slope slope_of(const DistillArgs& a, float mass, cons
     return g;
 }
 
+// The fma form of a slope, for the vectors a block holds.
+struct FmaSlope {
+    float r_kd, g_kd, r_ce, g_ce;
+};
+__device__ __forceinline__ FmaSlope fma_slope(const Slope& g, float c)
+{
+    return FmaSlope{g.m_kd * c, g.g_kd * rounded_by(g.m_kd, c), g.m_ce * kLog2e,
+                    g.g_ce * rounded_by(g.m_ce, kLog2e)};
+}
+
+template <Terms TM>
+__device__ __forceinline__ bool slope_fma(const Slope& g, float c)
+{
+    return fma_range(g.m_kd, c) && (TM != kKdCe || fma_range(g.m_ce, kLog2e));
+}
+
+template <typename T, Terms TM, int HOLD, typename Vector>
+__device__ __forceinline__ void put_held_slopes(T* out, typename Raw<T>::V (&raw)[HOLD],
+                                                Vector vector, int nv, const FmaSlope& g, float c)
+{
+    constexpr int N = Raw<T>::N;
+    const uint64_t to = reinterpret_cast<uint64_t>(out);
+#pragma unroll
+    for (int j = 0; j < HOLD; ++j) {
+        const int v = vector(j);
+        forget(raw[j]);
+        if (v < nv) {
+            float x[N];
+            Raw<T>::widen(raw[j], x);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float y = g.g_kd * exp2_hw(__builtin_fmaf(x[i], c, -g.r_kd));
+                if constexpr (TM == kKdCe)
+                    y += g.g_ce * exp2_hw(__builtin_fmaf(x[i], kLog2e, -g.r_ce));
+                x[i] = y;
+            }
+            put_held<T>(to, v, x);
+        }
+    }
+}
+
 template <typename T, Terms TM>
-__device__ __forceinline__ void put_slopes(T* out, const typename Raw<T>::V& raw, const Slope& g,
+__device__ __forceinline__ void put_slopes(T* out, typename Raw<T>::V raw, const Slope& g,
                                            float c)
 {
     constexpr int N = Raw<T>::N;
@@ -797,17 +946,16 @@ __device__ __forceinline__ void put_slopes(T* out, const typename Raw<T>::V& raw
     store_n<N>(out, x);
 }
 
-// The gradient of vectors [v0, nv) of the columns [c0, c1), and of the
-// elements behind the last vector.
-template <typename T, Terms TM, int THREADS>
+// The gradient of columns [c0, c1) of a row.
+template <typename T, Terms TM, int THREADS, int UNROLL>
 __device__ __forceinline__ void put_columns(const Slope& g, const T* row, T* out, int64_t c0,
-                                            int64_t c1, int v0, float c)
+                                            int64_t c1, float c)
 {
     constexpr int N = Raw<T>::N;
     const int nv = static_cast<int>((c1 - c0) / N);
-    const typename Raw<T>::V* p = reinterpret_cast<const typename Raw<T>::V*>(row + c0);
-#pragma unroll 4
-    for (int v = v0 + threadIdx.x; v < nv; v += THREADS)
+    const typename Raw<T>::M* p = reinterpret_cast<const typename Raw<T>::M*>(row + c0);
+#pragma unroll UNROLL
+    for (int v = threadIdx.x; v < nv; v += THREADS)
         put_slopes<T, TM>(out + c0 + static_cast<int64_t>(v) * N, p[v], g, c);
     const int64_t e = c0 + static_cast<int64_t>(nv) * N + threadIdx.x;
     if (e < c1) put(out + e, slope_at<TM>(g, widen(row[e]), c));
@@ -851,15 +999,14 @@ __device__ __forceinline__ void put_zeros(T* out, int64_t c0, int64_t c1)
     if (e < c1) put(out + e, 0.0f);
 }
 
-// Vectors of a row each thread keeps in registers between the two passes:
-// 64 registers, which with the rest stays under the 128 that 16 waves on a CU
-// have each.  A block of 1024 threads so keeps 131072 bf16 (65536 fp32)
-// logits; what a longer row has beyond that is read again.
+// Vectors of a row each thread keeps in registers: 64 registers of the 128
+// that 16 waves on a CU have each.  A block of 1024 threads so keeps 131072
+// bf16 (65536 fp32) logits; what a longer row has beyond that is read again.
 constexpr int kHold = 16;
-
 // One block per row: the loss, and with GRAD the gradient, the row read once.
-template <typename T, Terms TM, bool GRAD, int THREADS>
-__global__ void __launch_bounds__(THREADS) k_distill_row(DistillArgs a, int64_t b0)
+// (SHORT: a row may have no whole vector.)
+template <typename T, Terms TM, bool GRAD, int THREADS, int HOLD, bool SHORT>
+__global__ void __launch_bounds__(THREADS, 4) k_distill_row(DistillArgs a, int64_t b0)
 {
     extern __shared__ __align__(16) char lds[];
     __shared__ float red[kWaves(THREADS) * 3];
@@ -869,59 +1016,42 @@ __global__ void __launch_bounds__(THREADS) k_distill_row(DistillArgs a, int64_t 
     const T* s = static_cast<const T*>(a.logits) + row * a.logits_pitch;
     T* out = static_cast<T*>(a.grad) + row * a.grad_pitch;
     int label;
-    if (!row_counts(a, row, &label)) {
+    if (!label_counts(a, row, &label)) {
         put_no_loss(a, row);
         if constexpr (GRAD) put_zeros<T, THREADS>(out, 0, a.vocab);
         return;
     }
-    const int nv = static_cast<int>(a.vocab / N);
-    const int held = (nv < kHold * THREADS ? nv : kHold * THREADS);
-    const int turns = (held + THREADS - 1) / THREADS;
-    const typename Raw<T>::V* p = reinterpret_cast<const typename Raw<T>::V*>(s);
-    typename Raw<T>::V raw[kHold];
+    const int64_t vectors = a.vocab / N;
+    const int nv = static_cast<int>(vectors < HOLD * THREADS ? vectors : HOLD * THREADS);
+    const int64_t held = static_cast<int64_t>(nv) * N;
+    int tid = threadIdx.x;
+    typename Raw<T>::V raw[HOLD];
+    const auto vector = [&](int j) { return tid + j * THREADS; };
 #pragma unroll
-    for (int j = 0; j < kHold; ++j) {
-        if (j >= turns) continue;
-        const int v = threadIdx.x + j * THREADS;
-        raw[j] = v < held ? p[v] : Raw<T>::lowest();
-    }
+    for (int j = 0; j < HOLD; ++j)
+        raw[j] = SHORT && nv == 0 ? Raw<T>::lowest()
+                                  : held_vector<T>(reinterpret_cast<uint64_t>(s), vector(j), nv);
     const Entries e = entries_at(lds, a);
     if (threadIdx.x < kWave) load_entries<T, true>(a, e, row, label, s, 0, a.vocab);
-
     Stat st = {kLowest, 0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < kHold; ++j) {
-        if (j >= turns) continue;
-        float x[N];
-        Raw<T>::widen(raw[j], x);
-        st.m = max_n<N>(x, st.m);
-    }
-#pragma unroll
-    for (int j = 0; j < kHold; ++j) {
-        if (j >= turns) continue;
-        float x[N];
-        Raw<T>::widen(raw[j], x);
-        add_exp<TM, N>(st, x, c);
-    }
-    st = scan<T, TM, THREADS>(st, s, static_cast<int64_t>(held) * N, a.vocab, c);
+    const bool sums = held_stats<T, TM>(raw, [&](int j) { return vector(j) < nv; }, c, st);
+    st = scan<T, TM, THREADS, 4>(st, s, sums ? held : 0, a.vocab, c);
     st = block_join<TM, THREADS>(st, c, red);
-    if constexpr (!GRAD) {
-        if (threadIdx.x < kWave) put_loss(a, e, row, st, e.s);
-        return;
+    if (threadIdx.x / kWave == 1) put_loss(a, e, row, st, e.s);
+    if constexpr (GRAD) {
+        if (e.mass[1] == 0.0f) {
+            put_zeros<T, THREADS>(out, 0, a.vocab);
+            return;
+        }
+        const float rg = a.row_grad ? a.row_grad[row] : 1.0f;
+        const Slope g = slope_of(a, *e.mass, st, rg, TM == kSame);
+        const bool fma = slope_fma<TM>(g, c);
+        forget(tid);
+        if (fma) put_held_slopes<T, TM>(out, raw, vector, nv, fma_slope(g, c), c);
+        put_columns<T, TM, THREADS, 4>(g, s, out, fma ? held : 0, a.vocab, c);
+        __syncthreads();
+        put_entries<T, TM, THREADS>(a, e, g, rg, out, 0, a.vocab, c);
     }
-
-    const float rg = a.row_grad ? a.row_grad[row] : 1.0f;
-    const Slope g = slope_of(a, *e.mass, st, rg, TM == kSame);
-#pragma unroll
-    for (int j = 0; j < kHold; ++j) {
-        if (j >= turns) continue;
-        const int v = threadIdx.x + j * THREADS;
-        if (v < held) put_slopes<T, TM>(out + static_cast<int64_t>(v) * N, raw[j], g, c);
-    }
-    put_columns<T, TM, THREADS>(g, s, out, static_cast<int64_t>(held) * N, a.vocab, 0, c);
-    if (threadIdx.x < kWave) put_loss(a, e, row, st, e.s);
-    __syncthreads();
-    put_entries<T, TM, THREADS>(a, e, g, rg, out, 0, a.vocab, c);
 }
 
 constexpr int kPartThreads = 512;
@@ -935,7 +1065,7 @@ __global__ void __launch_bounds__(kPartThreads) k_distill_parts(DistillArgs a, i
     const int64_t block = b0 + blockIdx.x, row = block / a.splits;
     const int part = static_cast<int>(block - row * a.splits);
     int label;
-    if (!row_counts(a, row, &label)) return;
+    if (!label_counts(a, row, &label)) return;
     const T* s = static_cast<const T*>(a.logits) + row * a.logits_pitch;
     const int64_t c0 = part * a.part_cols;
     const int64_t c1 = c0 + a.part_cols < a.vocab ? c0 + a.part_cols : a.vocab;
@@ -945,7 +1075,7 @@ __global__ void __launch_bounds__(kPartThreads) k_distill_parts(DistillArgs a, i
         const int col = k < a.k ? read_entry(a, row * a.k + k, &u) : label;
         if (col >= c0 && col < c1) a.picked[row * (a.k + 1) + k] = widen(s[col]);
     }
-    Stat st = scan<T, TM, kPartThreads>(Stat{kLowest, 0.0f, 0.0f}, s, c0, c1, c);
+    Stat st = scan<T, TM, kPartThreads, 4>(Stat{kLowest, 0.0f, 0.0f}, s, c0, c1, c);
     st = block_join<TM, kPartThreads>(st, c, red);
     if (threadIdx.x == 0) {
         float* o = a.parts + block * kDistillPart;
@@ -977,7 +1107,7 @@ __global__ void __launch_bounds__(kWave) k_distill_loss(DistillArgs a, int64_t b
     extern __shared__ __align__(16) char lds[];
     const int64_t row = b0 + blockIdx.x;
     int label;
-    if (!row_counts(a, row, &label)) {
+    if (!label_counts(a, row, &label)) {
         put_no_loss(a, row);
         return;
     }
@@ -1000,7 +1130,7 @@ __global__ void __launch_bounds__(kPartThreads) k_distill_grad(DistillArgs a, in
     const int64_t c0 = part * a.part_cols;
     const int64_t c1 = c0 + a.part_cols < a.vocab ? c0 + a.part_cols : a.vocab;
     int label;
-    if (!row_counts(a, row, &label)) {
+    if (!label_counts(a, row, &label)) {
         if (!FROM_LSE && part == 0) put_no_loss(a, row);
         put_zeros<T, kPartThreads>(out, c0, c1);
         return;
@@ -1011,6 +1141,11 @@ __global__ void __launch_bounds__(kPartThreads) k_distill_grad(DistillArgs a, in
     Stat st = {};
     if constexpr (!FROM_LSE) st = join_parts<TM>(a, row, c);
     __syncthreads();
+    if (e.mass[1] == 0.0f) {
+        if (!FROM_LSE && part == 0) put_no_loss(a, row);
+        put_zeros<T, kPartThreads>(out, c0, c1);
+        return;
+    }
     Slope g;
     if constexpr (FROM_LSE) {
         // exp(s/tau - lse) = exp((s - m)/tau) * exp(m/tau - lse) with
@@ -1026,7 +1161,7 @@ __global__ void __launch_bounds__(kPartThreads) k_distill_grad(DistillArgs a, in
     } else {
         g = slope_of(a, *e.mass, st, rg, TM == kSame);
     }
-    put_columns<T, TM, kPartThreads>(g, s, out, c0, c1, 0, c);
+    put_columns<T, TM, kPartThreads, 4>(g, s, out, c0, c1, c);
     if (!FROM_LSE && part == 0 && threadIdx.x < kWave)
         put_loss(a, e, row, st, a.picked + row * (a.k + 1));
     __syncthreads();
@@ -1116,19 +1251,20 @@ int embed_sums(const EmbedArgs& a, const SumPlan& p, bool add, hipStream_t st)
     return add ? embed_sums<AT, GT, true>(a, p, st) : embed_sums<AT, GT, false>(a, p, st);
 }
 
-// Rows of up to kHold vectors a thread of 256, 512 or 1024 threads: the
-// smallest block that holds the row, so that 16 waves are on a CU at any
-// length.
+// The smallest block that holds the row, so that 16 waves are on a CU at any
+// length; short rows hold less.
 template <typename T, Terms TM, bool GRAD>
 int distill_rows(const DistillArgs& a, hipStream_t st)
 {
     const size_t lds = entry_bytes(a.k);
     const int64_t vectors = a.vocab / Raw<T>::N;
+    if (vectors <= 4 * 256)
+        return launch(k_distill_row<T, TM, GRAD, 256, 4, true>, a.rows, 256, lds, st, a);
     if (vectors <= kHold * 256)
-        return launch(k_distill_row<T, TM, GRAD, 256>, a.rows, 256, lds, st, a);
+        return launch(k_distill_row<T, TM, GRAD, 256, kHold, false>, a.rows, 256, lds, st, a);
     if (vectors <= kHold * 512)
-        return launch(k_distill_row<T, TM, GRAD, 512>, a.rows, 512, lds, st, a);
-    return launch(k_distill_row<T, TM, GRAD, 1024>, a.rows, 1024, lds, st, a);
+        return launch(k_distill_row<T, TM, GRAD, 512, kHold, false>, a.rows, 512, lds, st, a);
+    return launch(k_distill_row<T, TM, GRAD, 1024, kHold, false>, a.rows, 1024, lds, st, a);
 }
 
 template <typename T, Terms TM>

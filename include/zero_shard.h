@@ -446,8 +446,8 @@ size_t zs_distill_workspace_bytes(const zs_distill* d);
  *   KD = sum over K of p_k (log p_k - log q_{id_k});   CE = lse_1 - s_label
  *   loss_out[t] = alpha tau^2 KD + (1 - alpha) CE
  * A row counts when its label (where labels are given) is in [0, V) and, if
- * alpha == 1, it has a teacher entry.  Any other row has loss 0, and its
- * logits are not read.  An entry with p_k = 0 adds nothing; the same id twice
+ * alpha == 1, it has a teacher entry.  Any other row has loss 0, whatever its
+ * logits hold.  An entry with p_k = 0 adds nothing; the same id twice
  * is two entries.  alpha < 1 needs labels; alpha == 0 reads no teacher.  NaN
  * and +Inf in a row that counts propagate; a logit of -Inf has probability 0.
  *   loss_out   fp32[T].
