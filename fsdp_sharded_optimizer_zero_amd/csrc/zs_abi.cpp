@@ -341,7 +341,7 @@ int set_loss(const zs_distill* d, float* loss_out, float* lse_out, float* loss_s
         !aligned_to(loss_sum, 4) || !aligned_to(counted, 8))
         return ZS_EALIGN;
     if (workspace_bytes < zs_distill_workspace_bytes(d)) return ZS_EWORKSPACE;
-    const DistillSpace w = distill_space(d->rows, d->vocab, d->k);
+    const DistillSpace w = distill_space(d->rows, d->vocab, d->k, a->f32 != 0);
     char* base = static_cast<char*>(workspace);
     a->counts = reinterpret_cast<int32_t*>(base + w.counts);
     a->parts = reinterpret_cast<float*>(base + w.parts);

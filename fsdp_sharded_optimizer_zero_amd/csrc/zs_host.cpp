@@ -99,14 +99,15 @@ EmbedSpace embed_space(int64_t tokens, int64_t rows, int64_t dim)
     return w;
 }
 
-DistillSpace distill_space(int64_t rows, int64_t vocab, int32_t k)
+DistillSpace distill_space(int64_t rows, int64_t vocab, int32_t k, bool f32)
 {
     DistillSpace w;
-    const int64_t splits = distill_splits(rows, vocab);
+    const DistillShape s = distill_shape(rows, vocab, f32);
     w.counts = 0;
     w.parts = round_up(rows > 0 ? rows * 4 : 4, 256);
-    w.picked = w.parts + (splits > 1 ? round_up(rows * splits * kDistillPart * 4, 256) : 0);
-    w.bytes = w.picked + (splits > 1 ? round_up(rows * (k + 1) * 4, 256) : 0);
+    w.picked = w.parts +
+               (s.rows_loss ? 0 : round_up(rows * s.splits * kDistillPart * int64_t(4), 256));
+    w.bytes = w.picked + (s.rows_loss_grad ? 0 : round_up(rows * (k + 1) * int64_t(4), 256));
     return w;
 }
 
@@ -208,7 +209,7 @@ size_t zs_embed_workspace_bytes(const zs_embed* e)
 size_t zs_distill_workspace_bytes(const zs_distill* d)
 {
     if (zs::check_distill(d) != ZS_OK) return 0;
-    return static_cast<size_t>(zs::distill_space(d->rows, d->vocab, d->k).bytes);
+    return static_cast<size_t>(zs::distill_space(d->rows, d->vocab, d->k, d->logits_dtype == ZS_F32).bytes);
 }
 
 double zs_state_bytes(double psi, int32_t n_d, int32_t stage, double K)

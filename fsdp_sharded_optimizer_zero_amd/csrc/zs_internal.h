@@ -185,23 +185,49 @@ struct DistillArgs {
 };
 
 // A row cut into parts leaves per part: the maximum, and the sums of
-// exp((s - max)/tau) and exp(s - max).
+// exp((s - max)/tau) and exp(s - max) (and a fourth number, unused: 16 bytes).
 constexpr int kDistillPart = 4;
-// Rows below this number leave CUs idle, or a ragged last turn, at one block
-// a row: each row is then cut into parts.
+
+// How a call cuts its work.  A part is what a block of kDistillPartThreads
+// holds in registers at `hold` 16-byte vectors a thread: 8, or 2 where 8 would
+// make too few blocks to fill the GPU.
+//  - The gradient from saved statistics always runs in parts.
+//  - The loss runs a block a row where a block of 256 threads holds the row,
+//    otherwise in parts, then one wave a row.
+//  - Loss and gradient in one call run a block a row (reading the logits
+//    once) from kDistillRows rows on, or where a row is one part; fewer rows
+//    would leave CUs idle, and run in parts, twice.
+constexpr int kDistillPartThreads = 256;
+constexpr int kDistillHold = 8;
+constexpr int kDistillFewHold = 2;
+constexpr int64_t kDistillBlocks = 2048;    // 8 blocks of 4 waves on each of 256 CUs
 constexpr int64_t kDistillRows = 512;
-// Parts a row is cut into: about two blocks per CU in all, at least 4096
-// columns each.
-inline int32_t distill_splits(int64_t rows, int64_t vocab)
+struct DistillShape {
+    int32_t splits;         // parts of a row
+    int32_t hold;
+    int64_t part_cols;      // columns of a part
+    bool rows_loss;         // a block a row for the loss
+    bool rows_loss_grad;    // the same for loss and gradient
+};
+inline DistillShape distill_shape(int64_t rows, int64_t vocab, bool f32)
 {
-    if (rows < 1 || rows >= kDistillRows) return 1;
-    const int64_t want = (kDistillRows + rows - 1) / rows, most = (vocab + 4095) / 4096;
-    return static_cast<int32_t>(want < most ? want : most);
+    const int64_t vector = f32 ? 4 : 8;
+    const auto parts = [&](int64_t hold) {
+        const int64_t cols = hold * kDistillPartThreads * vector;
+        return (vocab + cols - 1) / cols;
+    };
+    DistillShape s;
+    s.hold = rows * parts(kDistillHold) >= kDistillBlocks ? kDistillHold : kDistillFewHold;
+    s.splits = static_cast<int32_t>(parts(s.hold));
+    s.part_cols = s.hold * kDistillPartThreads * vector;
+    s.rows_loss = s.splits == 1 || (rows >= kDistillRows && vocab / vector <= 16 * 256);
+    s.rows_loss_grad = s.splits == 1 || rows >= kDistillRows;
+    return s;
 }
 struct DistillSpace {
     int64_t counts, parts, picked, bytes;
 };
-DistillSpace distill_space(int64_t rows, int64_t vocab, int32_t k);
+DistillSpace distill_space(int64_t rows, int64_t vocab, int32_t k, bool f32);
 
 int enqueue_distill_loss(DistillArgs a, bool with_grad, void* stream);
 int enqueue_distill_grad(DistillArgs a, void* stream);

@@ -1054,35 +1054,56 @@ __global__ void __launch_bounds__(THREADS, 4) k_distill_row(DistillArgs a, int64
     }
 }
 
-constexpr int kPartThreads = 512;
+// A row cut into parts: a part is what one block of kPartThreads holds at HOLD
+// vectors a thread, all of them loaded at once.  Parts are dispatched in the
+// order of their addresses, so that the accesses under way are one window
+// that moves through the logits, which suits the HBM best (2048 x 50257 fp32:
+// the loss 60 + 7 us, its gradient 138; a block a row: 92 and 177).
+constexpr int kPartThreads = kDistillPartThreads;
 
-// One block per part of a row: the part's statistics, and the logits at the
-// entries in it, for the loss.
-template <typename T, Terms TM>
+// Vectors of a part that lie in the row.
+template <typename T, int HOLD>
+__device__ __forceinline__ int part_vectors(int64_t c0, int64_t vocab)
+{
+    const int64_t nv = (vocab - c0) / Raw<T>::N;
+    return static_cast<int>(nv < HOLD * kPartThreads ? nv : HOLD * kPartThreads);
+}
+
+// The part's statistics, and, if a gradient follows (which may overwrite
+// them), the logits at the entries in it.
+template <typename T, Terms TM, int HOLD>
 __global__ void __launch_bounds__(kPartThreads) k_distill_parts(DistillArgs a, int64_t b0)
 {
     __shared__ float red[kWaves(kPartThreads) * 3];
     const int64_t block = b0 + blockIdx.x, row = block / a.splits;
-    const int part = static_cast<int>(block - row * a.splits);
+    const int64_t c0 = (block - row * a.splits) * a.part_cols;
     int label;
     if (!label_counts(a, row, &label)) return;
-    const T* s = static_cast<const T*>(a.logits) + row * a.logits_pitch;
-    const int64_t c0 = part * a.part_cols;
     const int64_t c1 = c0 + a.part_cols < a.vocab ? c0 + a.part_cols : a.vocab;
+    const T* s = static_cast<const T*>(a.logits) + row * a.logits_pitch;
     const float c = a.inv_tau * kLog2e;
-    for (int k = threadIdx.x; k < a.k + a.ce; k += kPartThreads) {
-        float u;
-        const int col = k < a.k ? read_entry(a, row * a.k + k, &u) : label;
-        if (col >= c0 && col < c1) a.picked[row * (a.k + 1) + k] = widen(s[col]);
+    const int nv = part_vectors<T, HOLD>(c0, a.vocab);
+    const auto vector = [&](int j) { return static_cast<int>(threadIdx.x) + j * kPartThreads; };
+    typename Raw<T>::V raw[HOLD];
+#pragma unroll
+    for (int j = 0; j < HOLD; ++j)
+        raw[j] = nv == 0 ? Raw<T>::lowest()
+                         : held_vector<T>(reinterpret_cast<uint64_t>(s + c0), vector(j), nv);
+    if (a.grad) {
+        for (int k = threadIdx.x; k < a.k + a.ce; k += kPartThreads) {
+            float u;
+            const int col = k < a.k ? read_entry(a, row * a.k + k, &u) : label;
+            if (col >= c0 && col < c1) a.picked[row * (a.k + 1) + k] = widen(s[col]);
+        }
     }
-    Stat st = scan<T, TM, kPartThreads, 4>(Stat{kLowest, 0.0f, 0.0f}, s, c0, c1, c);
+    Stat st = {kLowest, 0.0f, 0.0f};
+    const bool sums = held_stats<T, TM>(raw, [&](int j) { return vector(j) < nv; }, c, st);
+    const int64_t rest = c0 + (sums ? static_cast<int64_t>(nv) * Raw<T>::N : 0);
+    st = scan<T, TM, kPartThreads, 1>(st, s, rest, c1, c);
     st = block_join<TM, kPartThreads>(st, c, red);
-    if (threadIdx.x == 0) {
-        float* o = a.parts + block * kDistillPart;
-        o[0] = st.m;
-        o[1] = st.a;
-        o[2] = st.b;
-    }
+    if (threadIdx.x == 0)
+        *reinterpret_cast<float4*>(a.parts + block * kDistillPart) =
+            float4{st.m, st.a, st.b, 0.0f};
 }
 
 // A row's statistics from its parts', by every wave for itself.
@@ -1091,17 +1112,18 @@ __device__ __forceinline__ Stat join_parts(const DistillArgs& a, int64_t row, fl
 {
     Stat s = {kLowest, 0.0f, 0.0f};
     for (int i = threadIdx.x % kWave; i < a.splits; i += kWave) {
-        const float* o = a.parts + (row * a.splits + i) * kDistillPart;
-        join<TM>(s, Stat{o[0], o[1], o[2]}, c);
+        const float4 o =
+            *reinterpret_cast<const float4*>(a.parts + (row * a.splits + i) * kDistillPart);
+        join<TM>(s, Stat{o.x, o.y, o.z}, c);
     }
     s = lanes_join<TM>(s, c, kWave);
     if constexpr (TM == kSame) s.b = s.a;
     return s;
 }
 
-// Rows cut into parts, once the parts' statistics are there: one wave per
-// row for its loss.
-template <Terms TM>
+// The loss of rows cut into parts, once the parts' statistics are there: one
+// wave per row.
+template <typename T, Terms TM>
 __global__ void __launch_bounds__(kWave) k_distill_loss(DistillArgs a, int64_t b0)
 {
     extern __shared__ __align__(16) char lds[];
@@ -1112,13 +1134,14 @@ __global__ void __launch_bounds__(kWave) k_distill_loss(DistillArgs a, int64_t b
         return;
     }
     const Entries e = entries_at(lds, a);
-    load_entries<float, false>(a, e, row, label, nullptr, 0, 0);
-    put_loss(a, e, row, join_parts<TM>(a, row, a.inv_tau * kLog2e), a.picked + row * (a.k + 1));
+    load_entries<T, true>(a, e, row, label,
+                          static_cast<const T*>(a.logits) + row * a.logits_pitch, 0, a.vocab);
+    put_loss(a, e, row, join_parts<TM>(a, row, a.inv_tau * kLog2e), e.s);
 }
 
-// One block per part of a row: its gradient, from the parts' statistics (the
-// first part's block writes the row's loss) or FROM_LSE, from saved ones.
-template <typename T, Terms TM, bool FROM_LSE>
+// The gradient of a part, from the parts' statistics (the first part's block
+// writes the row's loss) or FROM_LSE, from saved ones.
+template <typename T, Terms TM, int HOLD, bool FROM_LSE>
 __global__ void __launch_bounds__(kPartThreads) k_distill_grad(DistillArgs a, int64_t b0)
 {
     extern __shared__ __align__(16) char lds[];
@@ -1135,6 +1158,13 @@ __global__ void __launch_bounds__(kPartThreads) k_distill_grad(DistillArgs a, in
         put_zeros<T, kPartThreads>(out, c0, c1);
         return;
     }
+    const int nv = part_vectors<T, HOLD>(c0, a.vocab);
+    const auto vector = [&](int j) { return static_cast<int>(threadIdx.x) + j * kPartThreads; };
+    typename Raw<T>::V raw[HOLD];
+#pragma unroll
+    for (int j = 0; j < HOLD; ++j)
+        raw[j] = nv == 0 ? Raw<T>::lowest()
+                         : held_vector<T>(reinterpret_cast<uint64_t>(s + c0), vector(j), nv);
     const Entries e = entries_at(lds, a);
     if (threadIdx.x < kWave) load_entries<T, true>(a, e, row, label, s, c0, c1);
     const float rg = a.row_grad ? a.row_grad[row] : 1.0f;
@@ -1161,8 +1191,11 @@ __global__ void __launch_bounds__(kPartThreads) k_distill_grad(DistillArgs a, in
     } else {
         g = slope_of(a, *e.mass, st, rg, TM == kSame);
     }
-    put_columns<T, TM, kPartThreads, 4>(g, s, out, c0, c1, c);
-    if (!FROM_LSE && part == 0 && threadIdx.x < kWave)
+    const bool fma = slope_fma<TM>(g, c);
+    if (fma) put_held_slopes<T, TM>(out + c0, raw, vector, nv, fma_slope(g, c), c);
+    const int64_t rest = c0 + (fma ? static_cast<int64_t>(nv) * Raw<T>::N : 0);
+    put_columns<T, TM, kPartThreads, 1>(g, s, out, rest, c1, c);
+    if (!FROM_LSE && part == 0 && threadIdx.x / kWave == 1)
         put_loss(a, e, row, st, a.picked + row * (a.k + 1));
     __syncthreads();
     put_entries<T, TM, kPartThreads>(a, e, g, rg, out, c0, c1, c);
@@ -1267,24 +1300,35 @@ int distill_rows(const DistillArgs& a, hipStream_t st)
     return launch(k_distill_row<T, TM, GRAD, 1024, kHold, false>, a.rows, 1024, lds, st, a);
 }
 
-template <typename T, Terms TM>
-int distill_loss_t(const DistillArgs& a, bool grad, hipStream_t st)
+template <typename T, Terms TM, int HOLD>
+int distill_loss_parts(const DistillArgs& a, bool grad, hipStream_t st)
 {
     const size_t lds = entry_bytes(a.k);
-    if (a.splits == 1)
-        return grad ? distill_rows<T, TM, true>(a, st) : distill_rows<T, TM, false>(a, st);
     const int64_t parts = a.rows * a.splits;
-    const int rc = launch(k_distill_parts<T, TM>, parts, kPartThreads, 0, st, a);
+    const int rc = launch(k_distill_parts<T, TM, HOLD>, parts, kPartThreads, 0, st, a);
     if (rc != ZS_OK) return rc;
-    return grad ? launch(k_distill_grad<T, TM, false>, parts, kPartThreads, lds, st, a)
-                : launch(k_distill_loss<TM>, a.rows, kWave, lds, st, a);
+    return grad ? launch(k_distill_grad<T, TM, HOLD, false>, parts, kPartThreads, lds, st, a)
+                : launch(k_distill_loss<T, TM>, a.rows, kWave, lds, st, a);
 }
 
 template <typename T, Terms TM>
-int distill_grad_t(const DistillArgs& a, hipStream_t st)
+int distill_loss_t(const DistillArgs& a, const DistillShape& s, bool grad, hipStream_t st)
 {
-    return launch(k_distill_grad<T, TM, true>, a.rows * a.splits, kPartThreads, entry_bytes(a.k),
-                  st, a);
+    if (grad ? s.rows_loss_grad : s.rows_loss)
+        return grad ? distill_rows<T, TM, true>(a, st) : distill_rows<T, TM, false>(a, st);
+    return s.hold == kDistillHold ? distill_loss_parts<T, TM, kDistillHold>(a, grad, st)
+                                  : distill_loss_parts<T, TM, kDistillFewHold>(a, grad, st);
+}
+
+template <typename T, Terms TM>
+int distill_grad_t(const DistillArgs& a, const DistillShape& s, hipStream_t st)
+{
+    const int64_t parts = a.rows * a.splits;
+    const size_t lds = entry_bytes(a.k);
+    return s.hold == kDistillHold
+               ? launch(k_distill_grad<T, TM, kDistillHold, true>, parts, kPartThreads, lds, st, a)
+               : launch(k_distill_grad<T, TM, kDistillFewHold, true>, parts, kPartThreads, lds, st,
+                        a);
 }
 
 // f(type tag, terms) for the call's element type and softmaxes.
@@ -1300,13 +1344,6 @@ int by_type(const DistillArgs& a, F f)
         }
     };
     return a.f32 ? typed(float{}) : typed(uint16_t{});
-}
-
-// Parts of whole vectors (of either element type).
-int64_t part_columns(int64_t vocab, int32_t splits)
-{
-    const int64_t cols = (vocab + splits - 1) / splits;
-    return (cols + 7) / 8 * 8;
 }
 
 }  // namespace
@@ -1361,12 +1398,13 @@ int enqueue_distill_loss(DistillArgs a, bool with_grad, void* stream)
 {
     hipStream_t st = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
-    a.splits = distill_splits(a.rows, a.vocab);
-    a.part_cols = part_columns(a.vocab, a.splits);
+    const DistillShape s = distill_shape(a.rows, a.vocab, a.f32);
+    a.splits = s.splits;
+    a.part_cols = s.part_cols;
     int rc = ZS_OK;
     if (a.rows > 0)
         rc = by_type(a, [&](auto tag, auto terms) {
-            return distill_loss_t<decltype(tag), decltype(terms)::value>(a, with_grad, st);
+            return distill_loss_t<decltype(tag), decltype(terms)::value>(a, s, with_grad, st);
         });
     if (rc != ZS_OK || (!a.loss_sum && !a.counted)) return rc;
     hipLaunchKernelGGL(k_distill_total, dim3(1), dim3(kTotalThreads), 0, st, a);
@@ -1378,10 +1416,11 @@ int enqueue_distill_grad(DistillArgs a, void* stream)
     hipStream_t st = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
     if (a.rows == 0) return ZS_OK;
-    a.splits = distill_splits(a.rows, a.vocab);
-    a.part_cols = part_columns(a.vocab, a.splits);
+    const DistillShape s = distill_shape(a.rows, a.vocab, a.f32);
+    a.splits = s.splits;
+    a.part_cols = s.part_cols;
     return by_type(a, [&](auto tag, auto terms) {
-        return distill_grad_t<decltype(tag), decltype(terms)::value>(a, st);
+        return distill_grad_t<decltype(tag), decltype(terms)::value>(a, s, st);
     });
 }
 

@@ -176,10 +176,15 @@ def test_distill_pointers_are_refused():
     assert _dgrad(_distill(alpha=1.0), t=_t(labels=None), lse=None) == Z.ZS_ENULL
 
 
-def test_distill_workspace_grows_with_rows_until_they_fill_the_gpu():
-    for rows in (0, 1, 2, 100, 511, 512, 8192):
-        for vocab in (1, 4096, 4097, 128256):
-            n = Z.zs_distill_workspace_bytes(Z.make_distill(rows, vocab, 64))
-            assert n >= max(256, 4 * rows) and n % 256 == 0
-            if rows >= 512:
-                assert n <= 4 * rows + 512
+def test_distill_workspace_covers_its_parts():
+    """A flag a row; 16 bytes a part where the loss runs in parts; the logits
+    at the entries where loss and gradient do."""
+    for dtype, vector in ((Z.ZS_BF16, 8), (Z.ZS_F32, 4)):
+        for rows in (0, 1, 2, 100, 511, 512, 8192):
+            for vocab in (1, 4096, 4097, 16385, 50257, 128256):
+                n = Z.zs_distill_workspace_bytes(
+                    Z.make_distill(rows, vocab, 64, logits_dtype=dtype))
+                most = 4 * rows + 16 * rows * -(-vocab // (512 * vector)) + 4 * 65 * rows + 1024
+                assert max(256, 4 * rows) <= n <= most and n % 256 == 0
+                if vocab <= 512 * vector:
+                    assert n <= 4 * rows + 256
