@@ -101,6 +101,27 @@ __device__ __forceinline__ void store_n(float* p, const float v[N])
         *reinterpret_cast<f32x4_u*>(p + i) = f32x4_u{v[i], v[i + 1], v[i + 2], v[i + 3]};
 }
 
+// The same past the caches' reuse: rows that are not read again soon.
+template <int N>
+__device__ __forceinline__ void store_nt(uint16_t* p, const float v[N])
+{
+    if constexpr (N == 8)
+        __builtin_nontemporal_store(u32x4_u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])},
+                                    reinterpret_cast<u32x4_u*>(p));
+    else
+        __builtin_nontemporal_store(u32x2_u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])},
+                                    reinterpret_cast<u32x2_u*>(p));
+}
+template <int N>
+__device__ __forceinline__ void store_nt(float* p, const float v[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+        __builtin_nontemporal_store(f32x4_u{v[i], v[i + 1], v[i + 2], v[i + 3]},
+                                    reinterpret_cast<f32x4_u*>(p + i));
+}
+
 // Subtracting in 64 bits without a sign: an id below first gives a number
 // above every row count.
 __device__ __forceinline__ uint64_t row_of_id(int64_t id, int64_t first)
@@ -117,6 +138,7 @@ __device__ __forceinline__ int64_t read_id(const void* ids, int id64, int64_t i)
 // ---- embedding lookup -------------------------------------------------------------
 
 constexpr int kEmbedThreads = 256;
+constexpr int64_t kClearBytes = 65536;
 
 // Lanes (a power of two, as a shift) that share one row of `dim` elements at
 // n a lane, `most` at most.
@@ -127,45 +149,56 @@ int lane_shift(int64_t dim, int n, int most)
     return s;
 }
 
-// 1 << shift lanes take one token each time; a block takes 256 >> shift.
-template <typename TT, typename AT, int N>
+// 1 << shift lanes take one token; a block takes 256 >> shift.  A lane has
+// TURNS loads under way (a row of 4096 bf16 is two turns of a block).
+template <typename TT, typename AT, int N, int TURNS>
 __global__ void __launch_bounds__(kEmbedThreads)
     k_embed_lookup(EmbedArgs a, int shift, int64_t b0)
 {
     const int64_t t = ((b0 + blockIdx.x) << (8 - shift)) + (threadIdx.x >> shift);
     if (t >= a.tokens) return;
-    const int lanes = 1 << shift;
+    const int64_t step = static_cast<int64_t>(N) << shift;
     const uint64_t row = row_of_id(read_id(a.ids, a.id64, t), a.first_row);
     const bool here = row < static_cast<uint64_t>(a.rows);
     const TT* src = static_cast<const TT*>(a.src) + (here ? row * a.table_pitch : 0);
     AT* dst = static_cast<AT*>(a.dst) + t * a.act_pitch;
-    for (int64_t c = static_cast<int64_t>(threadIdx.x & (lanes - 1)) * N; c < a.dim;
-         c += static_cast<int64_t>(lanes) * N) {
-        if (c + N <= a.dim) {
-            float v[N];
-            if (here) {
-                load_n<N>(src + c, v);
+    for (int64_t c0 = static_cast<int64_t>(threadIdx.x & ((1 << shift) - 1)) * N; c0 < a.dim;
+         c0 += step * TURNS) {
+        float v[TURNS][N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) v[i] *= a.scale;
+        for (int u = 0; u < TURNS; ++u) {
+            const int64_t c = c0 + u * step;
+            if (here && c + N <= a.dim) {
+                load_n<N>(src + c, v[u]);
             } else {
 #pragma unroll
-                for (int i = 0; i < N; ++i) v[i] = 0.0f;
+                for (int i = 0; i < N; ++i) v[u][i] = 0.0f;
             }
-            store_n<N>(dst + c, v);
-        } else {
-            for (int64_t i = c; i < a.dim; ++i)
-                put(dst + i, here ? widen(src[i]) * a.scale : 0.0f);
+        }
+#pragma unroll
+        for (int u = 0; u < TURNS; ++u) {
+            const int64_t c = c0 + u * step;
+            if (c + N <= a.dim) {
+                if (here) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) v[u][i] *= a.scale;
+                }
+                store_nt<N>(dst + c, v[u]);
+            } else {
+                for (int64_t i = c; i < a.dim; ++i)
+                    put(dst + i, here ? widen(src[i]) * a.scale : 0.0f);
+            }
         }
     }
 }
 
 // ---- embedding gradient: sort -----------------------------------------------------
 
-constexpr int kSortThreads = 1024;
-constexpr int kSortWaves = kSortThreads / kWave;
 constexpr int kSortRows = 960;      // rows of one bucket at most: the counts of 16
                                     // waves and the sums fit 64 KB of LDS
 constexpr int kSortBuckets = 256;   // buckets at least (one per CU), rows permitting
+constexpr int kSortLoads = 8;       // ids a lane has under way
+constexpr int64_t kSortFewTokens = 4096;
 
 struct SortShape {
     int64_t buckets;
@@ -206,49 +239,68 @@ __device__ __forceinline__ uint64_t same_row(bool in, int row, int bits)
 // contiguous part of the tokens, so a token's place is: the row's start, the
 // tokens of that row in earlier waves, those in earlier turns of its wave,
 // and those in lower lanes.
-__global__ void __launch_bounds__(kSortThreads)
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS)
     k_embed_sort(EmbedArgs a, SortShape s, int32_t* order, int32_t* row_of, int32_t* starts)
 {
-    __shared__ int32_t hist[kSortWaves][kSortRows];
-    __shared__ int32_t wave_sum[kSortWaves];
-    __shared__ int32_t wave_below[kSortWaves];
+    constexpr int WAVES = THREADS / kWave;
+    __shared__ int32_t hist[WAVES][kSortRows];
+    __shared__ int32_t wave_sum[WAVES];
+    __shared__ int32_t wave_below[WAVES];
     const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
     // this bucket's rows: [lo, lo + here)
     const uint64_t lo = static_cast<uint64_t>(blockIdx.x) * s.rows;
     const uint64_t rows = a.rows;
     const uint32_t here = rows - lo < s.rows ? static_cast<uint32_t>(rows - lo) : s.rows;
-    for (int w = 0; w < kSortWaves; ++w)
-        for (uint32_t r = tid; r < here; r += kSortThreads) hist[w][r] = 0;
-    __syncthreads();
-
     const int tokens = static_cast<int>(a.tokens);
-    const int turns = (tokens + kSortThreads - 1) / kSortThreads;   // of one wave
-    const int t0 = wave * turns * kWave;
+    constexpr int kSpan = kSortLoads * kWave;
+    // tokens of one wave, a multiple of kSpan
+    const int part = (tokens + WAVES * kSpan - 1) / (WAVES * kSpan) * kSpan;
+    const int t0 = wave * part, t1 = t0 + part < tokens ? t0 + part : tokens;
     const uint64_t lower = (uint64_t(1) << lane) - 1;
+    const auto rows_at = [&](int base, uint64_t (&row)[kSortLoads]) {
+#pragma unroll
+        for (int u = 0; u < kSortLoads; ++u) {
+            const int t = base + u * kWave + lane;
+            row[u] = t < t1 ? row_of_id(read_id(a.ids, a.id64, t), a.first_row) : UINT64_MAX;
+        }
+    };
+    for (uint32_t r = lane; r < here; r += kWave) hist[wave][r] = 0;
+
     int below = 0;
-    for (int i = 0; i < turns; ++i) {
-        const int t = t0 + i * kWave + lane;
-        uint64_t row = UINT64_MAX;
-        if (t < tokens) row = row_of_id(read_id(a.ids, a.id64, t), a.first_row);
-        below += row < lo;
-        const bool in = row - lo < here;
-        const int r = static_cast<int>(row - lo);
-        if (__ballot(in) == 0) continue;
-        const uint64_t same = same_row(in, r, s.bits);
-        if (in && (same & lower) == 0) hist[wave][r] += __popcll(same);
+    for (int base = t0; base < t1; base += kSpan) {
+        uint64_t row[kSortLoads];
+        rows_at(base, row);
+#pragma unroll
+        for (int u = 0; u < kSortLoads; ++u) {
+            below += row[u] < lo;
+            const bool in = row[u] - lo < here;
+            if (__ballot(in) == 0) continue;
+            const int r = static_cast<int>(row[u] - lo);
+            const uint64_t same = same_row(in, r, s.bits);
+            // lanes of one wave: in order
+            if (in && (same & lower) == 0) hist[wave][r] += __popcll(same);
+        }
     }
     for (int o = kWave / 2; o > 0; o >>= 1) below += __shfl_xor(below, o);
     if (lane == 0) wave_below[wave] = below;
     __syncthreads();
 
-    // per row: counts of earlier waves, then the row's start in the bucket
-    int total = 0;
-    if (tid < static_cast<int>(here)) {
-        for (int w = 0; w < kSortWaves; ++w) {
-            const int n = hist[w][tid];
-            hist[w][tid] = total;
-            total += n;
+    // per row: the tokens of earlier waves, and the row's start in the bucket
+    // (a thread takes up to four consecutive rows)
+    constexpr int kRows = (kSortRows + THREADS - 1) / THREADS;
+    int count[kRows], total = 0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const uint32_t r = tid * kRows + i;
+        count[i] = 0;
+        if (r >= here) continue;
+        for (int w = 0; w < WAVES; ++w) {
+            const int n = hist[w][r];
+            hist[w][r] = count[i];
+            count[i] += n;
         }
+        total += count[i];
     }
     int incl = total;
     for (int o = 1; o < kWave; o <<= 1) {
@@ -257,37 +309,43 @@ __global__ void __launch_bounds__(kSortThreads)
     }
     if (lane == kWave - 1) wave_sum[wave] = incl;
     __syncthreads();
-    int base = incl - total;
-    for (int w = 0; w < kSortWaves; ++w) {
-        base += wave_below[w];
-        if (w < wave) base += wave_sum[w];
+    int start = incl - total;
+    for (int w = 0; w < WAVES; ++w) {
+        start += wave_below[w];
+        if (w < wave) start += wave_sum[w];
     }
-    if (tid < static_cast<int>(here)) {
-        starts[lo + tid] = base;
-        if (lo + tid == rows - 1) starts[rows] = base + total;
-        for (int w = 0; w < kSortWaves; ++w) hist[w][tid] += base;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const uint32_t r = tid * kRows + i;
+        if (r >= here) continue;
+        starts[lo + r] = start;
+        for (int w = 0; w < WAVES; ++w) hist[w][r] += start;
+        start += count[i];
+        if (lo + r == rows - 1) starts[rows] = start;
     }
     __syncthreads();
 
-    for (int i = 0; i < turns; ++i) {
-        const int t = t0 + i * kWave + lane;
-        uint64_t row = UINT64_MAX;
-        if (t < tokens) row = row_of_id(read_id(a.ids, a.id64, t), a.first_row);
-        const bool in = row - lo < here;
-        const int r = static_cast<int>(row - lo);
-        if (__ballot(in) == 0) continue;
-        const uint64_t same = same_row(in, r, s.bits);
-        int first = 0;
-        if (in) first = hist[wave][r];
-        // every lane has read before the first lane of each row adds
-        __builtin_amdgcn_wave_barrier();
-        if (in) {
-            const int before = __popcll(same & lower);
-            if (before == 0) hist[wave][r] = first + __popcll(same);
-            order[first + before] = t;
-            row_of[first + before] = static_cast<int32_t>(row);
+    for (int base = t0; base < t1; base += kSpan) {
+        uint64_t row[kSortLoads];
+        rows_at(base, row);
+#pragma unroll
+        for (int u = 0; u < kSortLoads; ++u) {
+            const bool in = row[u] - lo < here;
+            if (__ballot(in) == 0) continue;
+            const int r = static_cast<int>(row[u] - lo);
+            const uint64_t same = same_row(in, r, s.bits);
+            int first = 0;
+            if (in) first = hist[wave][r];
+            // every lane has read before the first lane of each row adds
+            __builtin_amdgcn_wave_barrier();
+            if (in) {
+                const int before = __popcll(same & lower);
+                if (before == 0) hist[wave][r] = first + __popcll(same);
+                order[first + before] = base + u * kWave + lane;
+                row_of[first + before] = static_cast<int32_t>(row[u]);
+            }
+            __builtin_amdgcn_wave_barrier();
         }
-        __builtin_amdgcn_wave_barrier();
     }
 }
 
@@ -305,6 +363,7 @@ struct SumPlan {
     int32_t chunk;          // sorted positions of a chunk
     int32_t shift;          // log2 of the lanes of one column part
     int32_t zero_shift;     // log2 of the lanes that clear one row
+    int32_t zero_rows;      // rows a block looks through, at most 64
 };
 
 // scale * acc into the gradient row (added to it if ADD).
@@ -342,6 +401,33 @@ __device__ __forceinline__ void put_partial(float* p, int64_t c, int64_t dim, co
     }
 }
 
+// One block: +0 into those of zero_rows consecutive rows that have no tokens.
+template <typename GT>
+__device__ __forceinline__ void clear_rows(const EmbedArgs& a, const SumPlan& p, int64_t block)
+{
+    constexpr int N = 16 / sizeof(GT);
+    const int64_t r0 = block * p.zero_rows;
+    const int lane = threadIdx.x % kWave;
+    bool empty = false;
+    if (lane < p.zero_rows && r0 + lane < a.rows)
+        empty = p.starts[r0 + lane] == p.starts[r0 + lane + 1];
+    const uint64_t mask = __ballot(empty);
+    const int lanes = 1 << p.zero_shift;
+    const float z[N] = {};
+    for (int i = threadIdx.x >> p.zero_shift; i < p.zero_rows; i += kEmbedThreads >> p.zero_shift) {
+        if (!(mask >> i & 1)) continue;
+        GT* g = static_cast<GT*>(a.dst) + (r0 + i) * a.table_pitch;
+        for (int64_t c = static_cast<int64_t>(threadIdx.x & (lanes - 1)) * N; c < a.dim;
+             c += static_cast<int64_t>(lanes) * N) {
+            if (c + N <= a.dim) {
+                store_nt<N>(g + c, z);
+            } else {
+                for (int64_t j = c; j < a.dim; ++j) put(g + j, 0.0f);
+            }
+        }
+    }
+}
+
 constexpr int kSumUnroll = 8;   // divides every embed_chunk
 
 // One worker (1 << shift lanes) sums one chunk of sorted positions over one
@@ -353,20 +439,7 @@ __global__ void __launch_bounds__(kEmbedThreads)
 {
     const int64_t block = b0 + blockIdx.x;
     if (!ADD && block >= p.sum_blocks) {
-        const int64_t row = ((block - p.sum_blocks) << (8 - p.zero_shift)) +
-                            (threadIdx.x >> p.zero_shift);
-        if (row >= a.rows || p.starts[row] != p.starts[row + 1]) return;
-        const int lanes = 1 << p.zero_shift;
-        GT* g = static_cast<GT*>(a.dst) + row * a.table_pitch;
-        const float z[N] = {};
-        for (int64_t c = static_cast<int64_t>(threadIdx.x & (lanes - 1)) * N; c < a.dim;
-             c += static_cast<int64_t>(lanes) * N) {
-            if (c + N <= a.dim) {
-                store_n<N>(g + c, z);
-            } else {
-                for (int64_t i = c; i < a.dim; ++i) put(g + i, 0.0f);
-            }
-        }
+        clear_rows<GT>(a, p, block - p.sum_blocks);
         return;
     }
     const int64_t worker = (block << (8 - p.shift)) + (threadIdx.x >> p.shift);
@@ -1257,8 +1330,11 @@ int lookup(const EmbedArgs& a, hipStream_t st)
 {
     const int shift = lane_shift(a.dim, N, 8);
     const int64_t per = kEmbedThreads >> shift;
-    return launch(k_embed_lookup<TT, AT, N>, (a.tokens + per - 1) / per, kEmbedThreads, 0, st, a,
-                  shift);
+    const int64_t blocks = (a.tokens + per - 1) / per;
+    // rows of one turn, or of several
+    return a.dim <= N * kEmbedThreads
+               ? launch(k_embed_lookup<TT, AT, N, 1>, blocks, kEmbedThreads, 0, st, a, shift)
+               : launch(k_embed_lookup<TT, AT, N, 4>, blocks, kEmbedThreads, 0, st, a, shift);
 }
 
 template <typename AT, typename GT, bool ADD>
@@ -1266,12 +1342,15 @@ int embed_sums(const EmbedArgs& a, SumPlan p, hipStream_t st)
 {
     constexpr int N = 16 / sizeof(AT);      // one 16-byte load of activations a lane
     p.shift = lane_shift(a.dim, N, 6);
-    p.zero_shift = lane_shift(a.dim, N, 8);
+    p.zero_shift = lane_shift(a.dim, 16 / sizeof(GT), 8);
+    // about 64 KB to clear a block
+    const int64_t zr = kClearBytes / (a.dim * static_cast<int64_t>(sizeof(GT)));
+    p.zero_rows = static_cast<int32_t>(zr < 1 ? 1 : (zr > kWave ? kWave : zr));
     const int64_t cols = static_cast<int64_t>(N) << p.shift;
     p.splits = (a.dim + cols - 1) / cols;
-    const int64_t per = kEmbedThreads >> p.shift, zero_per = kEmbedThreads >> p.zero_shift;
+    const int64_t per = kEmbedThreads >> p.shift;
     p.sum_blocks = (p.chunks * p.splits + per - 1) / per;
-    const int64_t zero_blocks = ADD ? 0 : (a.rows + zero_per - 1) / zero_per;
+    const int64_t zero_blocks = ADD ? 0 : (a.rows + p.zero_rows - 1) / p.zero_rows;
     int rc = launch(k_embed_sum<AT, GT, N, ADD>, p.sum_blocks + zero_blocks, kEmbedThreads, 0, st,
                     a, p);
     if (rc != ZS_OK || p.chunks <= 1) return rc;
@@ -1376,10 +1455,15 @@ int enqueue_embed_grad(const EmbedArgs& a, bool accumulate, void* workspace, voi
     int32_t* row_of = reinterpret_cast<int32_t*>(base + w.row_of);
     int32_t* starts = reinterpret_cast<int32_t*>(base + w.starts);
     const SortShape s = sort_shape(a.rows);
-    hipLaunchKernelGGL(k_embed_sort, dim3(static_cast<uint32_t>(s.buckets)), dim3(kSortThreads), 0,
-                       st, a, s, order, row_of, starts);
-    const int rc = launched();
-    if (rc != ZS_OK) return rc;
+    // blocks of 4 waves while a wave's part of the tokens is short
+    int rc;
+    if (a.tokens <= kSortFewTokens)
+        hipLaunchKernelGGL(k_embed_sort<256>, dim3(static_cast<uint32_t>(s.buckets)), dim3(256), 0,
+                           st, a, s, order, row_of, starts);
+    else
+        hipLaunchKernelGGL(k_embed_sort<1024>, dim3(static_cast<uint32_t>(s.buckets)), dim3(1024),
+                           0, st, a, s, order, row_of, starts);
+    if ((rc = launched()) != ZS_OK) return rc;
     SumPlan p{};
     p.order = order;
     p.row_of = row_of;
