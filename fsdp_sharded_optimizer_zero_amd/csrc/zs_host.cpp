@@ -92,7 +92,7 @@ EmbedSpace embed_space(int64_t tokens, int64_t rows, int64_t dim)
     w.order = 0;
     w.row_of = w.order + round_up(tokens * 4, 256);
     w.starts = w.row_of + round_up(tokens * 4, 256);
-    w.partials = w.starts + round_up((rows + 1) * 4, 256);
+    w.partials = w.starts + round_up((embed_slots(rows) + 1) * 4, 256);
     // one chunk has no run that crosses into another
     const int64_t chunks = embed_chunks(tokens);
     w.bytes = w.partials + (chunks > 1 ? round_up(chunks * 2 * dim * 4, 256) : 0);

@@ -144,11 +144,37 @@ inline int64_t embed_chunks(int64_t tokens)
     return (tokens + c - 1) / c;
 }
 
+// The sort deals the rows to a power of two of buckets, at least kSortBuckets
+// (rows permitting) and so many that none has more than kSortRows; the slots
+// are the rows' places in the sorted order, a whole number per bucket.
+constexpr int kSortRows = 512;
+constexpr int kSortBuckets = 256;
+struct SortShape {
+    int32_t bucket_bits;    // log2 of the buckets
+    int32_t rows;           // rows of a bucket
+    int32_t row_bits;       // bits of a row's number in its bucket
+};
+inline SortShape sort_shape(int64_t rows)
+{
+    SortShape s{0, 0, 0};
+    while ((int64_t(1) << s.bucket_bits) < kSortBuckets && (int64_t(1) << s.bucket_bits) < rows)
+        ++s.bucket_bits;
+    while ((rows - 1) >> s.bucket_bits >= kSortRows) ++s.bucket_bits;
+    s.rows = static_cast<int32_t>(((rows - 1) >> s.bucket_bits) + 1);
+    while ((1 << s.row_bits) < s.rows) ++s.row_bits;
+    return s;
+}
+inline int64_t embed_slots(int64_t rows)
+{
+    const SortShape s = sort_shape(rows);
+    return static_cast<int64_t>(s.rows) << s.bucket_bits;
+}
+
 // Workspace of embed_grad, in bytes from its start.
 struct EmbedSpace {
     int64_t order;     // int32[tokens]: token positions sorted by row
     int64_t row_of;    // int32[tokens]: their rows
-    int64_t starts;    // int32[rows + 1]: first sorted position of each row
+    int64_t starts;    // int32[slots + 1]: first sorted position of each slot
     int64_t partials;  // fp32[chunks][2][dim]
     int64_t bytes;
 };

@@ -194,27 +194,17 @@ __global__ void __launch_bounds__(kEmbedThreads)
 
 // ---- embedding gradient: sort -----------------------------------------------------
 
-constexpr int kSortRows = 960;      // rows of one bucket at most: the counts of 16
-                                    // waves and the sums fit 64 KB of LDS
-constexpr int kSortBuckets = 256;   // buckets at least (one per CU), rows permitting
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / kWave;
+// kSortRows: the counts of 16 waves and their queues take 48 KB of LDS.
 constexpr int kSortLoads = 8;       // ids a lane has under way
-constexpr int64_t kSortFewTokens = 4096;
 
-struct SortShape {
-    int64_t buckets;
-    uint32_t rows;      // rows of a bucket
-    int32_t bits;       // bits of a row number inside a bucket
-};
-SortShape sort_shape(int64_t rows)
+// Rows are dealt to buckets in turn (bucket = row mod buckets), because the
+// rows of small numbers tend to have most of the tokens.  The sorted order is
+// by bucket, then by row; a row's slot is its place in it.
+__device__ __forceinline__ int64_t sort_slot(const SortShape& s, int64_t row)
 {
-    SortShape s;
-    s.buckets = rows < kSortBuckets ? rows : kSortBuckets;
-    if (rows > s.buckets * kSortRows) s.buckets = (rows + kSortRows - 1) / kSortRows;
-    s.rows = static_cast<uint32_t>((rows + s.buckets - 1) / s.buckets);
-    s.buckets = (rows + s.rows - 1) / s.rows;
-    s.bits = 0;
-    while ((1u << s.bits) < s.rows) ++s.bits;
-    return s;
+    return (row & ((int64_t(1) << s.bucket_bits) - 1)) * s.rows + (row >> s.bucket_bits);
 }
 
 // Lanes of the wave whose row equals this lane's, among those with `in`
@@ -231,76 +221,88 @@ __device__ __forceinline__ uint64_t same_row(bool in, int row, int bits)
     return m;
 }
 
-// A stable counting sort of the tokens by row, one block per bucket of
-// consecutive rows and no exchange between blocks: every block reads all ids
-// (a batch of ids is small and comes from L2 after the first block), counts
-// the tokens of earlier buckets (where its own part of the order begins) and
-// of each of its rows, and then places its tokens.  Each wave takes one
-// contiguous part of the tokens, so a token's place is: the row's start, the
-// tokens of that row in earlier waves, those in earlier turns of its wave,
-// and those in lower lanes.
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS)
+// A stable counting sort of the tokens by slot, one block per bucket and no
+// exchange between blocks: every block reads all ids (a batch of ids is small
+// and comes from L2 after the first block), counts the tokens of earlier
+// buckets (where its own part of the order begins) and of each of its rows,
+// and then places its tokens.  Each wave takes one contiguous part of the
+// tokens; those of the bucket, few of each 64, are queued and handled 64 at a
+// time.  A token's place is: its row's start, the tokens of that row in
+// earlier waves, those handled earlier by its wave, and those in lower lanes.
+__global__ void __launch_bounds__(kSortThreads)
     k_embed_sort(EmbedArgs a, SortShape s, int32_t* order, int32_t* row_of, int32_t* starts)
 {
-    constexpr int WAVES = THREADS / kWave;
-    __shared__ int32_t hist[WAVES][kSortRows];
-    __shared__ int32_t wave_sum[WAVES];
-    __shared__ int32_t wave_below[WAVES];
+    __shared__ int32_t hist[kSortWaves][kSortRows];
+    __shared__ int2 queue[kSortWaves][2 * kWave];   // (token, row in the bucket)
+    __shared__ int32_t wave_sum[kSortWaves];
+    __shared__ int32_t wave_below[kSortWaves];
     const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
-    // this bucket's rows: [lo, lo + here)
-    const uint64_t lo = static_cast<uint64_t>(blockIdx.x) * s.rows;
-    const uint64_t rows = a.rows;
-    const uint32_t here = rows - lo < s.rows ? static_cast<uint32_t>(rows - lo) : s.rows;
+    const uint32_t bucket = blockIdx.x, low = (1u << s.bucket_bits) - 1;
     const int tokens = static_cast<int>(a.tokens);
     constexpr int kSpan = kSortLoads * kWave;
-    // tokens of one wave, a multiple of kSpan
-    const int part = (tokens + WAVES * kSpan - 1) / (WAVES * kSpan) * kSpan;
+    // tokens of one wave, a multiple of 64
+    const int part = (tokens + kSortThreads - 1) / kSortThreads * kWave;
     const int t0 = wave * part, t1 = t0 + part < tokens ? t0 + part : tokens;
     const uint64_t lower = (uint64_t(1) << lane) - 1;
-    const auto rows_at = [&](int base, uint64_t (&row)[kSortLoads]) {
-#pragma unroll
-        for (int u = 0; u < kSortLoads; ++u) {
-            const int t = base + u * kWave + lane;
-            row[u] = t < t1 ? row_of_id(read_id(a.ids, a.id64, t), a.first_row) : UINT64_MAX;
-        }
-    };
-    for (uint32_t r = lane; r < here; r += kWave) hist[wave][r] = 0;
+    for (int r = lane; r < s.rows; r += kWave) hist[wave][r] = 0;
 
+    // handle(n): the first n queued tokens, one a lane
     int below = 0;
-    for (int base = t0; base < t1; base += kSpan) {
-        uint64_t row[kSortLoads];
-        rows_at(base, row);
+    const auto walk = [&](auto handle) {
+        int queued = 0;
+        for (int base = t0; base < t1; base += kSpan) {
+            uint32_t row[kSortLoads];
 #pragma unroll
-        for (int u = 0; u < kSortLoads; ++u) {
-            below += row[u] < lo;
-            const bool in = row[u] - lo < here;
-            if (__ballot(in) == 0) continue;
-            const int r = static_cast<int>(row[u] - lo);
-            const uint64_t same = same_row(in, r, s.bits);
-            // lanes of one wave: in order
-            if (in && (same & lower) == 0) hist[wave][r] += __popcll(same);
+            for (int u = 0; u < kSortLoads; ++u) {
+                const int t = base + u * kWave + lane;
+                uint64_t r = UINT64_MAX;
+                if (t < t1) r = row_of_id(read_id(a.ids, a.id64, t), a.first_row);
+                row[u] = r < static_cast<uint64_t>(a.rows) ? static_cast<uint32_t>(r) : UINT32_MAX;
+            }
+#pragma unroll
+            for (int u = 0; u < kSortLoads; ++u) {
+                const bool here = row[u] != UINT32_MAX;
+                below += here && (row[u] & low) < bucket;
+                const bool in = here && (row[u] & low) == bucket;
+                const uint64_t mask = __ballot(in);
+                if (mask == 0) continue;
+                if (in)
+                    queue[wave][queued + __popcll(mask & lower)] =
+                        int2{base + u * kWave + lane, static_cast<int>(row[u] >> s.bucket_bits)};
+                queued += __popcll(mask);
+                __builtin_amdgcn_wave_barrier();
+                if (queued >= kWave) {
+                    handle(kWave);
+                    queued -= kWave;
+                    const int2 rest = queue[wave][kWave + lane];
+                    __builtin_amdgcn_wave_barrier();
+                    if (lane < queued) queue[wave][lane] = rest;
+                    __builtin_amdgcn_wave_barrier();
+                }
+            }
         }
-    }
+        if (queued > 0) handle(queued);
+    };
+    walk([&](int n) {
+        const int r = queue[wave][lane].y;
+        const uint64_t same = same_row(lane < n, r, s.row_bits);
+        if (lane < n && (same & lower) == 0) hist[wave][r] += __popcll(same);
+    });
     for (int o = kWave / 2; o > 0; o >>= 1) below += __shfl_xor(below, o);
     if (lane == 0) wave_below[wave] = below;
     __syncthreads();
 
-    // per row: the tokens of earlier waves, and the row's start in the bucket
-    // (a thread takes up to four consecutive rows)
-    constexpr int kRows = (kSortRows + THREADS - 1) / THREADS;
-    int count[kRows], total = 0;
+    // per row: the tokens of earlier waves, and the row's start
+    int total = 0;
+    if (tid < s.rows) {
+        int n[kSortWaves];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const uint32_t r = tid * kRows + i;
-        count[i] = 0;
-        if (r >= here) continue;
-        for (int w = 0; w < WAVES; ++w) {
-            const int n = hist[w][r];
-            hist[w][r] = count[i];
-            count[i] += n;
+        for (int w = 0; w < kSortWaves; ++w) n[w] = hist[w][tid];
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) {
+            hist[w][tid] = total;
+            total += n[w];
         }
-        total += count[i];
     }
     int incl = total;
     for (int o = 1; o < kWave; o <<= 1) {
@@ -310,43 +312,34 @@ __global__ void __launch_bounds__(THREADS)
     if (lane == kWave - 1) wave_sum[wave] = incl;
     __syncthreads();
     int start = incl - total;
-    for (int w = 0; w < WAVES; ++w) {
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
         start += wave_below[w];
         if (w < wave) start += wave_sum[w];
     }
+    if (tid < s.rows) {
+        starts[bucket * s.rows + tid] = start;
+        if (bucket == low && tid == s.rows - 1) starts[(low + 1) * s.rows] = start + total;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const uint32_t r = tid * kRows + i;
-        if (r >= here) continue;
-        starts[lo + r] = start;
-        for (int w = 0; w < WAVES; ++w) hist[w][r] += start;
-        start += count[i];
-        if (lo + r == rows - 1) starts[rows] = start;
+        for (int w = 0; w < kSortWaves; ++w) hist[w][tid] += start;
     }
     __syncthreads();
 
-    for (int base = t0; base < t1; base += kSpan) {
-        uint64_t row[kSortLoads];
-        rows_at(base, row);
-#pragma unroll
-        for (int u = 0; u < kSortLoads; ++u) {
-            const bool in = row[u] - lo < here;
-            if (__ballot(in) == 0) continue;
-            const int r = static_cast<int>(row[u] - lo);
-            const uint64_t same = same_row(in, r, s.bits);
-            int first = 0;
-            if (in) first = hist[wave][r];
-            // every lane has read before the first lane of each row adds
-            __builtin_amdgcn_wave_barrier();
-            if (in) {
-                const int before = __popcll(same & lower);
-                if (before == 0) hist[wave][r] = first + __popcll(same);
-                order[first + before] = base + u * kWave + lane;
-                row_of[first + before] = static_cast<int32_t>(row[u]);
-            }
-            __builtin_amdgcn_wave_barrier();
+    walk([&](int n) {
+        const int2 q = queue[wave][lane];
+        const uint64_t same = same_row(lane < n, q.y, s.row_bits);
+        int first = 0;
+        if (lane < n) first = hist[wave][q.y];
+        // every lane has read before the first lane of each row adds
+        __builtin_amdgcn_wave_barrier();
+        if (lane < n) {
+            const int before = __popcll(same & lower);
+            if (before == 0) hist[wave][q.y] = first + __popcll(same);
+            order[first + before] = q.x;
+            row_of[first + before] = static_cast<int32_t>(q.y << s.bucket_bits | bucket);
         }
-    }
+        __builtin_amdgcn_wave_barrier();
+    });
 }
 
 // ---- embedding gradient: sums -------------------------------------------------------
@@ -354,7 +347,10 @@ __global__ void __launch_bounds__(THREADS)
 struct SumPlan {
     const int32_t* order;
     const int32_t* row_of;
-    const int32_t* starts;
+    const int32_t* starts;  // first sorted position of each slot, and behind
+                            // the last slot, at `count`, the tokens sorted
+    const int32_t* count;
+    SortShape sort;
     float* partials;        // [chunks][2][dim]: a run that began before the
                             // chunk, a run that goes on behind it
     int64_t chunks;
@@ -366,27 +362,34 @@ struct SumPlan {
     int32_t zero_rows;      // rows a block looks through, at most 64
 };
 
-// scale * acc into the gradient row (added to it if ADD).
+// The gradient row's values at columns c.., for ADD.
+template <typename GT, int N>
+__device__ __forceinline__ void read_row(const EmbedArgs& a, int64_t row, int64_t c, float old[N])
+{
+    const GT* g = static_cast<const GT*>(a.dst) + row * a.table_pitch + c;
+    if (c + N <= a.dim) {
+        load_n<N>(g, old);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) old[i] = c + i < a.dim ? widen(g[i]) : 0.0f;
+    }
+}
+
+// scale * acc into the gradient row (with ADD: on top of what it held).
 template <typename GT, int N, bool ADD>
 __device__ __forceinline__ void put_row(const EmbedArgs& a, int64_t row, int64_t c,
-                                        const float acc[N])
+                                        const float acc[N], const float old[N])
 {
     GT* g = static_cast<GT*>(a.dst) + row * a.table_pitch + c;
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = ADD ? old[i] + a.scale * acc[i] : a.scale * acc[i];
     if (c + N <= a.dim) {
-        float v[N];
-        if constexpr (ADD) {
-            load_n<N>(g, v);
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] += a.scale * acc[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = a.scale * acc[i];
-        }
-        store_n<N>(g, v);
+        store_nt<N>(g, v);
     } else {
+#pragma unroll
         for (int i = 0; i < N; ++i)
-            if (c + i < a.dim)
-                put(g + i, ADD ? widen(g[i]) + a.scale * acc[i] : a.scale * acc[i]);
+            if (c + i < a.dim) put(g + i, v[i]);
     }
 }
 
@@ -409,8 +412,10 @@ __device__ __forceinline__ void clear_rows(const EmbedArgs& a, const SumPlan& p,
     const int64_t r0 = block * p.zero_rows;
     const int lane = threadIdx.x % kWave;
     bool empty = false;
-    if (lane < p.zero_rows && r0 + lane < a.rows)
-        empty = p.starts[r0 + lane] == p.starts[r0 + lane + 1];
+    if (lane < p.zero_rows && r0 + lane < a.rows) {
+        const int32_t* s = p.starts + sort_slot(p.sort, r0 + lane);
+        empty = s[0] == s[1];
+    }
     const uint64_t mask = __ballot(empty);
     const int lanes = 1 << p.zero_shift;
     const float z[N] = {};
@@ -430,9 +435,51 @@ __device__ __forceinline__ void clear_rows(const EmbedArgs& a, const SumPlan& p,
 
 constexpr int kSumUnroll = 8;   // divides every embed_chunk
 
+// N elements as loaded: bf16 stays packed until it is added.
+template <typename T, int N>
+struct Pack;
+template <>
+struct Pack<uint16_t, 8> {
+    u32x4 v;
+    __device__ __forceinline__ void load(const uint16_t* p)
+    {
+        v = *reinterpret_cast<const u32x4_u*>(p);
+    }
+    __device__ __forceinline__ void get(float x[8]) const
+    {
+        x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x);
+        x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
+        x[4] = bf16_lo(v.z); x[5] = bf16_hi(v.z);
+        x[6] = bf16_lo(v.w); x[7] = bf16_hi(v.w);
+    }
+    __device__ __forceinline__ void load_part(const uint16_t* p, int n)
+    {
+        const auto at = [&](int i) { return i < n ? static_cast<uint32_t>(p[i]) : 0u; };
+        v = u32x4{at(0) | at(1) << 16, at(2) | at(3) << 16, at(4) | at(5) << 16,
+                  at(6) | at(7) << 16};
+    }
+};
+template <>
+struct Pack<float, 4> {
+    f32x4 v;
+    __device__ __forceinline__ void load(const float* p)
+    {
+        v = *reinterpret_cast<const f32x4_u*>(p);
+    }
+    __device__ __forceinline__ void get(float x[4]) const
+    {
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    }
+    __device__ __forceinline__ void load_part(const float* p, int n)
+    {
+        const auto at = [&](int i) { return i < n ? p[i] : 0.0f; };
+        v = f32x4{at(0), at(1), at(2), at(3)};
+    }
+};
+
 // One worker (1 << shift lanes) sums one chunk of sorted positions over one
 // part of the columns: it walks the positions, kSumUnroll loads in flight,
-// and hands a run's sum on where the row changes.
+// and hands a run's sum on where the run ends or the chunk does.
 template <typename AT, typename GT, int N, bool ADD>
 __global__ void __launch_bounds__(kEmbedThreads)
     k_embed_sum(EmbedArgs a, SumPlan p, int64_t b0)
@@ -446,51 +493,53 @@ __global__ void __launch_bounds__(kEmbedThreads)
     const int64_t chunk = worker / p.splits;
     const int lanes = 1 << p.shift;
     const int64_t c = ((worker - chunk * p.splits) * lanes + (threadIdx.x & (lanes - 1))) * N;
-    const int32_t n = p.starts[a.rows];
-    const int64_t p0 = chunk * p.chunk;
-    if (p0 >= n || c >= a.dim) return;
-    const int64_t p1 = p0 + p.chunk < n ? p0 + p.chunk : n;
+    const int n = *p.count;
+    const int64_t first = chunk * p.chunk;
+    if (first >= n || c >= a.dim) return;
+    const int p0 = static_cast<int>(first), p1 = p0 + p.chunk < n ? p0 + p.chunk : n;
     const AT* src = static_cast<const AT*>(a.src) + c;
-    const bool full = c + N <= a.dim;
+    const int width = c + N <= a.dim ? N : static_cast<int>(a.dim - c);
     float* partial = p.partials + chunk * 2 * a.dim;
 
-    int row = p.row_of[p0];
-    bool began = p0 == 0 || p.row_of[p0 - 1] != row;
+    // whether the run under way began in this chunk
+    bool began = p0 == 0 || p.row_of[p0 - 1] != p.row_of[p0];
     float acc[N] = {};
-    for (int64_t q = p0; q < p1; q += kSumUnroll) {
-        float x[kSumUnroll][N];
-        int rows[kSumUnroll];
+    for (int q = p0; q < p1; q += kSumUnroll) {
+        int row[kSumUnroll + 1];
+        Pack<AT, N> x[kSumUnroll];
+#pragma unroll
+        for (int u = 0; u <= kSumUnroll; ++u) row[u] = q + u < n ? p.row_of[q + u] : -1;
 #pragma unroll
         for (int u = 0; u < kSumUnroll; ++u) {
-            const int64_t at = q + u < p1 ? q + u : p1 - 1;
-            rows[u] = p.row_of[at];
-            const AT* s = src + p.order[at] * a.act_pitch;
-            if (full) {
-                load_n<N>(s, x[u]);
-            } else {
+            const AT* s = src + p.order[q + u < p1 ? q + u : p1 - 1] * a.act_pitch;
+            if (width == N) x[u].load(s);
+            else x[u].load_part(s, width);
+        }
+        float old[ADD ? kSumUnroll : 1][N];
+        if constexpr (ADD) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) x[u][i] = c + i < a.dim ? widen(s[i]) : 0.0f;
-            }
+            for (int u = 0; u < kSumUnroll; ++u)
+                if (q + u < p1 && row[u + 1] != row[u]) read_row<GT, N>(a, row[u], c, old[u]);
         }
 #pragma unroll
         for (int u = 0; u < kSumUnroll; ++u) {
-            if (q + u >= p1) break;
-            if (rows[u] != row) {
-                if (began) put_row<GT, N, ADD>(a, row, c, acc);
-                else put_partial<N>(partial, c, a.dim, acc);
-                row = rows[u];
-                began = true;
+            if (q + u < p1) {
+                float v[N];
+                x[u].get(v);
 #pragma unroll
-                for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+                for (int i = 0; i < N; ++i) acc[i] += v[i];
+                const bool ends = row[u + 1] != row[u];
+                if (ends || q + u + 1 == p1) {
+                    if (!began) put_partial<N>(partial, c, a.dim, acc);
+                    else if (ends) put_row<GT, N, ADD>(a, row[u], c, acc, old[ADD ? u : 0]);
+                    else put_partial<N>(partial + a.dim, c, a.dim, acc);
+                    began = true;
+#pragma unroll
+                    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+                }
             }
-#pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] += x[u][i];
         }
     }
-    const bool ends = p1 >= n || p.row_of[p1] != row;
-    if (!began) put_partial<N>(partial, c, a.dim, acc);
-    else if (ends) put_row<GT, N, ADD>(a, row, c, acc);
-    else put_partial<N>(partial + a.dim, c, a.dim, acc);
 }
 
 // The runs that cross chunks: the block of the chunk a run begins in adds
@@ -502,24 +551,29 @@ __global__ void __launch_bounds__(kEmbedThreads)
     __shared__ float sums[kEmbedThreads * N];
     const int64_t block = b0 + blockIdx.x;
     const int64_t chunk = block / p.splits;
-    const int32_t n = p.starts[a.rows];
+    const int n = *p.count;
     const int64_t p0 = chunk * p.chunk, p1 = p0 + p.chunk;
     if (p1 >= n) return;
     const int32_t row = p.row_of[p1];
-    const int32_t begin = p.starts[row];
-    if (begin < p0 || begin >= p1) return;      // begins in another chunk
-    const int64_t count = (p.starts[row + 1] - 1) / p.chunk - chunk + 1;
+    if (p.row_of[p1 - 1] != row) return;                    // no run crosses here
+    const int32_t* span = p.starts + sort_slot(p.sort, row);
+    if (span[0] < p0) return;                               // it begins in an earlier chunk
+    const int64_t count = (span[1] - 1) / p.chunk - chunk + 1;
     const int lanes = 1 << p.shift, groups = kEmbedThreads >> p.shift;
     const int group = threadIdx.x >> p.shift, lane = threadIdx.x & (lanes - 1);
     const int64_t c = ((block - chunk * p.splits) * lanes + lane) * N;
-    float acc[N] = {};
+    float acc[N] = {}, old[N] = {};
     if (c < a.dim) {
-        for (int64_t i = group * count / groups; i < (group + 1) * count / groups; ++i) {
+        if (ADD && group == 0) read_row<GT, N>(a, row, c, old);
+        const int64_t i0 = group * count / groups, i1 = (group + 1) * count / groups;
+#pragma unroll 4
+        for (int64_t i = i0; i < i1; ++i) {
             const float* s = p.partials + ((chunk + i) * 2 + (i == 0 ? 1 : 0)) * a.dim + c;
             float x[N];
             if (c + N <= a.dim) {
                 load_n<N>(s, x);
             } else {
+#pragma unroll
                 for (int j = 0; j < N; ++j) x[j] = c + j < a.dim ? s[j] : 0.0f;
             }
 #pragma unroll
@@ -531,8 +585,9 @@ __global__ void __launch_bounds__(kEmbedThreads)
     __syncthreads();
     if (group != 0 || c >= a.dim) return;
     for (int g = 1; g < groups; ++g)
+#pragma unroll
         for (int j = 0; j < N; ++j) acc[j] += sums[(g * lanes + lane) * N + j];
-    put_row<GT, N, ADD>(a, row, c, acc);
+    put_row<GT, N, ADD>(a, row, c, acc, old);
 }
 
 // ---- distillation -------------------------------------------------------------------
@@ -1455,19 +1510,17 @@ int enqueue_embed_grad(const EmbedArgs& a, bool accumulate, void* workspace, voi
     int32_t* row_of = reinterpret_cast<int32_t*>(base + w.row_of);
     int32_t* starts = reinterpret_cast<int32_t*>(base + w.starts);
     const SortShape s = sort_shape(a.rows);
-    // blocks of 4 waves while a wave's part of the tokens is short
-    int rc;
-    if (a.tokens <= kSortFewTokens)
-        hipLaunchKernelGGL(k_embed_sort<256>, dim3(static_cast<uint32_t>(s.buckets)), dim3(256), 0,
-                           st, a, s, order, row_of, starts);
-    else
-        hipLaunchKernelGGL(k_embed_sort<1024>, dim3(static_cast<uint32_t>(s.buckets)), dim3(1024),
-                           0, st, a, s, order, row_of, starts);
-    if ((rc = launched()) != ZS_OK) return rc;
+    const int64_t buckets = int64_t(1) << s.bucket_bits;
+    hipLaunchKernelGGL(k_embed_sort, dim3(static_cast<uint32_t>(buckets)), dim3(kSortThreads), 0,
+                       st, a, s, order, row_of, starts);
+    const int rc = launched();
+    if (rc != ZS_OK) return rc;
     SumPlan p{};
     p.order = order;
     p.row_of = row_of;
     p.starts = starts;
+    p.count = starts + buckets * s.rows;
+    p.sort = s;
     p.partials = reinterpret_cast<float*>(base + w.partials);
     p.chunk = embed_chunk(a.tokens);
     p.chunks = embed_chunks(a.tokens);
