@@ -135,10 +135,19 @@ __device__ __forceinline__ int64_t read_id(const void* ids, int id64, int64_t i)
                 : static_cast<int64_t>(static_cast<const int32_t*>(ids)[i]);
 }
 
+// A value all lanes of the wave hold, in a scalar register.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ uint64_t uniform(uint64_t x)
+{
+    const uint64_t lo = static_cast<uint32_t>(uniform(static_cast<int>(x)));
+    const uint64_t hi = static_cast<uint32_t>(uniform(static_cast<int>(x >> 32)));
+    return hi << 32 | lo;
+}
+
 // ---- embedding lookup -------------------------------------------------------------
 
 constexpr int kEmbedThreads = 256;
-constexpr int64_t kClearBytes = 65536;
+constexpr int64_t kClearBytes = 16384;
 
 // Lanes (a power of two, as a shift) that share one row of `dim` elements at
 // n a lane, `most` at most.
@@ -357,7 +366,6 @@ struct SumPlan {
     int64_t splits;         // column parts of a row
     int64_t sum_blocks;     // blocks that sum; the rest clear empty rows
     int32_t chunk;          // sorted positions of a chunk
-    int32_t shift;          // log2 of the lanes of one column part
     int32_t zero_shift;     // log2 of the lanes that clear one row
     int32_t zero_rows;      // rows a block looks through, at most 64
 };
@@ -404,7 +412,8 @@ __device__ __forceinline__ void put_partial(float* p, int64_t c, int64_t dim, co
     }
 }
 
-// One block: +0 into those of zero_rows consecutive rows that have no tokens.
+// One block: +0 into those of zero_rows consecutive rows that have no tokens
+// (plain stores: 2.1 GB and its sums in 375 us, against 398 with nt ones).
 template <typename GT>
 __device__ __forceinline__ void clear_rows(const EmbedArgs& a, const SumPlan& p, int64_t block)
 {
@@ -425,7 +434,7 @@ __device__ __forceinline__ void clear_rows(const EmbedArgs& a, const SumPlan& p,
         for (int64_t c = static_cast<int64_t>(threadIdx.x & (lanes - 1)) * N; c < a.dim;
              c += static_cast<int64_t>(lanes) * N) {
             if (c + N <= a.dim) {
-                store_nt<N>(g + c, z);
+                store_n<N>(g + c, z);
             } else {
                 for (int64_t j = c; j < a.dim; ++j) put(g + j, 0.0f);
             }
@@ -433,7 +442,7 @@ __device__ __forceinline__ void clear_rows(const EmbedArgs& a, const SumPlan& p,
     }
 }
 
-constexpr int kSumUnroll = 8;   // divides every embed_chunk
+constexpr int kSumUnroll = 8;
 
 // N elements as loaded: bf16 stays packed until it is added.
 template <typename T, int N>
@@ -443,7 +452,7 @@ struct Pack<uint16_t, 8> {
     u32x4 v;
     __device__ __forceinline__ void load(const uint16_t* p)
     {
-        v = *reinterpret_cast<const u32x4_u*>(p);
+        v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_u*>(p));
     }
     __device__ __forceinline__ void get(float x[8]) const
     {
@@ -464,7 +473,7 @@ struct Pack<float, 4> {
     f32x4 v;
     __device__ __forceinline__ void load(const float* p)
     {
-        v = *reinterpret_cast<const f32x4_u*>(p);
+        v = __builtin_nontemporal_load(reinterpret_cast<const f32x4_u*>(p));
     }
     __device__ __forceinline__ void get(float x[4]) const
     {
@@ -477,9 +486,10 @@ struct Pack<float, 4> {
     }
 };
 
-// One worker (1 << shift lanes) sums one chunk of sorted positions over one
-// part of the columns: it walks the positions, kSumUnroll loads in flight,
-// and hands a run's sum on where the run ends or the chunk does.
+// One wave sums one chunk of sorted positions over one part of the columns.
+// Its lanes hold the chunk's tokens and rows, one position a lane, which the
+// walk takes into scalar registers one by one: kSumUnroll loads in flight, and
+// a run's sum handed on where the run ends or the chunk does.
 template <typename AT, typename GT, int N, bool ADD>
 __global__ void __launch_bounds__(kEmbedThreads)
     k_embed_sum(EmbedArgs a, SumPlan p, int64_t b0)
@@ -489,61 +499,66 @@ __global__ void __launch_bounds__(kEmbedThreads)
         clear_rows<GT>(a, p, block - p.sum_blocks);
         return;
     }
-    const int64_t worker = (block << (8 - p.shift)) + (threadIdx.x >> p.shift);
+    constexpr int UNROLL = ADD ? kSumUnroll / 2 : kSumUnroll;
+    const int wave = uniform(static_cast<int>(threadIdx.x / kWave)), lane = threadIdx.x % kWave;
+    const int64_t worker = block * (kEmbedThreads / kWave) + wave;
     const int64_t chunk = worker / p.splits;
-    const int lanes = 1 << p.shift;
-    const int64_t c = ((worker - chunk * p.splits) * lanes + (threadIdx.x & (lanes - 1))) * N;
+    const int64_t c = ((worker - chunk * p.splits) * kWave + lane) * N;
     const int n = *p.count;
     const int64_t first = chunk * p.chunk;
-    if (first >= n || c >= a.dim) return;
-    const int p0 = static_cast<int>(first), p1 = p0 + p.chunk < n ? p0 + p.chunk : n;
+    if (first >= n) return;
+    const int p0 = static_cast<int>(first), len = p0 + p.chunk < n ? p.chunk : n - p0;
+    // position p0 + lane (the chunk has at most 64), and the row behind it
+    const int own = lane < len ? lane : len - 1;
+    const int token = p.order[p0 + own], row = p.row_of[p0 + own];
+    const int row_next = p0 + own + 1 < n ? p.row_of[p0 + own + 1] : -1;
+    // whether the run under way began in this chunk
+    bool began = p0 == 0 || p.row_of[p0 - 1] != uniform(row);
+    if (c >= a.dim) return;
     const AT* src = static_cast<const AT*>(a.src) + c;
     const int width = c + N <= a.dim ? N : static_cast<int>(a.dim - c);
     float* partial = p.partials + chunk * 2 * a.dim;
-
-    // whether the run under way began in this chunk
-    bool began = p0 == 0 || p.row_of[p0 - 1] != p.row_of[p0];
     float acc[N] = {};
-    for (int q = p0; q < p1; q += kSumUnroll) {
-        int row[kSumUnroll + 1];
-        Pack<AT, N> x[kSumUnroll];
+    for (int q = 0; q < len; q += UNROLL) {
+        Pack<AT, N> x[UNROLL];
+        float old[ADD ? UNROLL : 1][N];
+        const auto at = [&](int u) { return q + u < len ? q + u : len - 1; };
 #pragma unroll
-        for (int u = 0; u <= kSumUnroll; ++u) row[u] = q + u < n ? p.row_of[q + u] : -1;
-#pragma unroll
-        for (int u = 0; u < kSumUnroll; ++u) {
-            const AT* s = src + p.order[q + u < p1 ? q + u : p1 - 1] * a.act_pitch;
+        for (int u = 0; u < UNROLL; ++u) {
+            const AT* s = src + __builtin_amdgcn_readlane(token, at(u)) * a.act_pitch;
             if (width == N) x[u].load(s);
             else x[u].load_part(s, width);
         }
-        float old[ADD ? kSumUnroll : 1][N];
         if constexpr (ADD) {
 #pragma unroll
-            for (int u = 0; u < kSumUnroll; ++u)
-                if (q + u < p1 && row[u + 1] != row[u]) read_row<GT, N>(a, row[u], c, old[u]);
+            for (int u = 0; u < UNROLL; ++u) {
+                const int r = __builtin_amdgcn_readlane(row, at(u));
+                if (q + u < len && __builtin_amdgcn_readlane(row_next, at(u)) != r)
+                    read_row<GT, N>(a, r, c, old[u]);
+            }
         }
 #pragma unroll
-        for (int u = 0; u < kSumUnroll; ++u) {
-            if (q + u < p1) {
-                float v[N];
-                x[u].get(v);
+        for (int u = 0; u < UNROLL; ++u) {
+            if (q + u >= len) continue;
+            float v[N];
+            x[u].get(v);
 #pragma unroll
-                for (int i = 0; i < N; ++i) acc[i] += v[i];
-                const bool ends = row[u + 1] != row[u];
-                if (ends || q + u + 1 == p1) {
-                    if (!began) put_partial<N>(partial, c, a.dim, acc);
-                    else if (ends) put_row<GT, N, ADD>(a, row[u], c, acc, old[ADD ? u : 0]);
-                    else put_partial<N>(partial + a.dim, c, a.dim, acc);
-                    began = true;
+            for (int i = 0; i < N; ++i) acc[i] += v[i];
+            const int r = __builtin_amdgcn_readlane(row, at(u));
+            const bool ends = __builtin_amdgcn_readlane(row_next, at(u)) != r;
+            if (!ends && q + u + 1 < len) continue;
+            if (!began) put_partial<N>(partial, c, a.dim, acc);
+            else if (ends) put_row<GT, N, ADD>(a, r, c, acc, old[ADD ? u : 0]);
+            else put_partial<N>(partial + a.dim, c, a.dim, acc);
+            began = true;
 #pragma unroll
-                    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
-                }
-            }
+            for (int i = 0; i < N; ++i) acc[i] = 0.0f;
         }
     }
 }
 
 // The runs that cross chunks: the block of the chunk a run begins in adds
-// its partials in order, each group of lanes a contiguous part of them.
+// its partials in order, each wave a contiguous part of them.
 template <typename GT, int N, bool ADD>
 __global__ void __launch_bounds__(kEmbedThreads)
     k_embed_join(EmbedArgs a, SumPlan p, int64_t b0)
@@ -559,8 +574,8 @@ __global__ void __launch_bounds__(kEmbedThreads)
     const int32_t* span = p.starts + sort_slot(p.sort, row);
     if (span[0] < p0) return;                               // it begins in an earlier chunk
     const int64_t count = (span[1] - 1) / p.chunk - chunk + 1;
-    const int lanes = 1 << p.shift, groups = kEmbedThreads >> p.shift;
-    const int group = threadIdx.x >> p.shift, lane = threadIdx.x & (lanes - 1);
+    constexpr int lanes = kWave, groups = kEmbedThreads / kWave;
+    const int group = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const int64_t c = ((block - chunk * p.splits) * lanes + lane) * N;
     float acc[N] = {}, old[N] = {};
     if (c < a.dim) {
@@ -881,15 +896,6 @@ __device__ __forceinline__ int read_entry(const DistillArgs& a, int64_t at, floa
                        : widen(static_cast<const uint16_t*>(a.teacher_logits)[at]);
     const int col = read_column(a.teacher_ids, a.id64, at, a.vocab);
     return *u == -INFINITY ? -1 : col;
-}
-
-// A value all lanes of the wave hold, in a scalar register.
-__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-__device__ __forceinline__ uint64_t uniform(uint64_t x)
-{
-    const uint64_t lo = static_cast<uint32_t>(uniform(static_cast<int>(x)));
-    const uint64_t hi = static_cast<uint32_t>(uniform(static_cast<int>(x >> 32)));
-    return hi << 32 | lo;
 }
 
 // Whether the row's label lets it count (it may still have no entry), and the
@@ -1396,14 +1402,13 @@ template <typename AT, typename GT, bool ADD>
 int embed_sums(const EmbedArgs& a, SumPlan p, hipStream_t st)
 {
     constexpr int N = 16 / sizeof(AT);      // one 16-byte load of activations a lane
-    p.shift = lane_shift(a.dim, N, 6);
     p.zero_shift = lane_shift(a.dim, 16 / sizeof(GT), 8);
-    // about 64 KB to clear a block
+    // about 16 KB to clear a block (2.1 GB: 393 us, against 421 at 64 KB a block)
     const int64_t zr = kClearBytes / (a.dim * static_cast<int64_t>(sizeof(GT)));
     p.zero_rows = static_cast<int32_t>(zr < 1 ? 1 : (zr > kWave ? kWave : zr));
-    const int64_t cols = static_cast<int64_t>(N) << p.shift;
+    constexpr int64_t cols = static_cast<int64_t>(N) * kWave;
     p.splits = (a.dim + cols - 1) / cols;
-    const int64_t per = kEmbedThreads >> p.shift;
+    constexpr int64_t per = kEmbedThreads / kWave;
     p.sum_blocks = (p.chunks * p.splits + per - 1) / per;
     const int64_t zero_blocks = ADD ? 0 : (a.rows + p.zero_rows - 1) / p.zero_rows;
     int rc = launch(k_embed_sum<AT, GT, N, ADD>, p.sum_blocks + zero_blocks, kEmbedThreads, 0, st,
