@@ -189,6 +189,14 @@ _F64 = ("float64",)
 _I64 = ("int64",)
 _B16 = ("int16", "bfloat16", "uint16")      # bf16 bit patterns
 _ANY = None
+_dtype_names = {}       # torch dtype -> its name
+
+
+def _dtype_name(dtype) -> str:
+    name = _dtype_names.get(dtype)
+    if name is None:
+        name = _dtype_names[dtype] = str(dtype).replace("torch.", "")
+    return name
 
 
 def _ptr(t, what: str = "buffer", dtypes=_ANY, min_numel: int = 0):
@@ -204,9 +212,9 @@ def _ptr(t, what: str = "buffer", dtypes=_ANY, min_numel: int = 0):
         return t
     if not hasattr(t, "data_ptr"):
         raise TypeError(f"{what}: a torch tensor, an int device address or None is required")
-    name = str(t.dtype).replace("torch.", "")
-    if dtypes is not None and name not in dtypes:
-        raise ValueError(f"{what}: dtype {name}, expected {' or '.join(dtypes)}")
+    if dtypes is not None and _dtype_name(t.dtype) not in dtypes:
+        raise ValueError(f"{what}: dtype {_dtype_name(t.dtype)}, expected "
+                         f"{' or '.join(dtypes)}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: the tensor must be contiguous")
     if t.numel() < min_numel:

@@ -132,6 +132,8 @@ struct EmbedArgs {
 // leaves one partial row in each (at most two per chunk) for the join.
 // Longer chunks mean fewer partials, shorter ones more parallel work: 8
 // positions until the chunks number 1024, then twice as many, up to 64.
+// Up to kEmbedFew tokens (one a lane) are not sorted at all.
+constexpr int64_t kEmbedFew = 64;
 inline int32_t embed_chunk(int64_t tokens)
 {
     int32_t c = 8;
