@@ -243,6 +243,10 @@ def _out_len(s: "zs_shard") -> int:
 def _stream(stream):
     if stream is None:
         import torch
+        # the same handle without building a Stream object (2.7 us a call)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and torch.cuda.is_initialized():
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -421,6 +425,16 @@ def _rows_ptr(t, what: str, dtypes, rows: int, width: int, pitch: int):
     return _ptr(t, what, dtypes, (rows - 1) * pitch + width if rows > 0 else 0)
 
 
+def _same_device(**tensors) -> None:
+    """The library works on the current device: tensors of another one are
+    refused (a raw address is not looked at)."""
+    import torch
+    current = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+    for what, t in tensors.items():
+        if hasattr(t, "get_device") and t.get_device() not in (current, -1):
+            raise ValueError(f"{what}: on GPU {t.get_device()}, the current device is {current}")
+
+
 def _sized(workspace, workspace_bytes, need: int):
     """(address, bytes) of a workspace argument."""
     if workspace_bytes is None:
@@ -442,6 +456,7 @@ def zs_embed_workspace_bytes(e: zs_embed) -> int:
 
 
 def embed_lookup(e: zs_embed, ids, table, out, stream=None) -> None:
+    _same_device(ids=ids, table=table, out=out)
     _check(lib().embed_lookup(
         C.byref(e), _ptr(ids, "ids", _IDS.get(e.id_dtype), e.tokens),
         _rows_ptr(table, "table", _ELEM.get(e.table_dtype), e.rows, e.dim, e.table_pitch),
@@ -453,6 +468,7 @@ def embed_grad(e: zs_embed, ids, grad_out, grad_table, workspace, accumulate: bo
                stream=None, workspace_bytes=None) -> None:
     """The gradient of embed_lookup: grad_out are the T gradients of its rows,
     grad_table (of e.table_dtype) receives the table's."""
+    _same_device(ids=ids, grad_out=grad_out, grad_table=grad_table, workspace=workspace)
     ws, nbytes = _sized(workspace, workspace_bytes, zs_embed_workspace_bytes(e))
     _check(lib().embed_grad(
         C.byref(e), _ptr(ids, "ids", _IDS.get(e.id_dtype), e.tokens),
@@ -492,6 +508,7 @@ def distill_loss(d: zs_distill, logits, teacher_ids, teacher_logits, loss, lse, 
                  workspace=None, stream=None, workspace_bytes=None) -> None:
     """Row losses (loss: fp32[T], lse: fp32[T, 2]); loss_sum: one fp32 and
     counted: one int64, or None."""
+    _same_device(logits=logits, teacher_ids=teacher_ids, loss=loss, workspace=workspace)
     t = _targets(d, teacher_ids, teacher_logits, teacher_lse, labels)
     ws, nbytes = _sized(workspace, workspace_bytes, zs_distill_workspace_bytes(d))
     _check(lib().distill_loss(
@@ -504,6 +521,7 @@ def distill_loss(d: zs_distill, logits, teacher_ids, teacher_logits, loss, lse, 
 def distill_grad(d: zs_distill, logits, teacher_ids, teacher_logits, lse, grad, teacher_lse=None,
                  labels=None, row_grad=None, stream=None) -> None:
     """The logits' gradient from the lse of distill_loss; grad may be logits."""
+    _same_device(logits=logits, teacher_ids=teacher_ids, lse=lse, grad=grad)
     t = _targets(d, teacher_ids, teacher_logits, teacher_lse, labels)
     _check(lib().distill_grad(
         C.byref(d), _logits_ptr(d, logits, "logits", d.logits_pitch), C.byref(t),
@@ -516,6 +534,8 @@ def distill_loss_grad(d: zs_distill, logits, teacher_ids, teacher_logits, loss, 
                       counted=None, accumulate: bool = False, workspace=None, stream=None,
                       workspace_bytes=None) -> None:
     """distill_loss and distill_grad in one call; grad may be logits."""
+    _same_device(logits=logits, teacher_ids=teacher_ids, loss=loss, grad=grad,
+                 workspace=workspace)
     t = _targets(d, teacher_ids, teacher_logits, teacher_lse, labels)
     ws, nbytes = _sized(workspace, workspace_bytes, zs_distill_workspace_bytes(d))
     _check(lib().distill_loss_grad(

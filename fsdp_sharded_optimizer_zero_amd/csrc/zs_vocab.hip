@@ -1180,16 +1180,22 @@ __device__ __forceinline__ void put_entries(const DistillArgs& a, const Entries&
     for (int k = threadIdx.x; k < e.n; k += THREADS) {
         const int col = e.col[k];
         if (col < c0 || col >= c1) continue;
-        float take = 0.0f;
-        bool first = true;
+        int same = 0;
         for (int j = 0; j < e.n; j += 4) {
-            const int4 other = *reinterpret_cast<const int4*>(e.col + j);
-            const int o[4] = {other.x, other.y, other.z, other.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (o[i] != col) continue;
-                if (j + i < k) first = false;
-                take += row_grad * (j + i < a.k ? a.grad_kd * e.p[j + i] : a.grad_ce);
+            const int4 o = *reinterpret_cast<const int4*>(e.col + j);
+            same += (o.x == col) + (o.y == col) + (o.z == col) + (o.w == col);
+        }
+        const auto share = [&](int j) {
+            return row_grad * (j < a.k ? a.grad_kd * e.p[j] : a.grad_ce);
+        };
+        float take = share(k);
+        bool first = true;
+        if (same > 1) {
+            take = 0.0f;
+            for (int j = 0; j < e.n; ++j) {
+                if (e.col[j] != col) continue;
+                if (j < k) first = false;
+                take += share(j);
             }
         }
         if (first) put(out + col, slope_at<TM>(g, e.s[k], c) - take);

@@ -19,6 +19,12 @@ the library calls of one optimizer step on one stream:
              shard_grad_reduce(micro=j, ...) for j = 0..m-1   per unit
              (the norm on the last micro-batch only), then
              zero_shard_step(mean_in=..., sqnorm=...)         per unit
+
+``TableRun`` is a training step of the tied vocabulary table as a unit of its
+own, its gradients made by the library's table operators instead of the
+generator: every simulated rank looks its tokens up, is held to a teacher's
+top logits, and leaves the table's gradient; then every rank's shard is
+reduced, weighted by the ranks' valid tokens, clipped and updated.
 """
 from __future__ import annotations
 
@@ -30,9 +36,11 @@ import zsgen
 from zsgen.workloads import (STREAM_EXP_AVG, STREAM_EXP_AVG_SQ, STREAM_MASTER, Workload,
                              grad_key, grad_stream)
 
-from . import (ZS_GRAD_BF16, ZS_GRAD_F32, ZS_OUT_GATHER, ZS_OUT_SHARD, adamw, make_reduce,
-               shard_grad_reduce, shard_grad_sqnorm, shard_grad_sqnorm_units, zero_shard_step,
-               zs_layout, zs_workspace_bytes, zs_workspace_bytes_units)
+from . import (ZS_F32, ZS_GRAD_BF16, ZS_GRAD_F32, ZS_OUT_GATHER, ZS_OUT_SHARD, adamw,
+               distill_loss_grad, embed_grad, embed_lookup, make_distill, make_embed, make_reduce,
+               shard_grad_reduce, shard_grad_sqnorm, shard_grad_sqnorm_units, shard_pack_gather,
+               zero_shard_step, zs_distill_workspace_bytes, zs_embed_workspace_bytes, zs_layout,
+               zs_workspace_bytes, zs_workspace_bytes_units)
 
 
 def _empty(n, dtype, device):
@@ -227,3 +235,121 @@ class ShardRun:
             red = 0
             upd = (2 * nd + 26) * V + 2 * pads
         return red * self.units, upd * self.units
+
+
+@dataclass
+class TableBatch:
+    """One rank's micro-batch: T token ids, the teacher's entries and the
+    labels of its T positions (int64 on the GPU; -100: not trained on), and
+    how many labels count, which the program that made them knows."""
+    ids: torch.Tensor              # int64 [T]
+    teacher_ids: torch.Tensor      # int64 [T, k]
+    teacher_logits: torch.Tensor   # float32 [T, k]
+    labels: torch.Tensor           # int64 [T]
+    valid: int
+
+
+class TableRun:
+    """The tied vocabulary table [rows, dim] as a ZeRO/FSDP unit of n_d ranks,
+    all of them simulated here: each holds its shard of the fp32 state, and
+    its own full gradient of the unit, of which every shard takes a slice.
+
+    step(): per rank   embed_lookup, body, logits = hidden table^T,
+                       distill_loss_grad, the head's gradient (a matrix
+                       product, set), body's gradient, embed_grad (added)
+            per shard  shard_grad_reduce(rank_tokens=valid tokens), the
+                       squared norms summed
+            per shard  zero_shard_step into its slot of the gathered table,
+                       from which the next step looks up.
+
+    body: a differentiable function of the hidden states [T, dim] that stands
+    for the model between the two uses of the table; None: the identity."""
+
+    def __init__(self, rows: int, dim: int, n_d: int, tokens: int, k: int, scale: float = 1.0,
+                 temperature: float = 1.0, alpha: float = 1.0, f32_grads: bool = True, body=None,
+                 lr: float = 1e-3, weight_decay: float = 0.01, max_grad_norm: float = 1.0,
+                 device: str = "cuda"):
+        self.rows, self.dim, self.n_d, self.tokens = rows, dim, n_d, tokens
+        self.body, self.f32_grads = body, f32_grads
+        self.lr, self.weight_decay, self.max_grad_norm = lr, weight_decay, max_grad_norm
+        self.shards = [zs_layout(rows * dim, n_d, r, 8, 3) for r in range(n_d)]
+        S = self.shards[0].shard_len
+        self.gather = torch.zeros(n_d * S, dtype=torch.bfloat16, device=device)
+        self.table = self.gather[:rows * dim].view(rows, dim)
+        grad_dtype = torch.float32 if f32_grads else torch.bfloat16
+        self.grads = torch.zeros((n_d, n_d * S), dtype=grad_dtype, device=device)
+        self.state = [[torch.zeros(max(s.valid_len, 8), device=device) for _ in range(3)]
+                      for s in self.shards]                    # master, exp_avg, exp_avg_sq
+        self.mean = [torch.empty(max(s.valid_len, 8), device=device) for s in self.shards]
+        self.sqnorm = torch.zeros(1, dtype=torch.float64, device=device)
+        self.reduce_ws = torch.empty(zs_workspace_bytes(self.shards[0]), dtype=torch.uint8,
+                                     device=device)
+        self.hidden = torch.empty((tokens, dim), dtype=torch.bfloat16, device=device)
+        self.logits = torch.empty((tokens, rows), dtype=torch.bfloat16, device=device)
+        self.dlogits = torch.empty_like(self.logits)
+        self.dhidden = torch.empty_like(self.hidden)
+        self.loss = torch.empty((n_d, tokens), device=device)
+        self.loss_sum = torch.zeros(1, device=device)
+        self.counted = torch.zeros(1, dtype=torch.int64, device=device)
+        self.look = make_embed(tokens, rows, dim, scale=scale)
+        self.back = make_embed(tokens, rows, dim, scale=scale,
+                               table_dtype=ZS_F32 if f32_grads else 0)
+        self.embed_ws = torch.empty(max(zs_embed_workspace_bytes(self.back), 16),
+                                    dtype=torch.uint8, device=device)
+        self.targets = make_distill(tokens, rows, k, temperature=temperature, alpha=alpha)
+        self.distill_ws = torch.empty(zs_distill_workspace_bytes(self.targets), dtype=torch.uint8,
+                                      device=device)
+
+    def load(self, table: torch.Tensor):
+        """Set the fp32 master table [rows, dim] and publish its bf16 copy."""
+        flat = table.reshape(-1)
+        for s, (w, _, _) in zip(self.shards, self.state):
+            w[:s.valid_len] = flat[s.shard_offset:s.shard_offset + s.valid_len]
+            shard_pack_gather(s, w, self.gather)
+
+    def grad_table(self, r: int) -> torch.Tensor:
+        return self.grads[r, :self.rows * self.dim].view(self.rows, self.dim)
+
+    def rank_pass(self, r: int, b: TableBatch):
+        """Rank r's forward and backward pass: its gradient and row losses."""
+        embed_lookup(self.look, b.ids, self.table, self.hidden)
+        if self.body is None:
+            out = self.hidden
+        else:
+            leaf = self.hidden.detach().requires_grad_()
+            out = self.body(leaf)
+        h = out.detach()
+        torch.mm(h, self.table.t(), out=self.logits)
+        # the gradient of the rank's mean loss over its valid tokens
+        self.targets.scale = 1.0 / max(b.valid, 1)
+        distill_loss_grad(self.targets, self.logits, b.teacher_ids, b.teacher_logits,
+                          self.loss[r], self.dlogits, labels=b.labels, loss_sum=self.loss_sum,
+                          counted=self.counted, accumulate=r > 0, workspace=self.distill_ws)
+        self.grad_table(r).copy_(torch.mm(self.dlogits.t(), h))
+        dh = torch.mm(self.dlogits, self.table)
+        if self.body is None:
+            self.dhidden.copy_(dh)
+        else:
+            self.dhidden.copy_(torch.autograd.grad(out, leaf, dh)[0])
+        embed_grad(self.back, b.ids, self.dhidden, self.grad_table(r), self.embed_ws,
+                   accumulate=True)
+
+    def update(self, t: int, valid):
+        """Reduce, clip and update every rank's shard."""
+        spec = make_reduce(ZS_GRAD_F32 if self.f32_grads else ZS_GRAD_BF16, rank_tokens=valid)
+        for k, s in enumerate(self.shards):
+            ptrs = [self.grads[r].data_ptr() + s.shard_offset * self.grads.element_size()
+                    for r in range(self.n_d)]
+            shard_grad_reduce(s, spec, ptrs, self.mean[k], self.reduce_ws, self.sqnorm,
+                              accumulate=k > 0)
+        h = adamw(lr=self.lr, weight_decay=self.weight_decay, step=t,
+                  max_grad_norm=self.max_grad_norm)
+        for s, mean, (w, m, v) in zip(self.shards, self.mean, self.state):
+            zero_shard_step(s, h, mean_in=mean, sqnorm=self.sqnorm, master=w, exp_avg=m,
+                            exp_avg_sq=v, param_out=self.gather)
+
+    def step(self, t: int, batches):
+        """One optimizer step at bias-correction step t from one batch a rank."""
+        for r, b in enumerate(batches):
+            self.rank_pass(r, b)
+        self.update(t, [b.valid for b in batches])
