@@ -1180,22 +1180,16 @@ __device__ __forceinline__ void put_entries(const DistillArgs& a, const Entries&
     for (int k = threadIdx.x; k < e.n; k += THREADS) {
         const int col = e.col[k];
         if (col < c0 || col >= c1) continue;
-        int same = 0;
+        float take = 0.0f;
+        bool first = true;
         for (int j = 0; j < e.n; j += 4) {
             const int4 o = *reinterpret_cast<const int4*>(e.col + j);
-            same += (o.x == col) + (o.y == col) + (o.z == col) + (o.w == col);
-        }
-        const auto share = [&](int j) {
-            return row_grad * (j < a.k ? a.grad_kd * e.p[j] : a.grad_ce);
-        };
-        float take = share(k);
-        bool first = true;
-        if (same > 1) {
-            take = 0.0f;
-            for (int j = 0; j < e.n; ++j) {
-                if (e.col[j] != col) continue;
-                if (j < k) first = false;
-                take += share(j);
+            if (!(o.x == col | o.y == col | o.z == col | o.w == col)) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if ((i == 0 ? o.x : i == 1 ? o.y : i == 2 ? o.z : o.w) != col) continue;
+                first = first && j + i >= k;
+                take += row_grad * (j + i < a.k ? a.grad_kd * e.p[j + i] : a.grad_ce);
             }
         }
         if (first) put(out + col, slope_at<TM>(g, e.s[k], c) - take);
