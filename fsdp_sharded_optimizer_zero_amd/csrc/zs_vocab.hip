@@ -205,7 +205,17 @@ __global__ void __launch_bounds__(kEmbedThreads)
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / kWave;
-// kSortRows: the counts of 16 waves and their queues take 48 KB of LDS.
+constexpr int kSortRowBits = 9;     // kSortRows rows
+static_assert((1 << kSortRowBits) == kSortRows && ZS_EMBED_MAX / kSortWaves <= (1 << 20),
+              "a token of a wave's part and a row of a bucket fit one entry");
+// LDS of the sort: the 16 waves' counts, and what is left of 63 KB as their
+// lists (at least 128 entries each, the queue of a second reading).
+constexpr int kSortLds = 63 * 1024;
+__host__ __device__ constexpr int sort_list(int rows)
+{
+    return (kSortLds / 4 - kSortWaves * rows) / kSortWaves;
+}
+static_assert(sort_list(kSortRows) >= 2 * kWave, "a queue of 64 and what comes on top");
 constexpr int kSortLoads = 8;       // ids a lane has under way
 
 // Rows are dealt to buckets in turn (bucket = row mod buckets), because the
@@ -235,14 +245,17 @@ __device__ __forceinline__ uint64_t same_row(bool in, int row, int bits)
 // and comes from L2 after the first block), counts the tokens of earlier
 // buckets (where its own part of the order begins) and of each of its rows,
 // and then places its tokens.  Each wave takes one contiguous part of the
-// tokens; those of the bucket, few of each 64, are queued and handled 64 at a
-// time.  A token's place is: its row's start, the tokens of that row in
-// earlier waves, those handled earlier by its wave, and those in lower lanes.
+// tokens and lists those of the bucket, few of each 64, which are then
+// handled 64 at a time.  A token's place is: its row's start, the tokens of
+// that row in earlier waves, those handled earlier by its wave, and those in
+// lower lanes.  Where a wave's list is too short for its tokens (one id in
+// most of them), all waves read the ids again and handle 64 whenever they
+// have them, once to count and once to place.
 __global__ void __launch_bounds__(kSortThreads)
     k_embed_sort(EmbedArgs a, SortShape s, int32_t* order, int32_t* row_of, int32_t* starts)
 {
-    __shared__ int32_t hist[kSortWaves][kSortRows];
-    __shared__ int2 queue[kSortWaves][2 * kWave];   // (token, row in the bucket)
+    // per wave: its count of each row, then its list
+    extern __shared__ __align__(16) int32_t sort_lds[];
     __shared__ int32_t wave_sum[kSortWaves];
     __shared__ int32_t wave_below[kSortWaves];
     const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
@@ -253,12 +266,15 @@ __global__ void __launch_bounds__(kSortThreads)
     const int part = (tokens + kSortThreads - 1) / kSortThreads * kWave;
     const int t0 = wave * part, t1 = t0 + part < tokens ? t0 + part : tokens;
     const uint64_t lower = (uint64_t(1) << lane) - 1;
-    for (int r = lane; r < s.rows; r += kWave) hist[wave][r] = 0;
+    const int room = sort_list(s.rows);
+    int32_t* hist = sort_lds + wave * s.rows;
+    // entries (token - t0) << kSortRowBits | row in the bucket: 20 + 9 bits
+    uint32_t* list =
+        reinterpret_cast<uint32_t*>(sort_lds) + kSortWaves * s.rows + wave * room;
+    for (int r = lane; r < s.rows; r += kWave) hist[r] = 0;
 
-    // handle(n): the first n queued tokens, one a lane
-    int below = 0;
-    const auto walk = [&](auto handle) {
-        int queued = 0;
+    // found(token, row, in): 64 tokens, `in` those of the bucket
+    const auto read_ids = [&](auto found) {
         for (int base = t0; base < t1; base += kSpan) {
             uint32_t row[kSortLoads];
 #pragma unroll
@@ -271,46 +287,88 @@ __global__ void __launch_bounds__(kSortThreads)
 #pragma unroll
             for (int u = 0; u < kSortLoads; ++u) {
                 const bool here = row[u] != UINT32_MAX;
-                below += here && (row[u] & low) < bucket;
-                const bool in = here && (row[u] & low) == bucket;
-                const uint64_t mask = __ballot(in);
-                if (mask == 0) continue;
-                if (in)
-                    queue[wave][queued + __popcll(mask & lower)] =
-                        int2{base + u * kWave + lane, static_cast<int>(row[u] >> s.bucket_bits)};
-                queued += __popcll(mask);
-                __builtin_amdgcn_wave_barrier();
-                if (queued >= kWave) {
-                    handle(kWave);
-                    queued -= kWave;
-                    const int2 rest = queue[wave][kWave + lane];
-                    __builtin_amdgcn_wave_barrier();
-                    if (lane < queued) queue[wave][lane] = rest;
-                    __builtin_amdgcn_wave_barrier();
-                }
+                found(base + u * kWave + lane, row[u], here,
+                      here && (row[u] & low) == bucket);
             }
         }
-        if (queued > 0) handle(queued);
     };
-    walk([&](int n) {
-        const int r = queue[wave][lane].y;
-        const uint64_t same = same_row(lane < n, r, s.row_bits);
-        if (lane < n && (same & lower) == 0) hist[wave][r] += __popcll(same);
+    const auto entry = [&](int t, uint32_t row) {
+        return static_cast<uint32_t>(t - t0) << kSortRowBits | row >> s.bucket_bits;
+    };
+    // count(e, in), place(e, in): one listed token a lane
+    const auto count = [&](uint32_t e, bool in) {
+        const int r = e & ((1 << kSortRowBits) - 1);
+        const uint64_t same = same_row(in, r, s.row_bits);
+        if (in && (same & lower) == 0) hist[r] += __popcll(same);
+        __builtin_amdgcn_wave_barrier();
+    };
+    const auto place = [&](uint32_t e, bool in) {
+        const int r = e & ((1 << kSortRowBits) - 1);
+        const uint64_t same = same_row(in, r, s.row_bits);
+        int first = 0;
+        if (in) first = hist[r];
+        // every lane has read before the first lane of each row adds
+        __builtin_amdgcn_wave_barrier();
+        if (in) {
+            const int before = __popcll(same & lower);
+            if (before == 0) hist[r] = first + __popcll(same);
+            order[first + before] = t0 + static_cast<int>(e >> kSortRowBits);
+            row_of[first + before] = r << s.bucket_bits | static_cast<int32_t>(bucket);
+        }
+        __builtin_amdgcn_wave_barrier();
+    };
+    // the listed tokens, or all of the bucket's by way of a queue of 64
+    const auto from_list = [&](int n, auto handle) {
+        for (int i = 0; i < n; i += kWave) {
+            const bool in = i + lane < n;
+            handle(in ? list[i + lane] : 0, in);
+        }
+    };
+    const auto from_ids = [&](auto handle) {
+        int queued = 0;
+        read_ids([&](int t, uint32_t row, bool, bool in) {
+            const uint64_t mask = __ballot(in);
+            if (mask == 0) return;
+            if (in) list[queued + __popcll(mask & lower)] = entry(t, row);
+            queued += __popcll(mask);
+            __builtin_amdgcn_wave_barrier();
+            if (queued < kWave) return;
+            handle(list[lane], true);
+            queued -= kWave;
+            const uint32_t rest = list[kWave + lane];
+            __builtin_amdgcn_wave_barrier();
+            if (lane < queued) list[lane] = rest;
+            __builtin_amdgcn_wave_barrier();
+        });
+        if (queued > 0) handle(list[lane], lane < queued);
+    };
+
+    int below = 0, n = 0;
+    read_ids([&](int t, uint32_t row, bool here, bool in) {
+        below += here && (row & low) < bucket;
+        const uint64_t mask = __ballot(in);
+        if (mask == 0) return;
+        const int at = n + __popcll(mask & lower);
+        if (in && at < room) list[at] = entry(t, row);
+        n += __popcll(mask);
     });
     for (int o = kWave / 2; o > 0; o >>= 1) below += __shfl_xor(below, o);
     if (lane == 0) wave_below[wave] = below;
+    const bool listed = __syncthreads_or(n > room) == 0;
+    if (listed) from_list(n, count);
+    else from_ids(count);
     __syncthreads();
 
     // per row: the tokens of earlier waves, and the row's start
     int total = 0;
     if (tid < s.rows) {
-        int n[kSortWaves];
+        int in_wave[kSortWaves];
 #pragma unroll
-        for (int w = 0; w < kSortWaves; ++w) n[w] = hist[w][tid];
+        for (int w = 0; w < kSortWaves; ++w) in_wave[w] = sort_lds[w * s.rows + tid];
 #pragma unroll
         for (int w = 0; w < kSortWaves; ++w) {
-            hist[w][tid] = total;
-            total += n[w];
+            sort_lds[w * s.rows + tid] = total;
+            total += in_wave[w];
         }
     }
     int incl = total;
@@ -330,25 +388,11 @@ __global__ void __launch_bounds__(kSortThreads)
         starts[bucket * s.rows + tid] = start;
         if (bucket == low && tid == s.rows - 1) starts[(low + 1) * s.rows] = start + total;
 #pragma unroll
-        for (int w = 0; w < kSortWaves; ++w) hist[w][tid] += start;
+        for (int w = 0; w < kSortWaves; ++w) sort_lds[w * s.rows + tid] += start;
     }
     __syncthreads();
-
-    walk([&](int n) {
-        const int2 q = queue[wave][lane];
-        const uint64_t same = same_row(lane < n, q.y, s.row_bits);
-        int first = 0;
-        if (lane < n) first = hist[wave][q.y];
-        // every lane has read before the first lane of each row adds
-        __builtin_amdgcn_wave_barrier();
-        if (lane < n) {
-            const int before = __popcll(same & lower);
-            if (before == 0) hist[wave][q.y] = first + __popcll(same);
-            order[first + before] = q.x;
-            row_of[first + before] = static_cast<int32_t>(q.y << s.bucket_bits | bucket);
-        }
-        __builtin_amdgcn_wave_barrier();
-    });
+    if (listed) from_list(n, place);
+    else from_ids(place);
 }
 
 // ---- embedding gradient: sums -------------------------------------------------------
@@ -1600,7 +1644,7 @@ int enqueue_embed_grad(const EmbedArgs& a, bool accumulate, void* workspace, voi
         const SortShape s = sort_shape(a.rows);
         const int64_t buckets = int64_t(1) << s.bucket_bits;
         hipLaunchKernelGGL(k_embed_sort, dim3(static_cast<uint32_t>(buckets)), dim3(kSortThreads),
-                           0, st, a, s, order, row_of, starts);
+                           kSortLds, st, a, s, order, row_of, starts);
         const int rc = launched();
         if (rc != ZS_OK) return rc;
         p.order = order;

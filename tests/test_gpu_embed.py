@@ -193,6 +193,16 @@ def test_grad_long_runs_and_many_rows(tokens, rows, dim):
     run_grad(make_ids("zipf", tokens, rows, 13), tokens, rows, dim, BF16, F32, False)
 
 
+@pytest.mark.parametrize("kind,tokens,rows", [("one", 40000, 130000), ("two", 40000, 500),
+                                              ("runs", 70000, 131072)])
+def test_grad_sort_lists_overflow(kind, tokens, rows):
+    """More tokens of one sort bucket than its waves list."""
+    ids = make_ids("zipf" if kind == "runs" else kind, tokens, rows, 21)
+    if kind == "runs":
+        ids[1000:9000], ids[30000:52000] = 77, 512
+    run_grad(ids, tokens, rows, 24, BF16, F32, False)
+
+
 def test_grad_without_tokens():
     e = Z.make_embed(0, 33, 20, table_dtype=Z.ZS_F32)
     ws = torch.empty(max(Z.zs_embed_workspace_bytes(e), 16), dtype=torch.uint8, device="cuda")
