@@ -425,14 +425,17 @@ def _rows_ptr(t, what: str, dtypes, rows: int, width: int, pitch: int):
     return _ptr(t, what, dtypes, (rows - 1) * pitch + width if rows > 0 else 0)
 
 
-def _same_device(**tensors) -> None:
-    """The library works on the current device: tensors of another one are
-    refused (a raw address is not looked at)."""
+def _stream_on(stream, *tensors):
+    """The stream's handle.  The library works on the current device: tensors
+    of another one are refused (raw addresses are not looked at)."""
     import torch
-    current = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
-    for what, t in tensors.items():
-        if hasattr(t, "get_device") and t.get_device() not in (current, -1):
-            raise ValueError(f"{what}: on GPU {t.get_device()}, the current device is {current}")
+    if not torch.cuda.is_initialized():
+        return _stream(stream)          # no GPU tensor yet: _ptr refuses the others
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != device:
+            raise ValueError(f"a tensor on GPU {t.get_device()}: the current device is {device}")
+    return _stream(stream)
 
 
 def _sized(workspace, workspace_bytes, need: int):
@@ -456,26 +459,25 @@ def zs_embed_workspace_bytes(e: zs_embed) -> int:
 
 
 def embed_lookup(e: zs_embed, ids, table, out, stream=None) -> None:
-    _same_device(ids=ids, table=table, out=out)
     _check(lib().embed_lookup(
         C.byref(e), _ptr(ids, "ids", _IDS.get(e.id_dtype), e.tokens),
         _rows_ptr(table, "table", _ELEM.get(e.table_dtype), e.rows, e.dim, e.table_pitch),
         _rows_ptr(out, "out", _ELEM.get(e.act_dtype), e.tokens, e.dim, e.act_pitch),
-        _stream(stream)), "embed_lookup")
+        _stream_on(stream, ids, table, out)), "embed_lookup")
 
 
 def embed_grad(e: zs_embed, ids, grad_out, grad_table, workspace, accumulate: bool = False,
                stream=None, workspace_bytes=None) -> None:
     """The gradient of embed_lookup: grad_out are the T gradients of its rows,
     grad_table (of e.table_dtype) receives the table's."""
-    _same_device(ids=ids, grad_out=grad_out, grad_table=grad_table, workspace=workspace)
     ws, nbytes = _sized(workspace, workspace_bytes, zs_embed_workspace_bytes(e))
     _check(lib().embed_grad(
         C.byref(e), _ptr(ids, "ids", _IDS.get(e.id_dtype), e.tokens),
         _rows_ptr(grad_out, "grad_out", _ELEM.get(e.act_dtype), e.tokens, e.dim, e.act_pitch),
         _rows_ptr(grad_table, "grad_table", _ELEM.get(e.table_dtype), e.rows, e.dim,
                   e.table_pitch),
-        1 if accumulate else 0, ws, nbytes, _stream(stream)), "embed_grad")
+        1 if accumulate else 0, ws, nbytes,
+        _stream_on(stream, ids, grad_out, grad_table, workspace)), "embed_grad")
 
 
 def make_distill(rows: int, vocab: int, k: int, logits_pitch=None, grad_pitch=None,
@@ -508,25 +510,27 @@ def distill_loss(d: zs_distill, logits, teacher_ids, teacher_logits, loss, lse, 
                  workspace=None, stream=None, workspace_bytes=None) -> None:
     """Row losses (loss: fp32[T], lse: fp32[T, 2]); loss_sum: one fp32 and
     counted: one int64, or None."""
-    _same_device(logits=logits, teacher_ids=teacher_ids, loss=loss, workspace=workspace)
     t = _targets(d, teacher_ids, teacher_logits, teacher_lse, labels)
     ws, nbytes = _sized(workspace, workspace_bytes, zs_distill_workspace_bytes(d))
     _check(lib().distill_loss(
         C.byref(d), _logits_ptr(d, logits, "logits", d.logits_pitch), C.byref(t),
         _ptr(loss, "loss", _F32, d.rows), _ptr(lse, "lse", _F32, 2 * d.rows),
         _ptr(loss_sum, "loss_sum", _F32, 1), _ptr(counted, "counted", _I64, 1),
-        1 if accumulate else 0, ws, nbytes, _stream(stream)), "distill_loss")
+        1 if accumulate else 0, ws, nbytes,
+        _stream_on(stream, logits, teacher_ids, teacher_logits, teacher_lse, labels, loss, lse,
+                   workspace)), "distill_loss")
 
 
 def distill_grad(d: zs_distill, logits, teacher_ids, teacher_logits, lse, grad, teacher_lse=None,
                  labels=None, row_grad=None, stream=None) -> None:
     """The logits' gradient from the lse of distill_loss; grad may be logits."""
-    _same_device(logits=logits, teacher_ids=teacher_ids, lse=lse, grad=grad)
     t = _targets(d, teacher_ids, teacher_logits, teacher_lse, labels)
     _check(lib().distill_grad(
         C.byref(d), _logits_ptr(d, logits, "logits", d.logits_pitch), C.byref(t),
         _ptr(lse, "lse", _F32, 2 * d.rows), _ptr(row_grad, "row_grad", _F32, d.rows),
-        _logits_ptr(d, grad, "grad", d.grad_pitch), _stream(stream)), "distill_grad")
+        _logits_ptr(d, grad, "grad", d.grad_pitch),
+        _stream_on(stream, logits, teacher_ids, teacher_logits, teacher_lse, labels, lse, row_grad,
+                   grad)), "distill_grad")
 
 
 def distill_loss_grad(d: zs_distill, logits, teacher_ids, teacher_logits, loss, grad,
@@ -534,8 +538,6 @@ def distill_loss_grad(d: zs_distill, logits, teacher_ids, teacher_logits, loss, 
                       counted=None, accumulate: bool = False, workspace=None, stream=None,
                       workspace_bytes=None) -> None:
     """distill_loss and distill_grad in one call; grad may be logits."""
-    _same_device(logits=logits, teacher_ids=teacher_ids, loss=loss, grad=grad,
-                 workspace=workspace)
     t = _targets(d, teacher_ids, teacher_logits, teacher_lse, labels)
     ws, nbytes = _sized(workspace, workspace_bytes, zs_distill_workspace_bytes(d))
     _check(lib().distill_loss_grad(
@@ -544,7 +546,8 @@ def distill_loss_grad(d: zs_distill, logits, teacher_ids, teacher_logits, loss, 
         _ptr(row_grad, "row_grad", _F32, d.rows),
         _logits_ptr(d, grad, "grad", d.grad_pitch), _ptr(loss_sum, "loss_sum", _F32, 1),
         _ptr(counted, "counted", _I64, 1), 1 if accumulate else 0, ws, nbytes,
-        _stream(stream)), "distill_loss_grad")
+        _stream_on(stream, logits, teacher_ids, teacher_logits, teacher_lse, labels, loss, lse,
+                   row_grad, grad, workspace)), "distill_loss_grad")
 
 
 def build(verbose: bool = False) -> str:

@@ -549,19 +549,27 @@ __global__ void __launch_bounds__(kEmbedThreads)
     const int64_t worker = block * (kEmbedThreads / kWave) + wave;
     const int64_t chunk = worker / p.splits;
     const int64_t c = ((worker - chunk * p.splits) * kWave + lane) * N;
-    const int n = *p.count;
     const int64_t first = chunk * p.chunk;
-    if (first >= n) return;
-    const int p0 = static_cast<int>(first), len = p0 + p.chunk < n ? p.chunk : n - p0;
-    // position p0 + lane (the chunk has at most 64), and the row behind it
-    const int own = lane < len ? lane : len - 1;
-    const int token = p.order[p0 + own], row = p.row_of[p0 + own];
-    const int row_next = p0 + own + 1 < n ? p.row_of[p0 + own + 1] : -1;
+    if (first >= a.tokens) return;
+    // Position p0 + lane (the chunk has at most 64), the row behind it and the
+    // one before the chunk, loaded beside the count of sorted positions: what
+    // lies behind that count is not used.
+    const int p0 = static_cast<int>(first), tokens = static_cast<int>(a.tokens);
+    const int at0 = p0 + lane < tokens ? p0 + lane : tokens - 1;
+    const int token = p.order[at0], row = p.row_of[at0];
+    int row_next = p.row_of[at0 + 1 < tokens ? at0 + 1 : at0];
+    const int row_before = p.row_of[p0 > 0 ? p0 - 1 : 0];
+    const int n = *p.count;
+    if (p0 >= n) return;
+    const int len = p0 + p.chunk < n ? p.chunk : n - p0;
+    if (at0 + 1 >= n) row_next = -1;
     // whether the run under way began in this chunk
-    bool began = p0 == 0 || p.row_of[p0 - 1] != uniform(row);
-    if (c >= a.dim) return;
-    const AT* src = static_cast<const AT*>(a.src) + c;
-    const int width = c + N <= a.dim ? N : static_cast<int>(a.dim - c);
+    bool began = p0 == 0 || row_before != uniform(row);
+    // Lanes behind the last column stay (the others read their token and row):
+    // they load the first columns again and store nothing.
+    const int64_t col = c < a.dim ? c : 0;
+    const AT* src = static_cast<const AT*>(a.src) + col;
+    const int width = col + N <= a.dim ? N : static_cast<int>(a.dim - col);
     float* partial = p.partials + chunk * 2 * a.dim;
     float acc[N] = {};
     for (int q = 0; q < len; q += UNROLL) {
@@ -579,7 +587,7 @@ __global__ void __launch_bounds__(kEmbedThreads)
             for (int u = 0; u < UNROLL; ++u) {
                 const int r = __builtin_amdgcn_readlane(row, at(u));
                 if (q + u < len && __builtin_amdgcn_readlane(row_next, at(u)) != r)
-                    read_row<GT, N>(a, r, c, old[u]);
+                    read_row<GT, N>(a, r, col, old[u]);
             }
         }
 #pragma unroll
@@ -592,9 +600,11 @@ __global__ void __launch_bounds__(kEmbedThreads)
             const int r = __builtin_amdgcn_readlane(row, at(u));
             const bool ends = __builtin_amdgcn_readlane(row_next, at(u)) != r;
             if (!ends && q + u + 1 < len) continue;
-            if (!began) put_partial<N>(partial, c, a.dim, acc);
-            else if (ends) put_row<GT, N, ADD>(a, r, c, acc, old[ADD ? u : 0]);
-            else put_partial<N>(partial + a.dim, c, a.dim, acc);
+            if (c < a.dim) {
+                if (!began) put_partial<N>(partial, c, a.dim, acc);
+                else if (ends) put_row<GT, N, ADD>(a, r, c, acc, old[ADD ? u : 0]);
+                else put_partial<N>(partial + a.dim, c, a.dim, acc);
+            }
             began = true;
 #pragma unroll
             for (int i = 0; i < N; ++i) acc[i] = 0.0f;
@@ -668,11 +678,10 @@ __global__ void __launch_bounds__(kEmbedThreads)
     __shared__ float sums[kEmbedThreads * N];
     const int64_t block = b0 + blockIdx.x;
     const int64_t chunk = block / p.splits;
-    const int n = *p.count;
     const int64_t p0 = chunk * p.chunk, p1 = p0 + p.chunk;
-    if (p1 >= n) return;
-    const int32_t row = p.row_of[p1];
-    if (p.row_of[p1 - 1] != row) return;                    // no run crosses here
+    if (p1 >= a.tokens) return;
+    const int32_t row = p.row_of[p1], row_before = p.row_of[p1 - 1];
+    if (p1 >= *p.count || row_before != row) return;        // no run crosses here
     const int32_t* span = p.starts + sort_slot(p.sort, row);
     if (span[0] < p0) return;                               // it begins in an earlier chunk
     const int64_t count = (span[1] - 1) / p.chunk - chunk + 1;
