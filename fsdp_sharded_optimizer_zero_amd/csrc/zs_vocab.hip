@@ -122,6 +122,67 @@ __device__ __forceinline__ void store_nt(float* p, const float v[N])
                                     reinterpret_cast<f32x4_u*>(p + i));
 }
 
+// 16 bytes of elements as loaded: bf16 stays packed until it is used.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+    static constexpr int N = 8;
+    using M = u32x4_u;  // in memory
+    using V = u32x4;    // in registers
+    static __device__ __forceinline__ V lowest()    // -Inf in every place
+    {
+        constexpr uint32_t x = 0xFF80FF80u;
+        return V{x, x, x, x};
+    }
+    static __device__ __forceinline__ V first(const uint16_t* p, int n)
+    {
+        const auto at = [&](int i) { return i < n ? static_cast<uint32_t>(p[i]) : 0u; };
+        return V{at(0) | at(1) << 16, at(2) | at(3) << 16, at(4) | at(5) << 16,
+                 at(6) | at(7) << 16};
+    }
+    static __device__ __forceinline__ void widen(V b, float v[8])
+    {
+        v[0] = bf16_lo(b.x); v[1] = bf16_hi(b.x);
+        v[2] = bf16_lo(b.y); v[3] = bf16_hi(b.y);
+        v[4] = bf16_lo(b.z); v[5] = bf16_hi(b.z);
+        v[6] = bf16_lo(b.w); v[7] = bf16_hi(b.w);
+    }
+    static __device__ __forceinline__ V pack(const float v[8])
+    {
+        return V{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                 pack_bf16x2(v[6], v[7])};
+    }
+};
+template <>
+struct Raw<float> {
+    static constexpr int N = 4;
+    using M = f32x4_u;
+    using V = f32x4;
+    static __device__ __forceinline__ V lowest()
+    {
+        return V{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    }
+    static __device__ __forceinline__ V first(const float* p, int n)
+    {
+        const auto at = [&](int i) { return i < n ? p[i] : 0.0f; };
+        return V{at(0), at(1), at(2), at(3)};
+    }
+    static __device__ __forceinline__ void widen(V b, float v[4])
+    {
+        v[0] = b.x; v[1] = b.y; v[2] = b.z; v[3] = b.w;
+    }
+    static __device__ __forceinline__ V pack(const float v[4]) { return V{v[0], v[1], v[2], v[3]}; }
+};
+// All of a vector (past the caches' reuse), or its first n elements and 0.
+template <typename T>
+__device__ __forceinline__ typename Raw<T>::V load_raw(const T* p, int n)
+{
+    return n == Raw<T>::N
+               ? __builtin_nontemporal_load(reinterpret_cast<const typename Raw<T>::M*>(p))
+               : Raw<T>::first(p, n);
+}
+
 // Subtracting in 64 bits without a sign: an id below first gives a number
 // above every row count.
 __device__ __forceinline__ uint64_t row_of_id(int64_t id, int64_t first)
@@ -159,7 +220,9 @@ int lane_shift(int64_t dim, int n, int most)
 }
 
 // 1 << shift lanes take one token; a block takes 256 >> shift.  A lane has
-// TURNS loads under way (a row of 4096 bf16 is two turns of a block).
+// TURNS loads under way (a row of 4096 bf16 is two turns of a block).  Bound
+// by HBM: 16384 tokens of 4096 bf16 in 31.7 us, 5.9 TB/s (41 us with one load
+// under way and plain stores).
 template <typename TT, typename AT, int N, int TURNS>
 __global__ void __launch_bounds__(kEmbedThreads)
     k_embed_lookup(EmbedArgs a, int shift, int64_t b0)
@@ -248,7 +311,8 @@ __device__ __forceinline__ uint64_t same_row(bool in, int row, int bits)
 // tokens and lists those of the bucket, few of each 64, which are then
 // handled 64 at a time.  A token's place is: its row's start, the tokens of
 // that row in earlier waves, those handled earlier by its wave, and those in
-// lower lanes.  Where a wave's list is too short for its tokens (one id in
+// lower lanes (4096 tokens 8 us, 65536 40 us: the ids' way from L2 to every
+// CU).  Where a wave's list is too short for its tokens (one id in
 // most of them), all waves read the ids again and handle 64 whenever they
 // have them, once to count and once to place.
 __global__ void __launch_bounds__(kSortThreads)
@@ -457,8 +521,8 @@ __device__ __forceinline__ void put_partial(float* p, int64_t c, int64_t dim, co
 }
 
 // One block: +0 into those of zero_rows consecutive rows from r0 whose bit in
-// `mask` is set
-// (plain stores: 2.1 GB and its sums in 375 us, against 398 with nt ones).
+// `mask` is set (plain stores: 2.1 GB and its sums in 375 us, against 398 with
+// nt ones).
 template <typename GT>
 __device__ __forceinline__ void clear_rows(const EmbedArgs& a, const SumPlan& p, int64_t r0,
                                            uint64_t mask)
@@ -482,49 +546,10 @@ __device__ __forceinline__ void clear_rows(const EmbedArgs& a, const SumPlan& p,
 
 constexpr int kSumUnroll = 8;
 
-// N elements as loaded: bf16 stays packed until it is added.
-template <typename T, int N>
-struct Pack;
-template <>
-struct Pack<uint16_t, 8> {
-    u32x4 v;
-    __device__ __forceinline__ void load(const uint16_t* p)
-    {
-        v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_u*>(p));
-    }
-    __device__ __forceinline__ void get(float x[8]) const
-    {
-        x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x);
-        x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
-        x[4] = bf16_lo(v.z); x[5] = bf16_hi(v.z);
-        x[6] = bf16_lo(v.w); x[7] = bf16_hi(v.w);
-    }
-    __device__ __forceinline__ void load_part(const uint16_t* p, int n)
-    {
-        const auto at = [&](int i) { return i < n ? static_cast<uint32_t>(p[i]) : 0u; };
-        v = u32x4{at(0) | at(1) << 16, at(2) | at(3) << 16, at(4) | at(5) << 16,
-                  at(6) | at(7) << 16};
-    }
-};
-template <>
-struct Pack<float, 4> {
-    f32x4 v;
-    __device__ __forceinline__ void load(const float* p)
-    {
-        v = __builtin_nontemporal_load(reinterpret_cast<const f32x4_u*>(p));
-    }
-    __device__ __forceinline__ void get(float x[4]) const
-    {
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-    }
-    __device__ __forceinline__ void load_part(const float* p, int n)
-    {
-        const auto at = [&](int i) { return i < n ? p[i] : 0.0f; };
-        v = f32x4{at(0), at(1), at(2), at(3)};
-    }
-};
-
-// One wave sums one chunk of sorted positions over one part of the columns.
+// One wave sums one chunk of sorted positions over one part of the columns:
+// equal work a wave whatever the ids, where a wave a row would leave the most
+// frequent token to one wave.  What bounds it is HBM (65536 x 4096 bf16 into
+// 128256 rows: 1.55 GB and 33 MB of partials in 269 us, 5.9 TB/s).
 // Its lanes hold the chunk's tokens and rows, one position a lane, which the
 // walk takes into scalar registers one by one: kSumUnroll loads in flight, and
 // a run's sum handed on where the run ends or the chunk does.
@@ -573,14 +598,12 @@ __global__ void __launch_bounds__(kEmbedThreads)
     float* partial = p.partials + chunk * 2 * a.dim;
     float acc[N] = {};
     for (int q = 0; q < len; q += UNROLL) {
-        Pack<AT, N> x[UNROLL];
+        typename Raw<AT>::V x[UNROLL];
         float old[ADD ? UNROLL : 1][N];
         const auto at = [&](int u) { return q + u < len ? q + u : len - 1; };
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
-            const AT* s = src + __builtin_amdgcn_readlane(token, at(u)) * a.act_pitch;
-            if (width == N) x[u].load(s);
-            else x[u].load_part(s, width);
+            x[u] = load_raw(src + __builtin_amdgcn_readlane(token, at(u)) * a.act_pitch, width);
         }
         if constexpr (ADD) {
 #pragma unroll
@@ -594,7 +617,7 @@ __global__ void __launch_bounds__(kEmbedThreads)
         for (int u = 0; u < UNROLL; ++u) {
             if (q + u >= len) continue;
             float v[N];
-            x[u].get(v);
+            Raw<AT>::widen(x[u], v);
 #pragma unroll
             for (int i = 0; i < N; ++i) acc[i] += v[i];
             const int r = __builtin_amdgcn_readlane(row, at(u));
@@ -612,7 +635,8 @@ __global__ void __launch_bounds__(kEmbedThreads)
     }
 }
 
-// Up to 64 tokens: no sort.  Every wave has all of their rows, one a lane; a
+// Up to 64 tokens: one launch, no sort (37 tokens of 768: 3.1 us, where sort,
+// sums and join take 12).  Every wave has all of their rows, one a lane; a
 // wave takes one token and one part of the columns, and if no earlier token
 // has its row, sums the tokens that have it, in order.
 template <typename AT, typename GT, int N, bool ADD>
@@ -646,21 +670,19 @@ __global__ void __launch_bounds__(kEmbedThreads)
     float acc[N] = {}, old[N] = {};
     if constexpr (ADD) read_row<GT, N>(a, r, c, old);
     while (same) {
-        Pack<AT, N> x[4];
+        typename Raw<AT>::V x[4] = {};
         uint64_t m = same;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             if (m == 0) continue;
-            const AT* s = src + __builtin_ctzll(m) * a.act_pitch;
-            if (width == N) x[u].load(s);
-            else x[u].load_part(s, width);
+            x[u] = load_raw(src + __builtin_ctzll(m) * a.act_pitch, width);
             m &= m - 1;
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             if (same == 0) continue;
             float v[N];
-            x[u].get(v);
+            Raw<AT>::widen(x[u], v);
 #pragma unroll
             for (int i = 0; i < N; ++i) acc[i] += v[i];
             same &= same - 1;
@@ -669,7 +691,8 @@ __global__ void __launch_bounds__(kEmbedThreads)
     put_row<GT, N, ADD>(a, r, c, acc, old);
 }
 
-// The runs that cross chunks: the block of the chunk a run begins in adds
+// The runs that cross chunks (at 65536 tokens 11 us, most of it blocks that
+// find none): the block of the chunk a run begins in adds
 // its partials in order, each wave a contiguous part of them.
 template <typename GT, int N, bool ADD>
 __global__ void __launch_bounds__(kEmbedThreads)
@@ -720,13 +743,15 @@ __global__ void __launch_bounds__(kEmbedThreads)
 //
 // One row is one softmax (two with labels at another temperature) over the
 // vocabulary plus K entries to look at.  The logits are what costs: HBM moves
-// them, and each takes about ten vector instructions and an exponential (four
-// issue slots) in each of the two passes, so the arithmetic is kept near half
-// of the time the bytes take:
-//  - exponentials are the hardware's base-2 one (1 ulp), arguments
-//    (s - m) * log2(e)/tau with the difference taken first, so that an error
-//    grows with the distance from the maximum, where the value is small;
-//  - the teacher's entries are one wave's work, beside the others' loads.
+// them, and each takes about six vector instructions and an exponential (four
+// issue slots) in each of the two passes, together half the time the bytes
+// take (8192 x 128256 bf16: without the exponentials 709 us, with them 740):
+//  - exponentials are the hardware's base-2 one (1 ulp), their arguments one
+//    fma each (see kFmaLimit), exact where the value is large;
+//  - logits and gradients pass the caches (nt: the loss of 2048 x 50257 fp32
+//    behind another kernel's stores took 75 us, with plain loads and stores
+//    113), labels come through the scalar cache, and the teacher's entries
+//    are a side job while a row's loads are under way.
 
 constexpr int kWaves(int threads) { return threads / kWave; }
 
@@ -803,45 +828,6 @@ __device__ __forceinline__ Stat block_join(Stat s, float c, float* red)
     if constexpr (TM == kSame) s.b = s.a;
     return s;
 }
-
-// A 16-byte vector of logits, and its elements.
-template <typename T>
-struct Raw;
-template <>
-struct Raw<uint16_t> {
-    static constexpr int N = 8;
-    using M = u32x4_u;  // in memory
-    using V = u32x4;    // in registers
-    static __device__ __forceinline__ V lowest() { return V{kNegInf2, kNegInf2, kNegInf2, kNegInf2}; }
-    static __device__ __forceinline__ V pack(const float v[8])
-    {
-        return V{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                 pack_bf16x2(v[6], v[7])};
-    }
-    static __device__ __forceinline__ void widen(V b, float v[8])
-    {
-        v[0] = bf16_lo(b.x); v[1] = bf16_hi(b.x);
-        v[2] = bf16_lo(b.y); v[3] = bf16_hi(b.y);
-        v[4] = bf16_lo(b.z); v[5] = bf16_hi(b.z);
-        v[6] = bf16_lo(b.w); v[7] = bf16_hi(b.w);
-    }
-    static constexpr uint32_t kNegInf2 = 0xFF80FF80u;
-};
-template <>
-struct Raw<float> {
-    static constexpr int N = 4;
-    using M = f32x4_u;
-    using V = f32x4;
-    static __device__ __forceinline__ V pack(const float v[4]) { return V{v[0], v[1], v[2], v[3]}; }
-    static __device__ __forceinline__ V lowest()
-    {
-        return V{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    }
-    static __device__ __forceinline__ void widen(V b, float v[4])
-    {
-        v[0] = b.x; v[1] = b.y; v[2] = b.z; v[3] = b.w;
-    }
-};
 
 template <int N>
 __device__ __forceinline__ float max_n(const float x[N], float m)
@@ -1028,9 +1014,9 @@ __device__ __forceinline__ bool label_counts(const DistillArgs& a, int64_t row, 
     return id >= 0 && id < a.vocab;
 }
 
-// The row's entries into LDS, a part of them a thread (`thread` of `threads`),
-// and with PICK the logits at those in columns [c0, c1).
-template <typename T, bool PICK>
+// The row's entries into LDS (u for log p), a part of them a thread (`thread`
+// of `threads`), and the logits at those in columns [c0, c1).
+template <typename T>
 __device__ __forceinline__ void read_entries(const DistillArgs& a, const Entries& e, int64_t row,
                                              int label, const T* s, int64_t c0, int64_t c1,
                                              int thread, int threads)
@@ -1040,13 +1026,12 @@ __device__ __forceinline__ void read_entries(const DistillArgs& a, const Entries
         float u = 0.0f;
         if (k < a.k) {
             col = read_entry(a, row * a.k + k, &u);
-            u *= a.inv_tau;
         } else if (k == a.k && a.ce) {
             col = label;
         }
         e.col[k] = col;
         e.logp[k] = u;
-        if (PICK && col >= c0 && col < c1) e.s[k] = widen(s[col]);
+        if (col >= c0 && col < c1) e.s[k] = widen(s[col]);
     }
 }
 
@@ -1064,18 +1049,20 @@ __device__ __forceinline__ void weigh_entries(const DistillArgs& a, const Entrie
     }
     const bool any = a.ce || __ballot(found) != 0;
     if (a.k > 0) {
-        float norm;
+        // log p = (u - from)/tau - norm: the difference first, so that no u/tau
+        // overflows where the entries are all the whole distribution
+        float from = 0.0f, norm;
         if (a.teacher_lse) {
             norm = a.teacher_lse[row];
         } else {
-            top = wave_max(top);
+            from = wave_max(top);
             float sum = 0.0f;
             for (int k = lane; k < a.k; k += kWave)
-                if (e.col[k] >= 0) sum += expf(e.logp[k] - top);
-            norm = top + logf(wave_sum(sum));
+                if (e.col[k] >= 0) sum += expf((e.logp[k] - from) * a.inv_tau);
+            norm = logf(wave_sum(sum));
         }
         for (int k = lane; k < a.k; k += kWave) {
-            const float logp = e.logp[k] - norm;
+            const float logp = (e.logp[k] - from) * a.inv_tau - norm;
             const float p = e.col[k] >= 0 ? expf(logp) : 0.0f;
             e.logp[k] = logp;
             e.p[k] = p;
@@ -1094,7 +1081,7 @@ template <typename T>
 __device__ __forceinline__ void load_entries(const DistillArgs& a, const Entries& e, int64_t row,
                                              int label, const T* s)
 {
-    read_entries<T, true>(a, e, row, label, s, 0, a.vocab, threadIdx.x % kWave, kWave);
+    read_entries<T>(a, e, row, label, s, 0, a.vocab, threadIdx.x % kWave, kWave);
     // a lane reads in weigh_entries what it wrote here
     weigh_entries(a, e, row);
 }
@@ -1265,7 +1252,13 @@ __device__ __forceinline__ void put_zeros(T* out, int64_t c0, int64_t c1)
 // that 16 waves on a CU have each.  A block of 1024 threads so keeps 131072
 // bf16 (65536 fp32) logits; what a longer row has beyond that is read again.
 constexpr int kHold = 16;
-// One block per row: the loss, and with GRAD the gradient, the row read once.
+// One block per row: the loss, and with GRAD the gradient, the row read once
+// (8192 x 128256 bf16, an eighth of the rows masked: 3.94 GB in 740 us, 5.3
+// TB/s; copying the rows in this pattern without arithmetic takes 660).
+// Measured and not taken: two blocks of 512 threads on a CU, each holding half
+// its row (865 us); loading the next row as this one's registers become free
+// (840 us, one block a CU for all rows: a row's blocks in dispatch order suit
+// the HBM better).
 // (SHORT: a row may have no whole vector.)
 template <typename T, Terms TM, bool GRAD, int THREADS, int HOLD, bool SHORT>
 __global__ void __launch_bounds__(THREADS, 4) k_distill_row(DistillArgs a, int64_t b0)
@@ -1427,7 +1420,7 @@ __global__ void __launch_bounds__(kPartThreads) k_distill_grad(DistillArgs a, in
         raw[j] = nv == 0 ? Raw<T>::lowest()
                          : held_vector<T>(reinterpret_cast<uint64_t>(s + c0), vector(j), nv);
     const Entries e = entries_at(lds, a);
-    read_entries<T, true>(a, e, row, label, s, c0, c1, threadIdx.x, kPartThreads);
+    read_entries<T>(a, e, row, label, s, c0, c1, threadIdx.x, kPartThreads);
     __syncthreads();
     if (threadIdx.x < kWave) weigh_entries(a, e, row);
     const float rg = a.row_grad ? a.row_grad[row] : 1.0f;

@@ -212,6 +212,24 @@ def test_large_and_constant_logits(dtype):
     p.check("pair")
 
 
+@pytest.mark.parametrize("rows", [3, 513])
+@pytest.mark.parametrize("tau", [0.5, 2.0])
+def test_teacher_entries_all_at_the_lowest_value(rows, tau):
+    """Equal entries are equally likely, at the type's lowest value too."""
+    p = Problem(rows, 200, 5, F32, labels=False, tau=tau)
+    p.u[0] = torch.finfo(F32).min
+    p.u[1] = torch.finfo(F32).max
+    p.ids[:2] = torch.tensor([3, 50, 60, 70, 199]).cuda()
+    o = p.run("step")
+    q = p.u.clone()
+    q[:2] = 0.0                          # the same distribution
+    p.u = q
+    p.check("step")
+    want = p.run("step")
+    # log p: the same five numbers, up to rounding of equal operations
+    assert torch.equal(o["loss"], want["loss"]) and torch.equal(o["grad"], want["grad"])
+
+
 def test_accumulate_and_no_rows():
     p = Problem(9, 100, 4, F32)
     r = p.ref()
