@@ -387,8 +387,8 @@ int embed_lookup(const zs_embed* e, const void* ids, const void* table, void* ou
 
 /* Bytes of device workspace embed_grad needs: the token positions sorted by
  * row (8 bytes a token), the row starts (4 bytes a row) and the partial sums
- * of rows with many tokens (at most 1/4 of an fp32 activation batch).  0 for
- * a NULL or invalid e.  Host only. */
+ * of rows with many tokens (2 D fp32 for every 8 to 64 tokens).  0 for a NULL
+ * or invalid e and above ZS_EMBED_MAX.  Host only. */
 size_t zs_embed_workspace_bytes(const zs_embed* e);
 
 /* The gradient of embed_lookup with respect to the table, dense:
@@ -399,7 +399,8 @@ size_t zs_embed_workspace_bytes(const zs_embed* e);
  * (micro-batches after the first, or a tied table whose head's gradient is
  * there already).  Tokens are sorted by row, stably, and summed in fp32 in an
  * order that depends on the sizes and ids alone (run-to-run deterministic:
- * no floating-point atomics); the result is rounded once to table_dtype.
+ * no floating-point atomics); the result is rounded once to table_dtype.  The
+ * sort reads the ids once for every 512 rows of the table, at least 256 times.
  *   workspace  device, 16-byte aligned, >= zs_embed_workspace_bytes(e) bytes;
  *              contents on entry are ignored.
  * Errors: ZS_ENULL, ZS_EINVAL_EMBED, ZS_EALIGN, ZS_EUNSUPPORTED (more than
@@ -435,9 +436,9 @@ typedef struct zs_targets {
 } zs_targets;
 
 /* Bytes of device workspace distill_loss and distill_loss_grad need: a flag
- * per row, and, where there are too few rows to fill the GPU, the partial
- * statistics of the parts each row is cut into.  0 for a NULL or invalid d.
- * Host only. */
+ * per row, 16 bytes for each part a row may be cut into (2048 to 16384
+ * logits), and below 512 rows 4 (k + 1) bytes a row.  0 for a NULL or invalid
+ * d.  Host only. */
 size_t zs_distill_workspace_bytes(const zs_distill* d);
 
 /* Row losses.  With s a row's logits, K its teacher entries, in fp32:
@@ -474,10 +475,12 @@ int distill_loss(const zs_distill* d, const void* logits, const zs_targets* t, f
 int distill_grad(const zs_distill* d, const void* logits, const zs_targets* t,
                  const float* lse_in, const float* row_grad, void* grad_out, void* stream);
 
-/* Both in one call, reading the logits once where a row's part fits the
- * registers: the loss is usually the last operator of the forward pass, so
- * its gradient can be taken there.  Arguments and errors as above; lse_out
- * may be NULL. */
+/* Both in one call: the loss is usually the last operator of the forward
+ * pass, so its gradient can be taken there.  From 512 rows on the logits are
+ * read once (of a row, the first 131072 in bf16, 65536 in fp32).  Arguments
+ * and errors as above; lse_out may be NULL.  The loss may differ from
+ * distill_loss's in its last bits, the gradient from distill_grad's by what
+ * rounding lse to fp32 takes. */
 int distill_loss_grad(const zs_distill* d, const void* logits, const zs_targets* t,
                       float* loss_out, float* lse_out, const float* row_grad, void* grad_out,
                       float* loss_sum, int64_t* counted, int32_t accumulate, void* workspace,
