@@ -212,6 +212,33 @@ def test_large_and_constant_logits(dtype):
     p.check("pair")
 
 
+@pytest.mark.parametrize("dtype,vocab", [(BF16, 140003), (F32, 70001), (BF16, 131072), (F32, 40005)])
+@pytest.mark.parametrize("alpha,tau", [(1.0, 1.0), (0.5, 2.0), (0.5, 1.0)])
+def test_long_rows_one_block_each(dtype, vocab, alpha, tau):
+    """Rows as long as a block holds, and longer; among them one with masked
+    columns, one of equal lowest values, one far from zero."""
+    rows = 512
+    p = Problem(rows, vocab, 20, dtype, alpha=alpha, tau=tau, pad=1)
+    use = [0, 3, 200, 201, 510, 511]
+    p.labels[:] = -100
+    for t in use:
+        p.labels[t] = 11 * t % vocab
+    low = torch.finfo(dtype).min
+    p.s[3, 100:vocab - 7] = low
+    p.ids[3] = torch.arange(20).cuda()
+    p.labels[3] = 5
+    p.s[200] = low
+    p.s[201] = (p.s[201].float() + 3e5).to(dtype)
+    p.s[510, ::3] = -math.inf
+    p.ids[510] = 3 * torch.arange(20).cuda() + 1
+    p.labels[510] = 31
+    ref = p.ref()
+    a = p.check("step", ref)
+    p.check("pair", ref)
+    b = p.run("step", in_place=True)
+    assert torch.equal(a["grad"], b["grad"]) and torch.equal(a["loss"], b["loss"])
+
+
 @pytest.mark.parametrize("rows", [3, 513])
 @pytest.mark.parametrize("tau", [0.5, 2.0])
 def test_teacher_entries_all_at_the_lowest_value(rows, tau):

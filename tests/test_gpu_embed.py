@@ -182,9 +182,11 @@ def test_grad_orders(kind, tokens, rows, dim, accumulate):
 @pytest.mark.parametrize("table_dtype", [BF16, F32])
 @pytest.mark.parametrize("accumulate", [False, True])
 @pytest.mark.parametrize("pad", [0, 3])
-def test_grad_types_pitches_ranges(act_dtype, table_dtype, accumulate, pad):
-    ids = make_ids("zipf", 2051, 900, 12, torch.int32)
-    run_grad(ids, 2051, 257, 519, act_dtype, table_dtype, accumulate, first=3, scale=22.5, pad=pad)
+@pytest.mark.parametrize("tokens", [64, 65, 2051])
+def test_grad_types_pitches_ranges(act_dtype, table_dtype, accumulate, pad, tokens):
+    ids = make_ids("zipf", tokens, 900, 12, torch.int32)
+    run_grad(ids, tokens, 257, 519, act_dtype, table_dtype, accumulate, first=3, scale=22.5,
+             pad=pad)
 
 
 @pytest.mark.parametrize("tokens,rows,dim", [(30011, 700, 72), (70001, 260, 40), (5000, 260000, 24),
@@ -201,6 +203,27 @@ def test_grad_sort_lists_overflow(kind, tokens, rows):
     if kind == "runs":
         ids[1000:9000], ids[30000:52000] = 77, 512
     run_grad(ids, tokens, rows, 24, BF16, F32, False)
+
+
+def test_grad_many_tokens():
+    """A million tokens into a quarter of a million rows, against torch's own
+    64-bit index_add on the GPU."""
+    tokens, rows, dim = 1 << 20, 1 << 18, 8
+    g = torch.Generator(device="cuda").manual_seed(5)
+    ids = torch.randint(-5, rows + 5, (tokens,), generator=g, device="cuda")
+    ids[::16] = 77
+    act = torch.randn((tokens, dim), generator=g, device="cuda")
+    e = Z.make_embed(tokens, rows, dim, table_dtype=Z.ZS_F32, act_dtype=Z.ZS_F32)
+    ws = torch.empty(Z.zs_embed_workspace_bytes(e), dtype=torch.uint8, device="cuda")
+    grad = torch.full((rows, dim), 3.0, device="cuda")
+    Z.embed_grad(e, ids, act, grad, ws)
+    here = (ids >= 0) & (ids < rows)
+    want, size = (torch.zeros((rows, dim), dtype=torch.float64, device="cuda") for _ in range(2))
+    want.index_add_(0, ids[here], act[here].double())
+    size.index_add_(0, ids[here], act[here].double().abs())
+    count = torch.bincount(ids[here], minlength=rows)
+    off = (grad.double() - want).abs()
+    assert bool((off <= embed_grad_bound(want, size, count, None, F32)).all())
 
 
 def test_grad_without_tokens():
