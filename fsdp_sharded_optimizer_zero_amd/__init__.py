@@ -240,14 +240,30 @@ def _out_len(s: "zs_shard") -> int:
     return s.shard_len + (s.shard_offset if s.out_mode == ZS_OUT_GATHER else 0)
 
 
+_torch = None
+
+
+def _cuda():
+    """torch.cuda, imported by the first call that needs it."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch.cuda
+
+
+def _current_stream(device) -> int:
+    # the same handle without building a Stream object (2.7 us a call)
+    raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device) if raw is not None else _torch.cuda.current_stream().cuda_stream
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        # the same handle without building a Stream object (2.7 us a call)
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None and torch.cuda.is_initialized():
-            return raw(torch.cuda.current_device())
-        return torch.cuda.current_stream().cuda_stream
+        cuda = _cuda()
+        if cuda.is_initialized():
+            return _current_stream(cuda.current_device())
+        return cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -414,8 +430,7 @@ _ELEM = {ZS_BF16: _B16, ZS_F32: _F32}
 def _rows_ptr(t, what: str, dtypes, rows: int, width: int, pitch: int):
     """As _ptr for `rows` rows of `width` elements, `pitch` apart: either a
     contiguous tensor that holds them, or a 2-D view with that row stride."""
-    if t is not None and not isinstance(t, int) and hasattr(t, "stride") and t.dim() == 2 \
-            and not t.is_contiguous():
+    if hasattr(t, "is_contiguous") and not t.is_contiguous() and t.dim() == 2:
         if t.shape[0] < rows or t.shape[1] < width or (width > 1 and t.stride(1) != 1) \
                 or (rows > 1 and t.stride(0) != pitch):
             raise ValueError(f"{what}: shape {tuple(t.shape)} with strides {t.stride()}, the call "
@@ -428,14 +443,14 @@ def _rows_ptr(t, what: str, dtypes, rows: int, width: int, pitch: int):
 def _stream_on(stream, *tensors):
     """The stream's handle.  The library works on the current device: tensors
     of another one are refused (raw addresses are not looked at)."""
-    import torch
-    if not torch.cuda.is_initialized():
+    cuda = _cuda()
+    if not cuda.is_initialized():
         return _stream(stream)          # no GPU tensor yet: _ptr refuses the others
-    device = torch.cuda.current_device()
+    device = cuda.current_device()
     for t in tensors:
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != device:
+        if t is not None and not isinstance(t, int) and t.get_device() != device:
             raise ValueError(f"a tensor on GPU {t.get_device()}: the current device is {device}")
-    return _stream(stream)
+    return _current_stream(device) if stream is None else _stream(stream)
 
 
 def _sized(workspace, workspace_bytes, need: int):
