@@ -670,16 +670,16 @@ __global__ void __launch_bounds__(kEmbedThreads)
     float acc[N] = {}, old[N] = {};
     if constexpr (ADD) read_row<GT, N>(a, r, c, old);
     while (same) {
-        typename Raw<AT>::V x[4] = {};
+        typename Raw<AT>::V x[kSumUnroll] = {};
         uint64_t m = same;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kSumUnroll; ++u) {
             if (m == 0) continue;
             x[u] = load_raw(src + __builtin_ctzll(m) * a.act_pitch, width);
             m &= m - 1;
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kSumUnroll; ++u) {
             if (same == 0) continue;
             float v[N];
             Raw<AT>::widen(x[u], v);
