@@ -927,28 +927,57 @@ __device__ __forceinline__ bool held_stats(typename Raw<T>::V (&raw)[HOLD], Own 
     return true;
 }
 
-// The statistics of columns [c0, c1) of a row, over the block's threads, in
-// one pass with the running maximum.
-template <typename T, Terms TM, int THREADS, int UNROLL>
-__device__ __forceinline__ Stat scan(Stat s, const T* row, int64_t c0, int64_t c1, float c)
+// Elements of a row before its first 16-byte boundary, where its vectors
+// begin: a bf16 row of odd length read from its start would take every vector
+// across a boundary (5341 x 50257: 248 us).
+template <typename T>
+__device__ __forceinline__ int row_head(const T* row, int64_t vocab)
+{
+    const int n = static_cast<int>((16 - (reinterpret_cast<uint64_t>(row) & 15)) & 15) /
+                  static_cast<int>(sizeof(T));
+    return static_cast<int>(n < vocab ? n : vocab);
+}
+
+// The statistics of a row's columns [0, head) and of its vectors from c0 to
+// c1 and the elements behind them, over the block's threads, in one pass with
+// the running maximum, BATCH loads under way.
+template <typename T, Terms TM, int THREADS, int BATCH>
+__device__ __forceinline__ Stat scan(Stat s, const T* row, int head, int64_t c0, int64_t c1,
+                                     float c)
 {
     constexpr int N = Raw<T>::N;
     const int nv = static_cast<int>((c1 - c0) / N);
     const typename Raw<T>::M* p = reinterpret_cast<const typename Raw<T>::M*>(row + c0);
-#pragma unroll UNROLL
-    for (int v = threadIdx.x; v < nv; v += THREADS) {
-        float x[N];
-        Raw<T>::widen(p[v], x);
-        const float m = max_n<N>(x, s.m);
+    for (int v0 = threadIdx.x; v0 - static_cast<int>(threadIdx.x) < nv; v0 += BATCH * THREADS) {
+        typename Raw<T>::V raw[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j)
+            raw[j] = p[v0 + j * THREADS < nv ? v0 + j * THREADS : nv - 1];
+        float m = s.m;
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            if (v0 + j * THREADS >= nv) raw[j] = Raw<T>::lowest();
+            float x[N];
+            Raw<T>::widen(raw[j], x);
+            m = max_n<N>(x, m);
+        }
         if (m > s.m) rescale<TM>(s, m, c);
-        add_exp<TM, N>(s, x, c);
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            float x[N];
+            forget(raw[j]);
+            Raw<T>::widen(raw[j], x);
+            add_exp<TM, N>(s, x, c);
+        }
     }
-    const int64_t e = c0 + static_cast<int64_t>(nv) * N + threadIdx.x;
-    if (e < c1) {
-        const float x = widen(row[e]);
+    const auto one = [&](int64_t col) {
+        const float x = widen(row[col]);
         if (x > s.m) rescale<TM>(s, x, c);
         add_exp<TM, 1>(s, &x, c);
-    }
+    };
+    if (static_cast<int>(threadIdx.x) < head) one(threadIdx.x);
+    const int64_t e = c0 + static_cast<int64_t>(nv) * N + threadIdx.x;
+    if (e < c1) one(e);
     return s;
 }
 
@@ -1183,31 +1212,35 @@ __device__ __forceinline__ void put_held_slopes(T* out, typename Raw<T>::V (&raw
     }
 }
 
-template <typename T, Terms TM>
-__device__ __forceinline__ void put_slopes(T* out, typename Raw<T>::V raw, const Slope& g,
-                                           float c)
-{
-    constexpr int N = Raw<T>::N;
-    float x[N];
-    Raw<T>::widen(raw, x);
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = slope_at<TM>(g, x[i], c);
-    store_n<N>(out, x);
-}
-
-// The gradient of columns [c0, c1) of a row.
-template <typename T, Terms TM, int THREADS, int UNROLL>
-__device__ __forceinline__ void put_columns(const Slope& g, const T* row, T* out, int64_t c0,
-                                            int64_t c1, float c)
+// The gradient of a row's columns [0, head) and of its vectors from c0 to c1
+// and the elements behind them.
+template <typename T, Terms TM, int THREADS, int BATCH>
+__device__ __forceinline__ void put_columns(const Slope& g, const T* row, T* out, int head,
+                                            int64_t c0, int64_t c1, float c)
 {
     constexpr int N = Raw<T>::N;
     const int nv = static_cast<int>((c1 - c0) / N);
     const typename Raw<T>::M* p = reinterpret_cast<const typename Raw<T>::M*>(row + c0);
-#pragma unroll UNROLL
-    for (int v = threadIdx.x; v < nv; v += THREADS)
-        put_slopes<T, TM>(out + c0 + static_cast<int64_t>(v) * N, p[v], g, c);
+    for (int v0 = threadIdx.x; v0 - static_cast<int>(threadIdx.x) < nv; v0 += BATCH * THREADS) {
+        typename Raw<T>::V raw[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j)
+            raw[j] = p[v0 + j * THREADS < nv ? v0 + j * THREADS : nv - 1];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            const int v = v0 + j * THREADS;
+            if (v >= nv) continue;
+            float x[N];
+            Raw<T>::widen(raw[j], x);
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = slope_at<TM>(g, x[i], c);
+            store_nt<N>(out + c0 + static_cast<int64_t>(v) * N, x);
+        }
+    }
+    const auto one = [&](int64_t col) { put(out + col, slope_at<TM>(g, widen(row[col]), c)); };
+    if (static_cast<int>(threadIdx.x) < head) one(threadIdx.x);
     const int64_t e = c0 + static_cast<int64_t>(nv) * N + threadIdx.x;
-    if (e < c1) put(out + e, slope_at<TM>(g, widen(row[e]), c));
+    if (e < c1) one(e);
 }
 
 // After a barrier behind the columns: the entries' columns once more, with
@@ -1241,9 +1274,12 @@ __device__ __forceinline__ void put_zeros(T* out, int64_t c0, int64_t c1)
 {
     constexpr int N = Raw<T>::N;
     const float z[N] = {};
+    const int head = row_head(out + c0, c1 - c0);
+    if (static_cast<int>(threadIdx.x) < head) put(out + c0 + threadIdx.x, 0.0f);
+    c0 += head;
     const int nv = static_cast<int>((c1 - c0) / N);
     for (int v = threadIdx.x; v < nv; v += THREADS)
-        store_n<N>(out + c0 + static_cast<int64_t>(v) * N, z);
+        store_nt<N>(out + c0 + static_cast<int64_t>(v) * N, z);
     const int64_t e = c0 + static_cast<int64_t>(nv) * N + threadIdx.x;
     if (e < c1) put(out + e, 0.0f);
 }
@@ -1276,21 +1312,28 @@ __global__ void __launch_bounds__(THREADS, 4) k_distill_row(DistillArgs a, int64
         if constexpr (GRAD) put_zeros<T, THREADS>(out, 0, a.vocab);
         return;
     }
-    const int64_t vectors = a.vocab / N;
+    const int head = row_head(s, a.vocab);
+    const int64_t vectors = (a.vocab - head) / N;
     const int nv = static_cast<int>(vectors < HOLD * THREADS ? vectors : HOLD * THREADS);
-    const int64_t held = static_cast<int64_t>(nv) * N;
+    const int64_t behind = head + static_cast<int64_t>(nv) * N;     // the held vectors
     int tid = threadIdx.x;
     typename Raw<T>::V raw[HOLD];
     const auto vector = [&](int j) { return tid + j * THREADS; };
 #pragma unroll
     for (int j = 0; j < HOLD; ++j)
         raw[j] = SHORT && nv == 0 ? Raw<T>::lowest()
-                                  : held_vector<T>(reinterpret_cast<uint64_t>(s), vector(j), nv);
+                                  : held_vector<T>(reinterpret_cast<uint64_t>(s + head), vector(j), nv);
     const Entries e = entries_at(lds, a);
-    if (threadIdx.x < kWave) load_entries<T>(a, e, row, label, s);
+    if (a.k <= kWave) {
+        if (threadIdx.x < kWave) load_entries<T>(a, e, row, label, s);
+    } else {
+        read_entries<T>(a, e, row, label, s, 0, a.vocab, threadIdx.x, THREADS);
+        __syncthreads();
+        if (threadIdx.x < kWave) weigh_entries(a, e, row);
+    }
     Stat st = {kLowest, 0.0f, 0.0f};
     const bool sums = held_stats<T, TM>(raw, [&](int j) { return vector(j) < nv; }, c, st);
-    st = scan<T, TM, THREADS, 4>(st, s, sums ? held : 0, a.vocab, c);
+    st = scan<T, TM, THREADS, 4>(st, s, head, sums ? behind : head, a.vocab, c);
     st = block_join<TM, THREADS>(st, c, red);
     if (threadIdx.x / kWave == 1) put_loss(a, e, row, st, e.s);
     if constexpr (GRAD) {
@@ -1302,8 +1345,8 @@ __global__ void __launch_bounds__(THREADS, 4) k_distill_row(DistillArgs a, int64
         const Slope g = slope_of(a, *e.mass, st, rg, TM == kSame);
         const bool fma = slope_fma<TM>(g, c);
         forget(tid);
-        if (fma) put_held_slopes<T, TM>(out, raw, vector, nv, fma_slope(g, c), c);
-        put_columns<T, TM, THREADS, 4>(g, s, out, fma ? held : 0, a.vocab, c);
+        if (fma) put_held_slopes<T, TM>(out + head, raw, vector, nv, fma_slope(g, c), c);
+        put_columns<T, TM, THREADS, 4>(g, s, out, head, fma ? behind : head, a.vocab, c);
         __syncthreads();
         put_entries<T, TM, THREADS>(a, e, g, rg, out, 0, a.vocab, c);
     }
@@ -1316,12 +1359,28 @@ __global__ void __launch_bounds__(THREADS, 4) k_distill_row(DistillArgs a, int64
 // the loss 60 + 7 us, its gradient 138; a block a row: 92 and 177).
 constexpr int kPartThreads = kDistillPartThreads;
 
-// Vectors of a part that lie in the row.
+// A part of a row: its columns [c0, c1), of which `head` lie before the row's
+// vectors (the first part's) and nv vectors from `from` on are held.
+struct Part {
+    int64_t c0, c1, from;
+    int head, nv;
+};
 template <typename T, int HOLD>
-__device__ __forceinline__ int part_vectors(int64_t c0, int64_t vocab)
+__device__ __forceinline__ Part part_of(const DistillArgs& a, const T* row, int part)
 {
-    const int64_t nv = (vocab - c0) / Raw<T>::N;
-    return static_cast<int>(nv < HOLD * kPartThreads ? nv : HOLD * kPartThreads);
+    const int head = row_head(row, a.vocab);
+    const auto bound = [&](int64_t i) {
+        const int64_t c = head + i * a.part_cols;
+        return i >= a.splits || c > a.vocab ? a.vocab : c;
+    };
+    Part p;
+    p.from = bound(part);
+    p.c0 = part == 0 ? 0 : p.from;
+    p.c1 = bound(part + 1);
+    p.head = part == 0 ? head : 0;
+    const int64_t nv = (p.c1 - p.from) / Raw<T>::N;
+    p.nv = static_cast<int>(nv < HOLD * kPartThreads ? nv : HOLD * kPartThreads);
+    return p;
 }
 
 // The part's statistics, and, if a gradient follows (which may overwrite
@@ -1331,30 +1390,29 @@ __global__ void __launch_bounds__(kPartThreads) k_distill_parts(DistillArgs a, i
 {
     __shared__ float red[kWaves(kPartThreads) * 3];
     const int64_t block = b0 + blockIdx.x, row = block / a.splits;
-    const int64_t c0 = (block - row * a.splits) * a.part_cols;
     int label;
     if (!label_counts(a, row, &label)) return;
-    const int64_t c1 = c0 + a.part_cols < a.vocab ? c0 + a.part_cols : a.vocab;
     const T* s = static_cast<const T*>(a.logits) + row * a.logits_pitch;
     const float c = a.inv_tau * kLog2e;
-    const int nv = part_vectors<T, HOLD>(c0, a.vocab);
+    const Part p = part_of<T, HOLD>(a, s, static_cast<int>(block - row * a.splits));
     const auto vector = [&](int j) { return static_cast<int>(threadIdx.x) + j * kPartThreads; };
     typename Raw<T>::V raw[HOLD];
 #pragma unroll
     for (int j = 0; j < HOLD; ++j)
-        raw[j] = nv == 0 ? Raw<T>::lowest()
-                         : held_vector<T>(reinterpret_cast<uint64_t>(s + c0), vector(j), nv);
+        raw[j] = p.nv == 0 ? Raw<T>::lowest()
+                           : held_vector<T>(reinterpret_cast<uint64_t>(s + p.from), vector(j),
+                                            p.nv);
     if (a.grad) {
         for (int k = threadIdx.x; k < a.k + a.ce; k += kPartThreads) {
             float u;
             const int col = k < a.k ? read_entry(a, row * a.k + k, &u) : label;
-            if (col >= c0 && col < c1) a.picked[row * (a.k + 1) + k] = widen(s[col]);
+            if (col >= p.c0 && col < p.c1) a.picked[row * (a.k + 1) + k] = widen(s[col]);
         }
     }
     Stat st = {kLowest, 0.0f, 0.0f};
-    const bool sums = held_stats<T, TM>(raw, [&](int j) { return vector(j) < nv; }, c, st);
-    const int64_t rest = c0 + (sums ? static_cast<int64_t>(nv) * Raw<T>::N : 0);
-    st = scan<T, TM, kPartThreads, 1>(st, s, rest, c1, c);
+    const bool sums = held_stats<T, TM>(raw, [&](int j) { return vector(j) < p.nv; }, c, st);
+    const int64_t rest = p.from + (sums ? static_cast<int64_t>(p.nv) * Raw<T>::N : 0);
+    st = scan<T, TM, kPartThreads, 2>(st, s, p.head, rest, p.c1, c);
     st = block_join<TM, kPartThreads>(st, c, red);
     if (threadIdx.x == 0)
         *reinterpret_cast<float4*>(a.parts + block * kDistillPart) =
@@ -1404,23 +1462,22 @@ __global__ void __launch_bounds__(kPartThreads) k_distill_grad(DistillArgs a, in
     const float c = a.inv_tau * kLog2e;
     const T* s = static_cast<const T*>(a.logits) + row * a.logits_pitch;
     T* out = static_cast<T*>(a.grad) + row * a.grad_pitch;
-    const int64_t c0 = part * a.part_cols;
-    const int64_t c1 = c0 + a.part_cols < a.vocab ? c0 + a.part_cols : a.vocab;
+    const Part p = part_of<T, HOLD>(a, s, part);
     int label;
     if (!label_counts(a, row, &label)) {
         if (!FROM_LSE && part == 0) put_no_loss(a, row);
-        put_zeros<T, kPartThreads>(out, c0, c1);
+        put_zeros<T, kPartThreads>(out, p.c0, p.c1);
         return;
     }
-    const int nv = part_vectors<T, HOLD>(c0, a.vocab);
     const auto vector = [&](int j) { return static_cast<int>(threadIdx.x) + j * kPartThreads; };
     typename Raw<T>::V raw[HOLD];
 #pragma unroll
     for (int j = 0; j < HOLD; ++j)
-        raw[j] = nv == 0 ? Raw<T>::lowest()
-                         : held_vector<T>(reinterpret_cast<uint64_t>(s + c0), vector(j), nv);
+        raw[j] = p.nv == 0 ? Raw<T>::lowest()
+                           : held_vector<T>(reinterpret_cast<uint64_t>(s + p.from), vector(j),
+                                            p.nv);
     const Entries e = entries_at(lds, a);
-    read_entries<T>(a, e, row, label, s, c0, c1, threadIdx.x, kPartThreads);
+    read_entries<T>(a, e, row, label, s, p.c0, p.c1, threadIdx.x, kPartThreads);
     __syncthreads();
     if (threadIdx.x < kWave) weigh_entries(a, e, row);
     const float rg = a.row_grad ? a.row_grad[row] : 1.0f;
@@ -1429,7 +1486,7 @@ __global__ void __launch_bounds__(kPartThreads) k_distill_grad(DistillArgs a, in
     __syncthreads();
     if (e.mass[1] == 0.0f) {
         if (!FROM_LSE && part == 0) put_no_loss(a, row);
-        put_zeros<T, kPartThreads>(out, c0, c1);
+        put_zeros<T, kPartThreads>(out, p.c0, p.c1);
         return;
     }
     Slope g;
@@ -1448,13 +1505,13 @@ __global__ void __launch_bounds__(kPartThreads) k_distill_grad(DistillArgs a, in
         g = slope_of(a, *e.mass, st, rg, TM == kSame);
     }
     const bool fma = slope_fma<TM>(g, c);
-    if (fma) put_held_slopes<T, TM>(out + c0, raw, vector, nv, fma_slope(g, c), c);
-    const int64_t rest = c0 + (fma ? static_cast<int64_t>(nv) * Raw<T>::N : 0);
-    put_columns<T, TM, kPartThreads, 1>(g, s, out, rest, c1, c);
+    if (fma) put_held_slopes<T, TM>(out + p.from, raw, vector, p.nv, fma_slope(g, c), c);
+    const int64_t rest = p.from + (fma ? static_cast<int64_t>(p.nv) * Raw<T>::N : 0);
+    put_columns<T, TM, kPartThreads, 2>(g, s, out, p.head, rest, p.c1, c);
     if (!FROM_LSE && part == 0 && threadIdx.x / kWave == 1)
         put_loss(a, e, row, st, a.picked + row * (a.k + 1));
     __syncthreads();
-    put_entries<T, TM, kPartThreads>(a, e, g, rg, out, c0, c1, c);
+    put_entries<T, TM, kPartThreads>(a, e, g, rg, out, p.c0, p.c1, c);
 }
 
 constexpr int kTotalThreads = 1024;
