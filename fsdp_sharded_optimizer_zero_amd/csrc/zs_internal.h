@@ -205,6 +205,7 @@ struct DistillArgs {
     int64_t part_cols;      // columns of one part (a multiple of 8)
     int32_t splits;         // parts a row is cut into
     int32_t k;              // 0 where alpha is 0
+    int32_t entry_bits;     // log2 of the hash chains of the entries (set per launch)
     int32_t accumulate;
     int32_t f32, teacher_f32, id64, kd, ce;
     float inv_tau;          // 1/tau

@@ -989,12 +989,34 @@ struct Entries {
     float* p;
     float* s;
     float* mass;    // sum of p, and behind it 1 if the row counts, else 0
+    int32_t* heads; // more than 64 entries: the last entry of each hash of a
+    int32_t* next;  // column, and the entry before each with its hash (-1: none)
     int n;          // K, or K + 1 with the label
+    int hash_bits;
 };
+
+// Up to kWave entries, one wave reads them all and a column's others are
+// found by looking through them; more are read by the whole block, and chained
+// by a hash of their column.
+__device__ __forceinline__ uint32_t entry_hash(const Entries& e, int col)
+{
+    return static_cast<uint32_t>(col) * 2654435769u >> (32 - e.hash_bits);
+}
 
 // Entries a row can hold, a multiple of 4.
 __host__ __device__ constexpr int entry_slots(int k) { return (k + 1 + 3) / 4 * 4; }
-size_t entry_bytes(int k) { return static_cast<size_t>(entry_slots(k)) * 16 + 16; }
+// log2 of the chains of K > 64 entries: at least K.
+__host__ __device__ constexpr int entry_hash_bits(int k)
+{
+    int b = 7;
+    while ((1 << b) < k) ++b;
+    return b;
+}
+size_t entry_bytes(int k)
+{
+    const size_t chains = k > kWave ? (size_t(1) << entry_hash_bits(k)) + entry_slots(k) : 0;
+    return static_cast<size_t>(entry_slots(k)) * 16 + 16 + chains * 4;
+}
 
 __device__ __forceinline__ Entries entries_at(char* lds, const DistillArgs& a)
 {
@@ -1005,6 +1027,9 @@ __device__ __forceinline__ Entries entries_at(char* lds, const DistillArgs& a)
     e.p = e.logp + slots;
     e.s = e.p + slots;
     e.mass = e.s + slots;
+    e.hash_bits = a.entry_bits;
+    e.heads = reinterpret_cast<int32_t*>(e.mass + 4);
+    e.next = e.heads + (1 << a.entry_bits);
     e.n = a.k + a.ce;
     return e;
 }
@@ -1061,7 +1086,18 @@ __device__ __forceinline__ void read_entries(const DistillArgs& a, const Entries
         e.col[k] = col;
         e.logp[k] = u;
         if (col >= c0 && col < c1) e.s[k] = widen(s[col]);
+        if (a.k > kWave)
+            e.next[k] = col < 0 ? -1 : atomicExch(e.heads + entry_hash(e, col), k);
     }
+}
+
+// Before read_entries, by the whole block, with a barrier behind it.
+template <int THREADS>
+__device__ __forceinline__ void clear_chains(const DistillArgs& a, const Entries& e)
+{
+    if (a.k <= kWave) return;
+    for (int i = threadIdx.x; i < 1 << e.hash_bits; i += THREADS) e.heads[i] = -1;
+    __syncthreads();
 }
 
 // One wave's work once they are there: log p, p and their sum.  The block's
@@ -1253,16 +1289,33 @@ __device__ __forceinline__ void put_entries(const DistillArgs& a, const Entries&
     for (int k = threadIdx.x; k < e.n; k += THREADS) {
         const int col = e.col[k];
         if (col < c0 || col >= c1) continue;
+        const auto share = [&](int j) {
+            return row_grad * (j < a.k ? a.grad_kd * e.p[j] : a.grad_ce);
+        };
         float take = 0.0f;
         bool first = true;
-        for (int j = 0; j < e.n; j += 4) {
-            const int4 o = *reinterpret_cast<const int4*>(e.col + j);
-            if (!(o.x == col | o.y == col | o.z == col | o.w == col)) continue;
+        int same = 3;
+        if (a.k > kWave) {
+            // one or two entries of the column: their sum has no order
+            same = 0;
+            for (int j = e.heads[entry_hash(e, col)]; j >= 0; j = e.next[j]) {
+                if (e.col[j] != col) continue;
+                first = first && j >= k;
+                take += ++same <= 2 ? share(j) : 0.0f;
+            }
+        }
+        if (same > 2) {
+            take = 0.0f;
+            first = true;
+            for (int j = 0; j < e.n; j += 4) {
+                const int4 o = *reinterpret_cast<const int4*>(e.col + j);
+                if (!(o.x == col | o.y == col | o.z == col | o.w == col)) continue;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if ((i == 0 ? o.x : i == 1 ? o.y : i == 2 ? o.z : o.w) != col) continue;
-                first = first && j + i >= k;
-                take += row_grad * (j + i < a.k ? a.grad_kd * e.p[j + i] : a.grad_ce);
+                for (int i = 0; i < 4; ++i) {
+                    if ((i == 0 ? o.x : i == 1 ? o.y : i == 2 ? o.z : o.w) != col) continue;
+                    first = first && j + i >= k;
+                    take += share(j + i);
+                }
             }
         }
         if (first) put(out + col, slope_at<TM>(g, e.s[k], c) - take);
@@ -1327,6 +1380,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_distill_row(DistillArgs a, int64
     if (a.k <= kWave) {
         if (threadIdx.x < kWave) load_entries<T>(a, e, row, label, s);
     } else {
+        clear_chains<THREADS>(a, e);
         read_entries<T>(a, e, row, label, s, 0, a.vocab, threadIdx.x, THREADS);
         __syncthreads();
         if (threadIdx.x < kWave) weigh_entries(a, e, row);
@@ -1447,6 +1501,7 @@ __global__ void __launch_bounds__(kWave) k_distill_loss(DistillArgs a, int64_t b
         return;
     }
     const Entries e = entries_at(lds, a);
+    clear_chains<kWave>(a, e);
     load_entries<T>(a, e, row, label, static_cast<const T*>(a.logits) + row * a.logits_pitch);
     put_loss(a, e, row, join_parts<TM>(a, row, a.inv_tau * kLog2e), e.s);
 }
@@ -1477,6 +1532,7 @@ __global__ void __launch_bounds__(kPartThreads) k_distill_grad(DistillArgs a, in
                            : held_vector<T>(reinterpret_cast<uint64_t>(s + p.from), vector(j),
                                             p.nv);
     const Entries e = entries_at(lds, a);
+    clear_chains<kPartThreads>(a, e);
     read_entries<T>(a, e, row, label, s, p.c0, p.c1, threadIdx.x, kPartThreads);
     __syncthreads();
     if (threadIdx.x < kWave) weigh_entries(a, e, row);
@@ -1729,6 +1785,7 @@ int enqueue_distill_loss(DistillArgs a, bool with_grad, void* stream)
     const DistillShape s = distill_shape(a.rows, a.vocab, a.f32);
     a.splits = s.splits;
     a.part_cols = s.part_cols;
+    a.entry_bits = entry_hash_bits(a.k);
     int rc = ZS_OK;
     if (a.rows > 0)
         rc = by_type(a, [&](auto tag, auto terms) {
@@ -1747,6 +1804,7 @@ int enqueue_distill_grad(DistillArgs a, void* stream)
     const DistillShape s = distill_shape(a.rows, a.vocab, a.f32);
     a.splits = s.splits;
     a.part_cols = s.part_cols;
+    a.entry_bits = entry_hash_bits(a.k);
     return by_type(a, [&](auto tag, auto terms) {
         return distill_grad_t<decltype(tag), decltype(terms)::value>(a, s, st);
     });

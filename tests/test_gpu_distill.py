@@ -152,6 +152,24 @@ def test_most_entries_and_repeats(rows, k):
         Problem(rows, vocab, k, F32, tau=2.0, alpha=0.5).check("step")
 
 
+@pytest.mark.parametrize("rows", [3, 600])
+@pytest.mark.parametrize("k", [63, 64, 65, 127, 128, 129, 300])
+def test_entries_past_one_wave(rows, k):
+    """Columns once, twice and more often, and the same bits on every run."""
+    for vocab, dtype in ((101, F32), (20011, BF16), (40009, F32)):
+        p = Problem(rows, vocab, k, dtype, tau=2.0, alpha=0.5, pad=1)
+        p.ids[:, k // 2] = p.ids[:, 0]                     # a pair of every row's
+        p.ids[:, k // 3] = p.ids[:, 1]
+        p.ids[:, k - 1] = p.ids[:, 1]                      # and three of a column
+        keep = p.labels >= 0
+        keep &= p.labels < vocab
+        p.labels[keep] = p.ids[keep, 2].clamp(0, vocab - 1)  # the label's is an entry's too
+        ref = p.ref()
+        for calls in ("pair", "step"):
+            a, b = p.check(calls, ref), p.run(calls)
+            assert torch.equal(a["grad"], b["grad"]) and torch.equal(a["loss"], b["loss"])
+
+
 @pytest.mark.parametrize("rows", [5, 600])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("calls", ["pair", "step"])
