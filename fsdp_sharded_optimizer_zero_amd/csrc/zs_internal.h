@@ -221,16 +221,22 @@ constexpr int kDistillPart = 4;
 // holds in registers at `hold` 16-byte vectors a thread: 8, or 2 where 8 would
 // make too few blocks to fill the GPU.
 //  - The gradient from saved statistics always runs in parts.
-//  - The loss runs a block a row where a block of 256 threads holds the row,
-//    otherwise in parts, then one wave a row.
 //  - Loss and gradient in one call run a block a row (reading the logits
-//    once) from kDistillRows rows on, or where a row is one part; fewer rows
-//    would leave CUs idle, and run in parts, twice.
+//    once) from kDistillRows rows on, or where a row is at most kDistillShort
+//    vectors; fewer rows would leave CUs idle, and run in parts, twice (bf16,
+//    a block a row against parts: 511 x 128256 56 us and 75, 128 x 128256 24
+//    and 34, 64 x 128256 23 and 22, 8 x 128256 22 and 13, 8 x 8192 12 and 14;
+//    the one size where parts win above the bound, 320 x 262144, 99 and 88).
+//  - The loss runs a block a row where that does and a block of 256 threads
+//    holds the row (then both calls' losses are the same bits; 511 x 32000 and
+//    its gradient 33 us, in parts 37), otherwise in parts, then one wave a
+//    row.
 constexpr int kDistillPartThreads = 256;
 constexpr int kDistillHold = 8;
 constexpr int kDistillFewHold = 2;
 constexpr int64_t kDistillBlocks = 2048;    // 8 blocks of 4 waves on each of 256 CUs
-constexpr int64_t kDistillRows = 512;
+constexpr int64_t kDistillRows = 128;
+constexpr int64_t kDistillShort = 1024;     // 4 vectors for each of 256 threads
 struct DistillShape {
     int32_t splits;         // parts of a row
     int32_t hold;
@@ -249,8 +255,8 @@ inline DistillShape distill_shape(int64_t rows, int64_t vocab, bool f32)
     s.hold = rows * parts(kDistillHold) >= kDistillBlocks ? kDistillHold : kDistillFewHold;
     s.splits = static_cast<int32_t>(parts(s.hold));
     s.part_cols = s.hold * kDistillPartThreads * vector;
-    s.rows_loss = s.splits == 1 || (rows >= kDistillRows && vocab / vector <= 16 * 256);
-    s.rows_loss_grad = s.splits == 1 || rows >= kDistillRows;
+    s.rows_loss_grad = rows >= kDistillRows || vocab / vector <= kDistillShort;
+    s.rows_loss = s.rows_loss_grad && vocab / vector <= 16 * 256;
     return s;
 }
 struct DistillSpace {

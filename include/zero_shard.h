@@ -437,7 +437,7 @@ typedef struct zs_targets {
 
 /* Bytes of device workspace distill_loss and distill_loss_grad need: a flag
  * per row, 16 bytes for each part a row may be cut into (2048 to 16384
- * logits), and below 512 rows 4 (k + 1) bytes a row.  0 for a NULL or invalid
+ * logits), and below 128 rows 4 (k + 1) bytes a row.  0 for a NULL or invalid
  * d.  Host only. */
 size_t zs_distill_workspace_bytes(const zs_distill* d);
 
@@ -476,7 +476,7 @@ int distill_grad(const zs_distill* d, const void* logits, const zs_targets* t,
                  const float* lse_in, const float* row_grad, void* grad_out, void* stream);
 
 /* Both in one call: the loss is usually the last operator of the forward
- * pass, so its gradient can be taken there.  From 512 rows on the logits are
+ * pass, so its gradient can be taken there.  From 128 rows on the logits are
  * read once (of a row, the first 131072 in bf16, 65536 in fp32).  Arguments
  * and errors as above; lse_out may be NULL.  The loss may differ from
  * distill_loss's in its last bits, the gradient from distill_grad's by what

@@ -105,7 +105,7 @@ class Problem:
         return o
 
 
-# rows 1..511 take the call that cuts rows into parts, 512 and more one block a row
+# long rows up to 127 of them are cut into parts, 128 and more (and short ones) take one block each
 SIZES = [(1, 1, 1), (1, 7, 3), (2, 8, 8), (3, 9, 1), (5, 1000, 16), (2, 50257, 64), (1, 131075, 130),
          (40, 12345, 33), (513, 61, 5), (515, 4097, 20)]
 
@@ -255,6 +255,30 @@ def test_long_rows_one_block_each(dtype, vocab, alpha, tau):
     p.check("pair", ref)
     b = p.run("step", in_place=True)
     assert torch.equal(a["grad"], b["grad"]) and torch.equal(a["loss"], b["loss"])
+
+
+@pytest.mark.parametrize("rows", [6, 127, 128])
+@pytest.mark.parametrize("dtype,vocab", [(BF16, 50003), (F32, 40005), (BF16, 8199), (F32, 4103)])
+@pytest.mark.parametrize("alpha,tau", [(1.0, 1.0), (0.5, 2.0), (0.5, 1.0)])
+def test_masked_places_in_parts(rows, dtype, vocab, alpha, tau):
+    """Whole parts masked by -Inf or the type's lowest value, masked rows, a
+    row without entries, at row counts around the two ways to cut the work."""
+    p = Problem(rows, vocab, 12, dtype, alpha=alpha, tau=tau, pad=1)
+    p.labels[:] = torch.arange(rows).cuda() * 13 % vocab
+    p.labels[0], p.s[0] = -100, math.nan
+    low = torch.finfo(dtype).min
+    for t, masked in ((1, -math.inf), (2, low)):
+        p.s[t, 40:vocab - 3] = masked                  # what is left is at both ends
+        p.ids[t] = torch.arange(12).cuda()
+        p.labels[t] = vocab - 1
+    p.ids[3] = -1
+    p.s[4, :-2] = -math.inf                            # the last part alone has any
+    p.ids[4] = vocab - 1
+    p.labels[4] = vocab - 2
+    ref = p.ref()
+    for calls in ("pair", "step"):
+        a, b = p.check(calls, ref), p.run(calls, in_place=True)
+        assert torch.equal(a["grad"], b["grad"]) and torch.equal(a["loss"], b["loss"])
 
 
 @pytest.mark.parametrize("rows", [3, 513])
