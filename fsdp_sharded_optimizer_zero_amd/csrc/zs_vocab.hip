@@ -326,6 +326,7 @@ __device__ __forceinline__ uint64_t same_row(bool in, int row, int bits)
 // CU).  Where a wave's list is too short for its tokens (one id in
 // most of them), all waves read the ids again and handle 64 whenever they
 // have them, once to count and once to place.
+template <typename ID>
 __global__ void __launch_bounds__(kSortThreads)
     k_embed_sort(EmbedArgs a, SortShape s, int32_t* order, int32_t* row_of, int32_t* starts)
 {
@@ -343,27 +344,30 @@ __global__ void __launch_bounds__(kSortThreads)
     const uint64_t lower = (uint64_t(1) << lane) - 1;
     const int room = sort_list(s.rows);
     int32_t* hist = sort_lds + wave * s.rows;
+    const ID* ids = static_cast<const ID*>(a.ids);
     // entries (token - t0) << kSortRowBits | row in the bucket: 20 + 9 bits
     uint32_t* list =
         reinterpret_cast<uint32_t*>(sort_lds) + kSortWaves * s.rows + wave * room;
     for (int r = lane; r < s.rows; r += kWave) hist[r] = 0;
 
-    // found(token, row, in): 64 tokens, `in` those of the bucket
+    // found(token, row, its bucket): 64 tokens; those without a row here are
+    // of no bucket (UINT32_MAX)
     const auto read_ids = [&](auto found) {
         for (int base = t0; base < t1; base += kSpan) {
-            uint32_t row[kSortLoads];
+            // all loads first, without a branch between them
+            ID id[kSortLoads];
 #pragma unroll
             for (int u = 0; u < kSortLoads; ++u) {
                 const int t = base + u * kWave + lane;
-                uint64_t r = UINT64_MAX;
-                if (t < t1) r = row_of_id(read_id(a.ids, a.id64, t), a.first_row);
-                row[u] = r < static_cast<uint64_t>(a.rows) ? static_cast<uint32_t>(r) : UINT32_MAX;
+                id[u] = ids[t < t1 ? t : t1 - 1];
             }
 #pragma unroll
             for (int u = 0; u < kSortLoads; ++u) {
-                const bool here = row[u] != UINT32_MAX;
-                found(base + u * kWave + lane, row[u], here,
-                      here && (row[u] & low) == bucket);
+                const int t = base + u * kWave + lane;
+                const uint64_t r = row_of_id(id[u], a.first_row);
+                const bool here = r < static_cast<uint64_t>(a.rows) && t < t1;
+                const uint32_t row = static_cast<uint32_t>(r);
+                found(t, row, here ? row & low : UINT32_MAX);
             }
         }
     };
@@ -401,7 +405,8 @@ __global__ void __launch_bounds__(kSortThreads)
     };
     const auto from_ids = [&](auto handle) {
         int queued = 0;
-        read_ids([&](int t, uint32_t row, bool, bool in) {
+        read_ids([&](int t, uint32_t row, uint32_t of) {
+            const bool in = of == bucket;
             const uint64_t mask = __ballot(in);
             if (mask == 0) return;
             if (in) list[queued + __popcll(mask & lower)] = entry(t, row);
@@ -419,8 +424,9 @@ __global__ void __launch_bounds__(kSortThreads)
     };
 
     int below = 0, n = 0;
-    read_ids([&](int t, uint32_t row, bool here, bool in) {
-        below += here && (row & low) < bucket;
+    read_ids([&](int t, uint32_t row, uint32_t of) {
+        const bool in = of == bucket;
+        below += of < bucket;
         const uint64_t mask = __ballot(in);
         if (mask == 0) return;
         const int at = n + __popcll(mask & lower);
@@ -1774,8 +1780,9 @@ int enqueue_embed_grad(const EmbedArgs& a, bool accumulate, void* workspace, voi
         int32_t* starts = reinterpret_cast<int32_t*>(base + w.starts);
         const SortShape s = sort_shape(a.rows);
         const int64_t buckets = int64_t(1) << s.bucket_bits;
-        hipLaunchKernelGGL(k_embed_sort, dim3(static_cast<uint32_t>(buckets)), dim3(kSortThreads),
-                           kSortLds, st, a, s, order, row_of, starts);
+        hipLaunchKernelGGL(a.id64 ? k_embed_sort<int64_t> : k_embed_sort<int32_t>,
+                           dim3(static_cast<uint32_t>(buckets)), dim3(kSortThreads), kSortLds, st,
+                           a, s, order, row_of, starts);
         const int rc = launched();
         if (rc != ZS_OK) return rc;
         p.order = order;
