@@ -210,7 +210,7 @@ __device__ __forceinline__ uint64_t uniform(uint64_t x)
 // Where the vector of N columns that would begin at c lies: the last one ends
 // with the row and repeats columns of the one before it, where a vector's worth
 // of the row's end element by element is a wave's slowest lane (16384 tokens of
-// 771 bf16: lookup 18 us, gradient 60 us).
+// 771 bf16: the gradient 44 us, 60 with elements; 32768: the lookup 15, 18).
 template <int N>
 __device__ __forceinline__ int64_t in_row(int64_t c, int64_t dim)
 {
@@ -322,8 +322,8 @@ __device__ __forceinline__ uint64_t same_row(bool in, int row, int bits)
 // tokens and lists those of the bucket, few of each 64, which are then
 // handled 64 at a time.  A token's place is: its row's start, the tokens of
 // that row in earlier waves, those handled earlier by its wave, and those in
-// lower lanes (4096 tokens 8 us, 65536 40 us: the ids' way from L2 to every
-// CU).  Where a wave's list is too short for its tokens (one id in
+// lower lanes (4096 tokens 7 us, 65536 23 us, 40 with a wait behind each
+// load: every CU looks at every id, some 20 instructions for 64).  Where a wave's list is too short for its tokens (one id in
 // most of them), all waves read the ids again and handle 64 whenever they
 // have them, once to count and once to place.
 template <typename ID>
@@ -767,7 +767,8 @@ __global__ void __launch_bounds__(kEmbedThreads)
 // vocabulary plus K entries to look at.  The logits are what costs: HBM moves
 // them, and each takes about six vector instructions and an exponential (four
 // issue slots) in each of the two passes, together half the time the bytes
-// take (8192 x 128256 bf16: without the exponentials 709 us, with them 740):
+// take (8192 x 128256 bf16, at the time: without the exponentials 709 us, with them
+// 740):
 //  - exponentials are the hardware's base-2 one (1 ulp), their arguments one
 //    fma each (see kFmaLimit), exact where the value is large;
 //  - logits and gradients pass the caches (nt: the loss of 2048 x 50257 fp32
@@ -951,7 +952,7 @@ __device__ __forceinline__ bool held_stats(typename Raw<T>::V (&raw)[HOLD], Own 
 
 // Elements of a row before its first 16-byte boundary, where its vectors
 // begin: a bf16 row of odd length read from its start would take every vector
-// across a boundary (5341 x 50257: 248 us).
+// across a boundary (5341 x 50257: 217 us, 248 from the start).
 template <typename T>
 __device__ __forceinline__ int row_head(const T* row, int64_t vocab)
 {
@@ -1364,7 +1365,7 @@ __device__ __forceinline__ void put_zeros(T* out, int64_t c0, int64_t c1)
 // bf16 (65536 fp32) logits; what a longer row has beyond that is read again.
 constexpr int kHold = 16;
 // One block per row: the loss, and with GRAD the gradient, the row read once
-// (8192 x 128256 bf16, an eighth of the rows masked: 3.94 GB in 740 us, 5.3
+// (8192 x 128256 bf16, an eighth of the rows masked: 3.94 GB in 726 us, 5.4
 // TB/s; copying the rows in this pattern without arithmetic takes 660).
 // Measured and not taken: two blocks of 512 threads on a CU, each holding half
 // its row (865 us); loading the next row as this one's registers become free
