@@ -195,6 +195,20 @@ def test_grad_long_runs_and_many_rows(tokens, rows, dim):
     run_grad(make_ids("zipf", tokens, rows, 13), tokens, rows, dim, BF16, F32, False)
 
 
+WIDTHS = [*range(1, 18), 255, 257, 263, 511, 513, 519, 1025, 1031, 2047, 2049, 2055, 4097]
+
+
+@pytest.mark.parametrize("act_dtype", [BF16, F32])
+@pytest.mark.parametrize("table_dtype", [BF16, F32])
+def test_every_end_of_a_row(act_dtype, table_dtype):
+    """Rows that end at any place of a vector, at any alignment."""
+    for dim in WIDTHS:
+        test_lookup(table_dtype, act_dtype, 66, 40, dim, 1)
+        for accumulate in (False, True):
+            run_grad(make_ids("zipf", 200, 40, 14), 200, 30, dim, act_dtype, table_dtype,
+                     accumulate, first=2, scale=-0.5, pad=1)
+
+
 @pytest.mark.parametrize("kind,tokens,rows", [("one", 40000, 130000), ("two", 40000, 500),
                                               ("runs", 70000, 131072)])
 def test_grad_sort_lists_overflow(kind, tokens, rows):
