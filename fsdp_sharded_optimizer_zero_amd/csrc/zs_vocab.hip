@@ -1412,7 +1412,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_distill_row(DistillArgs a, int64
     const bool sums = held_stats<T, TM>(raw, [&](int j) { return vector(j) < nv; }, c, st);
     st = scan<T, TM, THREADS, 4>(st, s, head, sums ? behind : head, a.vocab, c);
     st = block_join<TM, THREADS>(st, c, red);
-    if (threadIdx.x / kWave == 1) put_loss(a, e, row, st, e.s);
+    if (threadIdx.x / kWave == (THREADS > kWave ? 1 : 0)) put_loss(a, e, row, st, e.s);
     if constexpr (GRAD) {
         if (e.mass[1] == 0.0f) {
             put_zeros<T, THREADS>(out, 0, a.vocab);
@@ -1693,6 +1693,8 @@ int distill_rows(const DistillArgs& a, hipStream_t st)
 {
     const size_t lds = entry_bytes(a.k);
     const int64_t vectors = a.vocab / Raw<T>::N;
+    if (vectors <= 4 * 64)
+        return launch(k_distill_row<T, TM, GRAD, 64, 4, true>, a.rows, 64, lds, st, a);
     if (vectors <= 4 * 256)
         return launch(k_distill_row<T, TM, GRAD, 256, 4, true>, a.rows, 256, lds, st, a);
     if (vectors <= kHold * 256)
