@@ -236,7 +236,7 @@ constexpr int kDistillHold = 8;
 constexpr int kDistillFewHold = 2;
 constexpr int64_t kDistillBlocks = 2048;    // 8 blocks of 4 waves on each of 256 CUs
 constexpr int64_t kDistillRows = 128;
-constexpr int64_t kDistillShort = 1024;     // 4 vectors for each of 256 threads
+constexpr int64_t kDistillShort = 1024;     // 8 vectors for each of 128 threads
 struct DistillShape {
     int32_t splits;         // parts of a row
     int32_t hold;

@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(kEmbedThreads)
 // vocabulary plus K entries to look at.  The logits are what costs: HBM moves
 // them, and each takes about six vector instructions and an exponential (four
 // issue slots) in each of the two passes, together half the time the bytes
-// take (8192 x 128256 bf16, at the time: without the exponentials 709 us, with them
+// take (8192 x 128256 bf16: without the exponentials 709 us, with them 726 to
 // 740):
 //  - exponentials are the hardware's base-2 one (1 ulp), their arguments one
 //    fma each (see kFmaLimit), exact where the value is large;
@@ -1687,7 +1687,9 @@ int embed_sums(const EmbedArgs& a, const SumPlan& p, bool add, hipStream_t st)
 }
 
 // The smallest block that holds the row, so that 16 waves are on a CU at any
-// length; short rows hold less.
+// length.  Short rows hold less and take one wave or two, so that more of them
+// are under way (8192 rows of bf16, kernel: of 1000 logits 25 us and 44 with a
+// block of 256 threads, of 4000 38 and 50, of 8000 53 and 58).
 template <typename T, Terms TM, bool GRAD>
 int distill_rows(const DistillArgs& a, hipStream_t st)
 {
@@ -1695,8 +1697,10 @@ int distill_rows(const DistillArgs& a, hipStream_t st)
     const int64_t vectors = a.vocab / Raw<T>::N;
     if (vectors <= 4 * 64)
         return launch(k_distill_row<T, TM, GRAD, 64, 4, true>, a.rows, 64, lds, st, a);
-    if (vectors <= 4 * 256)
-        return launch(k_distill_row<T, TM, GRAD, 256, 4, true>, a.rows, 256, lds, st, a);
+    if (vectors <= 8 * 64)
+        return launch(k_distill_row<T, TM, GRAD, 64, 8, false>, a.rows, 64, lds, st, a);
+    if (vectors <= 8 * 128)
+        return launch(k_distill_row<T, TM, GRAD, 128, 8, false>, a.rows, 128, lds, st, a);
     if (vectors <= kHold * 256)
         return launch(k_distill_row<T, TM, GRAD, 256, kHold, false>, a.rows, 256, lds, st, a);
     if (vectors <= kHold * 512)
