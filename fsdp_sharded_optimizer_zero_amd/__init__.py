@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes as C
+import math
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -427,16 +428,41 @@ _IDS = {ZS_ID_I32: ("int32",), ZS_ID_I64: ("int64",)}
 _ELEM = {ZS_BF16: _B16, ZS_F32: _F32}
 
 
+def _rows_fit(shape, rows: int, width: int, pitch: int) -> bool:
+    """Whether the sizes of a contiguous tensor agree with `rows` rows of
+    `width` elements, `pitch` apart.  Rows are one dimension or the last few
+    ([T, heads, head_dim]); one dimension, sizes of 1 aside, is a flat buffer;
+    several rows may lie in one dimension if the rows fill the tensor."""
+    sizes = [n for n in shape if n != 1]
+    if len(sizes) < 2 or rows < 1:
+        return True
+    total = math.prod(sizes)
+    n = 1
+    for size in reversed(sizes):
+        n *= size
+        if n == pitch or (n % pitch == 0 and n < total == rows * pitch):
+            return True
+        if rows == 1 and (n == width or width < n < total):
+            return True
+    return False
+
+
 def _rows_ptr(t, what: str, dtypes, rows: int, width: int, pitch: int):
     """As _ptr for `rows` rows of `width` elements, `pitch` apart: either a
-    contiguous tensor that holds them, or a 2-D view with that row stride."""
-    if hasattr(t, "is_contiguous") and not t.is_contiguous() and t.dim() == 2:
-        if t.shape[0] < rows or t.shape[1] < width or (width > 1 and t.stride(1) != 1) \
-                or (rows > 1 and t.stride(0) != pitch):
-            raise ValueError(f"{what}: shape {tuple(t.shape)} with strides {t.stride()}, the call "
-                             f"needs {rows} rows of {width} elements, {pitch} apart")
-        # the checks of _ptr on its first row; the rows' extent is checked above
-        return _ptr(t[0, :width], what, dtypes)
+    contiguous tensor that holds them, or a 2-D view with that row stride.
+    A tensor whose own rows are of another pitch is refused."""
+    if hasattr(t, "is_contiguous"):
+        if not t.is_contiguous() and t.dim() == 2:
+            if t.shape[0] < rows or t.shape[1] < width or (width > 1 and t.stride(1) != 1) \
+                    or (rows > 1 and t.stride(0) != pitch):
+                raise ValueError(f"{what}: shape {tuple(t.shape)} with strides {t.stride()}, the "
+                                 f"call needs {rows} rows of {width} elements, {pitch} apart")
+            # the checks of _ptr on its first row; the rows' extent is checked above
+            return _ptr(t[0, :width], what, dtypes)
+        if pitch > 0 and t.dim() > 1 and t.shape[-1] != pitch \
+                and not _rows_fit(t.shape, rows, width, pitch):
+            raise ValueError(f"{what}: shape {tuple(t.shape)}, the call needs {rows} rows of "
+                             f"{width} elements, {pitch} apart")
     return _ptr(t, what, dtypes, (rows - 1) * pitch + width if rows > 0 else 0)
 
 

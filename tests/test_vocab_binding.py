@@ -1,0 +1,77 @@
+"""The binding's own checks of the vocabulary-table calls, on the CPU: what a
+tensor's shape says about its rows is held against the call's row widths and
+pitches.  A CPU tensor whose shape is accepted is refused last, for not being
+on the GPU, so every case ends before the C ABI."""
+import pytest
+import torch
+
+import fsdp_sharded_optimizer_zero_amd as Z
+
+BF16 = torch.bfloat16
+ACCEPTED = "GPU tensor is required"
+REFUSED = "apart"
+
+
+def rows_ptr(shape, rows, width, pitch, dtype=BF16):
+    return Z._rows_ptr(torch.zeros(shape, dtype=dtype), "rows", None, rows, width, pitch)
+
+
+# shape of a contiguous tensor, rows, width, pitch
+HOLDS = [((6, 50), 6, 50, 50), ((6, 56), 6, 50, 56),
+         ((8, 50), 6, 50, 50),                              # more rows than asked
+         ((300,), 6, 50, 50), ((5 * 56 + 50,), 6, 50, 56),  # a flat buffer
+         ((1, 300), 6, 50, 50), ((300, 1), 6, 50, 50),      # the same, by its sizes
+         ((2, 3, 50), 6, 50, 50), ((6, 5, 10), 6, 50, 50), ((2, 3, 5, 10), 6, 50, 50),
+         ((1, 6, 56), 6, 50, 56), ((1, 56), 1, 50, 50), ((4, 56), 1, 50, 50),
+         ((5, 10), 1, 50, 50),
+         ((3, 100), 6, 50, 50), ((2, 150), 6, 50, 50),      # [batch, length x 50]
+         ((6, 1), 6, 1, 1), ((0, 50), 0, 50, 50), ((4, 56), 0, 50, 50)]
+# the padded rows of a contiguous tensor at the pitch of narrower ones, and others
+WRONG = [((6, 56), 6, 50, 50), ((50, 6), 6, 50, 50), ((2, 3, 56), 6, 50, 50),
+         ((6, 100), 6, 50, 50), ((12, 25), 6, 50, 56), ((2, 300), 6, 50, 50), ((5, 8), 1, 20, 20)]
+
+
+@pytest.mark.parametrize("shape,rows,width,pitch", HOLDS)
+def test_rows_of_the_calls_pitch_are_accepted(shape, rows, width, pitch):
+    with pytest.raises(ValueError, match=ACCEPTED):
+        rows_ptr(shape, rows, width, pitch)
+
+
+@pytest.mark.parametrize("shape,rows,width,pitch", WRONG)
+def test_rows_of_another_pitch_are_refused(shape, rows, width, pitch):
+    with pytest.raises(ValueError, match=REFUSED):
+        rows_ptr(shape, rows, width, pitch)
+
+
+def test_padded_tables_and_logits_need_their_pitch():
+    """Each tensor of rows of each call: 8 columns wider than the default
+    pitch is refused, with the pitch named it is accepted."""
+    T, R, D, K = 5, 30, 16, 2
+    table = torch.zeros((R, D + 8), dtype=BF16)
+    act, ok = torch.zeros((T, D + 8), dtype=BF16), torch.zeros((T, D), dtype=BF16)
+
+    def calls(**pitch):
+        e = Z.make_embed(T, R, D, **{k: v for k, v in pitch.items() if k[0] in "ta"})
+        d = Z.make_distill(T, R, K, **{k: v for k, v in pitch.items() if k[0] in "lg"})
+        w = dict(table=(e.rows, e.dim, e.table_pitch), act=(e.tokens, e.dim, e.act_pitch),
+                 logits=(d.rows, d.vocab, d.logits_pitch), grad=(d.rows, d.vocab, d.grad_pitch))
+        return lambda name, t: Z._rows_ptr(t, name, None, *w[name])
+
+    plain, padded = calls(), calls(table_pitch=D + 8, act_pitch=D + 8, logits_pitch=R + 8,
+                                   grad_pitch=R + 8)
+    wide = torch.zeros((T, R + 8), dtype=BF16)
+    for name, t in (("table", table), ("act", act), ("logits", wide), ("grad", wide)):
+        with pytest.raises(ValueError, match=REFUSED):
+            plain(name, t)
+        with pytest.raises(ValueError, match=ACCEPTED):
+            padded(name, t)
+    # as the entry points are called: the first tensor of rows is what is wrong
+    e, d = Z.make_embed(T, R, D), Z.make_distill(T, R, K)
+    at = 4096           # an address, not looked at
+    for call in (lambda: Z.embed_lookup(e, at, table, ok),
+                 lambda: Z.embed_grad(e, at, act, table, 0),
+                 lambda: Z.distill_loss(d, wide, at, at, 0, 0, workspace=0),
+                 lambda: Z.distill_grad(d, wide, at, at, 0, wide),
+                 lambda: Z.distill_loss_grad(d, wide, at, at, 0, wide, workspace=0)):
+        with pytest.raises(ValueError, match=REFUSED):
+            call()
