@@ -537,9 +537,13 @@ def zs_distill_workspace_bytes(d: zs_distill) -> int:
 def _targets(d: zs_distill, teacher_ids, teacher_logits, teacher_lse, labels) -> zs_targets:
     ids = _IDS.get(d.id_dtype)
     return zs_targets(
-        _ptr(teacher_ids, "teacher_ids", ids, d.rows * d.k),
-        _ptr(teacher_logits, "teacher_logits", _ELEM.get(d.teacher_dtype), d.rows * d.k),
+        _rows_ptr(teacher_ids, "teacher_ids", ids, d.rows, d.k, d.k),
+        _rows_ptr(teacher_logits, "teacher_logits", _ELEM.get(d.teacher_dtype), d.rows, d.k, d.k),
         _ptr(teacher_lse, "teacher_lse", _F32, d.rows), _ptr(labels, "labels", ids, d.rows))
+
+
+def _lse_ptr(d: zs_distill, t):
+    return _rows_ptr(t, "lse", _F32, d.rows, 2, 2)
 
 
 def _logits_ptr(d: zs_distill, t, what: str, pitch: int):
@@ -555,7 +559,7 @@ def distill_loss(d: zs_distill, logits, teacher_ids, teacher_logits, loss, lse, 
     ws, nbytes = _sized(workspace, workspace_bytes, zs_distill_workspace_bytes(d))
     _check(lib().distill_loss(
         C.byref(d), _logits_ptr(d, logits, "logits", d.logits_pitch), C.byref(t),
-        _ptr(loss, "loss", _F32, d.rows), _ptr(lse, "lse", _F32, 2 * d.rows),
+        _ptr(loss, "loss", _F32, d.rows), _lse_ptr(d, lse),
         _ptr(loss_sum, "loss_sum", _F32, 1), _ptr(counted, "counted", _I64, 1),
         1 if accumulate else 0, ws, nbytes,
         _stream_on(stream, logits, teacher_ids, teacher_logits, teacher_lse, labels, loss, lse,
@@ -568,7 +572,7 @@ def distill_grad(d: zs_distill, logits, teacher_ids, teacher_logits, lse, grad, 
     t = _targets(d, teacher_ids, teacher_logits, teacher_lse, labels)
     _check(lib().distill_grad(
         C.byref(d), _logits_ptr(d, logits, "logits", d.logits_pitch), C.byref(t),
-        _ptr(lse, "lse", _F32, 2 * d.rows), _ptr(row_grad, "row_grad", _F32, d.rows),
+        _lse_ptr(d, lse), _ptr(row_grad, "row_grad", _F32, d.rows),
         _logits_ptr(d, grad, "grad", d.grad_pitch),
         _stream_on(stream, logits, teacher_ids, teacher_logits, teacher_lse, labels, lse, row_grad,
                    grad)), "distill_grad")
@@ -583,7 +587,7 @@ def distill_loss_grad(d: zs_distill, logits, teacher_ids, teacher_logits, loss, 
     ws, nbytes = _sized(workspace, workspace_bytes, zs_distill_workspace_bytes(d))
     _check(lib().distill_loss_grad(
         C.byref(d), _logits_ptr(d, logits, "logits", d.logits_pitch), C.byref(t),
-        _ptr(loss, "loss", _F32, d.rows), _ptr(lse, "lse", _F32, 2 * d.rows),
+        _ptr(loss, "loss", _F32, d.rows), _lse_ptr(d, lse),
         _ptr(row_grad, "row_grad", _F32, d.rows),
         _logits_ptr(d, grad, "grad", d.grad_pitch), _ptr(loss_sum, "loss_sum", _F32, 1),
         _ptr(counted, "counted", _I64, 1), 1 if accumulate else 0, ws, nbytes,

@@ -75,3 +75,85 @@ def test_padded_tables_and_logits_need_their_pitch():
                  lambda: Z.distill_loss_grad(d, wide, at, at, 0, wide, workspace=0)):
         with pytest.raises(ValueError, match=REFUSED):
             call()
+
+
+class OnGpu:
+    """A CPU tensor that says it is on a GPU, for checks that stop before the
+    library is called."""
+
+    def __init__(self, t, device=0):
+        self._t, self._device = t, device
+
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return self._device
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+
+def stopped(monkeypatch):
+    """The library's calls raise: all checks of the binding were passed."""
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                raise ArithmeticError("called")
+            return call
+
+    sizes = {n: getattr(Z, n) for n in ("zs_embed_workspace_bytes", "zs_distill_workspace_bytes")}
+    real = Z.lib()
+    monkeypatch.setattr(Z, "lib", lambda: Library())
+    for name in sizes:
+        monkeypatch.setattr(Z, name, lambda s, f=getattr(real, name): f(Z.C.byref(s)))
+
+
+def distill_tensors(T=6, V=40, K=4):
+    f = torch.float32
+    return Z.make_distill(T, V, K), dict(
+        logits=torch.zeros((T, V), dtype=BF16), teacher_ids=torch.zeros((T, K), dtype=torch.int64),
+        teacher_logits=torch.zeros((T, K), dtype=f), teacher_lse=torch.zeros(T, dtype=f),
+        labels=torch.zeros(T, dtype=torch.int64), loss=torch.zeros(T, dtype=f),
+        lse=torch.zeros((T, 2), dtype=f), grad=torch.zeros((T, V), dtype=BF16),
+        loss_sum=torch.zeros(1, dtype=f), counted=torch.zeros(1, dtype=torch.int64),
+        workspace=torch.zeros(1 << 16, dtype=torch.uint8))
+
+
+def distill_calls(d, x):
+    """The three calls on the same tensors."""
+    t = dict(teacher_lse=x["teacher_lse"], labels=x["labels"])
+    sums = dict(loss_sum=x["loss_sum"], counted=x["counted"], workspace=x["workspace"])
+    who = (x["logits"], x["teacher_ids"], x["teacher_logits"])
+    return {"loss": lambda: Z.distill_loss(d, *who, x["loss"], x["lse"], **t, **sums, stream=0),
+            "grad": lambda: Z.distill_grad(d, *who, x["lse"], x["grad"], **t, stream=0),
+            "both": lambda: Z.distill_loss_grad(d, *who, x["loss"], x["grad"], lse=x["lse"], **t,
+                                                **sums, stream=0)}
+
+
+def on_gpu(x, **device):
+    return {k: OnGpu(t, device.get(k, 0)) for k, t in x.items()}
+
+
+@pytest.mark.parametrize("name,shape", [
+    ("teacher_ids", (6, 5)), ("teacher_logits", (6, 5)), ("teacher_ids", (3, 2, 8)),
+    ("teacher_logits", (6, 8)), ("teacher_ids", (4, 7)), ("lse", (6, 3)), ("lse", (3, 5))])
+def test_teacher_entries_of_another_count_are_refused(monkeypatch, name, shape):
+    """[T, k'] tensors at k entries a row, and an lse that is not [T, 2]."""
+    stopped(monkeypatch)
+    d, x = distill_tensors()
+    x[name] = torch.zeros(shape, dtype=x[name].dtype)
+    for call in distill_calls(d, on_gpu(x)).values():
+        with pytest.raises(ValueError, match=REFUSED):
+            call()
+
+
+@pytest.mark.parametrize("shape", [(6, 4), (2, 3, 4), (24,), (8, 4), (1, 24), (2, 12)])
+def test_teacher_entries_of_the_calls_count_are_accepted(monkeypatch, shape):
+    stopped(monkeypatch)
+    d, x = distill_tensors()
+    for name in ("teacher_ids", "teacher_logits"):
+        x[name] = torch.zeros(shape, dtype=x[name].dtype)
+    x["lse"] = torch.zeros((12,))
+    for call in distill_calls(d, on_gpu(x)).values():
+        with pytest.raises(ArithmeticError):
+            call()
