@@ -563,7 +563,7 @@ def distill_loss(d: zs_distill, logits, teacher_ids, teacher_logits, loss, lse, 
         _ptr(loss_sum, "loss_sum", _F32, 1), _ptr(counted, "counted", _I64, 1),
         1 if accumulate else 0, ws, nbytes,
         _stream_on(stream, logits, teacher_ids, teacher_logits, teacher_lse, labels, loss, lse,
-                   workspace)), "distill_loss")
+                   loss_sum, counted, workspace)), "distill_loss")
 
 
 def distill_grad(d: zs_distill, logits, teacher_ids, teacher_logits, lse, grad, teacher_lse=None,
@@ -592,7 +592,7 @@ def distill_loss_grad(d: zs_distill, logits, teacher_ids, teacher_logits, loss, 
         _logits_ptr(d, grad, "grad", d.grad_pitch), _ptr(loss_sum, "loss_sum", _F32, 1),
         _ptr(counted, "counted", _I64, 1), 1 if accumulate else 0, ws, nbytes,
         _stream_on(stream, logits, teacher_ids, teacher_logits, teacher_lse, labels, loss, lse,
-                   row_grad, grad, workspace)), "distill_loss_grad")
+                   row_grad, grad, loss_sum, counted, workspace)), "distill_loss_grad")
 
 
 def build(verbose: bool = False) -> str:

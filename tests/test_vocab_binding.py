@@ -157,3 +157,25 @@ def test_teacher_entries_of_the_calls_count_are_accepted(monkeypatch, shape):
     for call in distill_calls(d, on_gpu(x)).values():
         with pytest.raises(ArithmeticError):
             call()
+
+
+def current(monkeypatch, device):
+    class Cuda:
+        is_initialized = staticmethod(lambda: True)
+        current_device = staticmethod(lambda: device)
+
+    monkeypatch.setattr(Z, "_cuda", lambda: Cuda)
+
+
+@pytest.mark.parametrize("call", ["loss", "grad", "both"])
+def test_every_tensor_of_another_device_is_refused(monkeypatch, call):
+    """One tensor after the other on GPU 1 while GPU 0 is current."""
+    stopped(monkeypatch)
+    current(monkeypatch, 0)
+    d, x = distill_tensors()
+    with pytest.raises(ArithmeticError):
+        distill_calls(d, on_gpu(x))[call]()
+    unused = {"loss": {"grad"}, "grad": {"loss", "loss_sum", "counted", "workspace"}, "both": set()}
+    for name in set(x) - unused[call]:
+        with pytest.raises(ValueError, match="current device"):
+            distill_calls(d, on_gpu(x, **{name: 1}))[call]()
