@@ -468,7 +468,8 @@ def _rows_ptr(t, what: str, dtypes, rows: int, width: int, pitch: int):
 
 def _stream_on(stream, *tensors):
     """The stream's handle.  The library works on the current device: tensors
-    of another one are refused (raw addresses are not looked at)."""
+    and streams of another one are refused (raw addresses and handles are not
+    looked at)."""
     cuda = _cuda()
     if not cuda.is_initialized():
         return _stream(stream)          # no GPU tensor yet: _ptr refuses the others
@@ -476,7 +477,11 @@ def _stream_on(stream, *tensors):
     for t in tensors:
         if t is not None and not isinstance(t, int) and t.get_device() != device:
             raise ValueError(f"a tensor on GPU {t.get_device()}: the current device is {device}")
-    return _current_stream(device) if stream is None else _stream(stream)
+    if stream is None:
+        return _current_stream(device)
+    if getattr(stream, "device_index", device) != device:
+        raise ValueError(f"a stream of GPU {stream.device_index}: the current device is {device}")
+    return _stream(stream)
 
 
 def _sized(workspace, workspace_bytes, need: int):

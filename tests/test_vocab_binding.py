@@ -179,3 +179,17 @@ def test_every_tensor_of_another_device_is_refused(monkeypatch, call):
     for name in set(x) - unused[call]:
         with pytest.raises(ValueError, match="current device"):
             distill_calls(d, on_gpu(x, **{name: 1}))[call]()
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """The kernels of a call are those of the current device."""
+    class Stream:
+        cuda_stream = 77
+
+        def __init__(self, device):
+            self.device_index = device
+
+    current(monkeypatch, 0)
+    assert Z._stream_on(Stream(0)) == 77 and Z._stream_on(5) == 5
+    with pytest.raises(ValueError, match="current device"):
+        Z._stream_on(Stream(1))
