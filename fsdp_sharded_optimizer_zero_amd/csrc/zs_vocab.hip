@@ -1208,15 +1208,16 @@ __device__ __forceinline__ void put_no_loss(const DistillArgs& a, int64_t row)
     if (a.lse_out) a.lse_out[2 * row] = a.lse_out[2 * row + 1] = 0.0f;
 }
 
-// A softmax's share of the gradient: g * exp2((s - m) * c), for both.
+// A softmax's share of the gradient: g * exp2((s - m) * c), for both, the
+// teacher's with an exponent e on top.
 struct Slope {
-    float m_kd, g_kd, m_ce, g_ce;
+    float m_kd, g_kd, m_ce, g_ce, e_kd;
 };
 
 template <Terms TM>
 __device__ __forceinline__ float slope_at(const Slope& g, float x, float c)
 {
-    float v = g.g_kd * exp2_hw((x - g.m_kd) * c);
+    float v = g.g_kd * exp2_hw(__builtin_fmaf(x - g.m_kd, c, g.e_kd));
     if constexpr (TM == kKdCe) v += g.g_ce * exp2_hw((x - g.m_ce) * kLog2e);
     return v;
 }
@@ -1225,7 +1226,7 @@ __device__ __forceinline__ Slope slope_of(const DistillArgs& a, float mass, cons
                                           float row_grad, bool same)
 {
     Slope g = {st.m, row_grad * a.grad_kd * mass / st.a, st.m,
-               a.ce ? row_grad * a.grad_ce / st.b : 0.0f};
+               a.ce ? row_grad * a.grad_ce / st.b : 0.0f, 0.0f};
     if (same) g.g_kd += g.g_ce;
     return g;
 }
@@ -1236,7 +1237,7 @@ struct FmaSlope {
 };
 __device__ __forceinline__ FmaSlope fma_slope(const Slope& g, float c)
 {
-    return FmaSlope{g.m_kd * c, g.g_kd * rounded_by(g.m_kd, c), g.m_ce * kLog2e,
+    return FmaSlope{g.m_kd * c, g.g_kd * (rounded_by(g.m_kd, c) * exp2_hw(g.e_kd)), g.m_ce * kLog2e,
                     g.g_ce * rounded_by(g.m_ce, kLog2e)};
 }
 
@@ -1570,13 +1571,14 @@ __global__ void __launch_bounds__(kPartThreads) k_distill_grad(DistillArgs a, in
     }
     Slope g;
     if constexpr (FROM_LSE) {
-        // exp(s/tau - lse) = exp((s - m)/tau) * exp(m/tau - lse) with
-        // m = tau * lse rounded: the second factor, near 1, takes up the
-        // rounding
+        // exp(s/tau - lse) = exp((s - m)/tau + rest) with m = tau * lse
+        // rounded and rest = m/tau - lse what the rounding leaves: near 0 for
+        // an ordinary lse, above 1 past 2^24
         const float lse = a.lse_in[2 * row], m = lse / a.inv_tau;
         const double rest = static_cast<double>(m) * a.inv_tau - lse;
         g.m_kd = m;
-        g.g_kd = rg * a.grad_kd * *e.mass * (1.0f + static_cast<float>(rest));
+        g.g_kd = rg * a.grad_kd * *e.mass;
+        g.e_kd = static_cast<float>(rest) * kLog2e;
         g.m_ce = a.lse_in[2 * row + 1];
         g.g_ce = rg * a.grad_ce;
         if constexpr (TM == kSame) g.g_kd += g.g_ce;
