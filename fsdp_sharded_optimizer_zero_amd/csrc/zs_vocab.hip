@@ -1194,7 +1194,11 @@ __device__ __forceinline__ void put_loss(const DistillArgs& a, const Entries& e,
     a.loss[row] = counts ? loss : 0.0f;
     a.counts[row] = counts;
     if (a.lse_out) {
-        a.lse_out[2 * row] = counts ? st.m * a.inv_tau + log_a : 0.0f;
+        // the quotient may pass the largest number; a row of -Inf alone (or
+        // with NaN) keeps its -Inf (NaN)
+        float lse = st.m * a.inv_tau + log_a;
+        if (st.a > 0.0f) lse = fminf(fmaxf(lse, kLowest), -kLowest);
+        a.lse_out[2 * row] = counts ? lse : 0.0f;
         a.lse_out[2 * row + 1] = a.ce ? st.m + log_b : 0.0f;
     }
 }
@@ -1209,15 +1213,16 @@ __device__ __forceinline__ void put_no_loss(const DistillArgs& a, int64_t row)
 }
 
 // A softmax's share of the gradient: g * exp2((s - m) * c), for both, the
-// teacher's with an exponent e on top.
+// teacher's with an exponent e on top, and held to `top` at most.
 struct Slope {
-    float m_kd, g_kd, m_ce, g_ce, e_kd;
+    float m_kd, g_kd, m_ce, g_ce, e_kd, top_kd;
 };
 
 template <Terms TM>
 __device__ __forceinline__ float slope_at(const Slope& g, float x, float c)
 {
-    float v = g.g_kd * exp2_hw(__builtin_fmaf(x - g.m_kd, c, g.e_kd));
+    const float z = __builtin_fmaf(x - g.m_kd, c, g.e_kd);
+    float v = g.g_kd * exp2_hw(z > g.top_kd ? g.top_kd : z);    // NaN stays
     if constexpr (TM == kKdCe) v += g.g_ce * exp2_hw((x - g.m_ce) * kLog2e);
     return v;
 }
@@ -1226,10 +1231,15 @@ __device__ __forceinline__ Slope slope_of(const DistillArgs& a, float mass, cons
                                           float row_grad, bool same)
 {
     Slope g = {st.m, row_grad * a.grad_kd * mass / st.a, st.m,
-               a.ce ? row_grad * a.grad_ce / st.b : 0.0f, 0.0f};
+               a.ce ? row_grad * a.grad_ce / st.b : 0.0f, 0.0f, INFINITY};
     if (same) g.g_kd += g.g_ce;
     return g;
 }
+
+// From this |lse| on its neighbours in fp32 are 16 apart, and it says which
+// logits have a weight but not how much: their values are held to 1, where the
+// rounding alone would take them to any size (rows of the type's lowest value).
+constexpr float kVagueLse = 134217728.0f;
 
 // The fma form of a slope, for the vectors a block holds.
 struct FmaSlope {
@@ -1573,12 +1583,15 @@ __global__ void __launch_bounds__(kPartThreads) k_distill_grad(DistillArgs a, in
     if constexpr (FROM_LSE) {
         // exp(s/tau - lse) = exp((s - m)/tau + rest) with m = tau * lse
         // rounded and rest = m/tau - lse what the rounding leaves: near 0 for
-        // an ordinary lse, above 1 past 2^24
-        const float lse = a.lse_in[2 * row], m = lse / a.inv_tau;
+        // an ordinary lse, above 1 past 2^24.  (The quotient of a finite lse
+        // may pass the largest number by its rounding.)
+        const float lse = a.lse_in[2 * row];
+        const float m = fminf(fmaxf(lse / a.inv_tau, kLowest), -kLowest);
         const double rest = static_cast<double>(m) * a.inv_tau - lse;
         g.m_kd = m;
         g.g_kd = rg * a.grad_kd * *e.mass;
         g.e_kd = static_cast<float>(rest) * kLog2e;
+        g.top_kd = fabsf(lse) >= kVagueLse ? 0.0f : INFINITY;
         g.m_ce = a.lse_in[2 * row + 1];
         g.g_ce = rg * a.grad_ce;
         if constexpr (TM == kSame) g.g_kd += g.g_ce;

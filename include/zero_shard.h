@@ -454,6 +454,7 @@ size_t zs_distill_workspace_bytes(const zs_distill* d);
  *   loss_out   fp32[T].
  *   lse_out    fp32[T, 2] or NULL (required by distill_loss): lse_tau and
  *              lse_1 (0 if alpha == 1); both 0 for a row that does not count.
+ *              An lse_tau beyond fp32's range is its largest number.
  *   loss_sum   one fp32 or NULL: the sum of loss_out, taken in fp64 in a fixed
  *              order and rounded once.   counted  one int64 or NULL: how many
  *              rows count.  accumulate != 0 adds to what they hold.
@@ -467,7 +468,9 @@ int distill_loss(const zs_distill* d, const void* logits, const zs_targets* t, f
  *   grad_out[t, v] = scale * row_grad[t] * (alpha tau (M q_v - sum of p_k with id_k = v)
  *                    + (1 - alpha) (exp(s_v - lse_1) - [v = label])),  M = sum of p_k
  * (M is 1 without teacher_lse), rounded once to logits_dtype; +0 in rows that
- * do not count.
+ * do not count.  q_v = exp(s_v / tau - lse_tau) is as exact as lse_in: fp32
+ * holds it to |lse| 2^-24, and from |lse_tau| = 2^27 on q_v is held to 1 (a row
+ * of equal values so far from zero is uniform in distill_loss_grad alone).
  *   row_grad  fp32[T] or NULL (1): the gradient each row's loss receives.
  *   grad_out  T rows; may be the logits themselves (then of the same pitch).
  * Errors: ZS_ENULL, ZS_EINVAL_DISTILL (also: in place with another pitch),
