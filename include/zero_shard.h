@@ -437,8 +437,8 @@ typedef struct zs_targets {
 
 /* Bytes of device workspace distill_loss and distill_loss_grad need: a flag
  * per row, 16 bytes for each part a row may be cut into (2048 to 16384
- * logits), and below 128 rows 4 (k + 1) bytes a row.  0 for a NULL or invalid
- * d.  Host only. */
+ * logits), and for fewer than 128 rows of more than 1024 16-byte vectors of
+ * logits 4 (k + 1) bytes a row.  0 for a NULL or invalid d.  Host only. */
 size_t zs_distill_workspace_bytes(const zs_distill* d);
 
 /* Row losses.  With s a row's logits, K its teacher entries, in fp32:
@@ -479,11 +479,12 @@ int distill_grad(const zs_distill* d, const void* logits, const zs_targets* t,
                  const float* lse_in, const float* row_grad, void* grad_out, void* stream);
 
 /* Both in one call: the loss is usually the last operator of the forward
- * pass, so its gradient can be taken there.  From 128 rows on the logits are
- * read once (of a row, the first 131072 in bf16, 65536 in fp32).  Arguments
- * and errors as above; lse_out may be NULL.  The loss may differ from
- * distill_loss's in its last bits, the gradient from distill_grad's by what
- * rounding lse to fp32 takes. */
+ * pass, so its gradient can be taken there.  From 128 rows on, and for rows of
+ * at most 1024 16-byte vectors, the logits are read once (of a row, the first
+ * 131072 in bf16, 65536 in fp32; all of it twice where its largest logit times
+ * log2(e) / tau is beyond 65536).  Arguments and errors as above; lse_out may
+ * be NULL.  The loss may differ from distill_loss's in its last bits, the
+ * gradient from distill_grad's by what rounding lse to fp32 takes. */
 int distill_loss_grad(const zs_distill* d, const void* logits, const zs_targets* t,
                       float* loss_out, float* lse_out, const float* row_grad, void* grad_out,
                       float* loss_sum, int64_t* counted, int32_t accumulate, void* workspace,
