@@ -451,17 +451,17 @@ def _rows_ptr(t, what: str, dtypes, rows: int, width: int, pitch: int):
     """As _ptr for `rows` rows of `width` elements, `pitch` apart: either a
     contiguous tensor that holds them, or a 2-D view with that row stride.
     A tensor whose own rows are of another pitch is refused."""
-    if hasattr(t, "is_contiguous"):
-        if not t.is_contiguous() and t.dim() == 2:
-            if t.shape[0] < rows or t.shape[1] < width or (width > 1 and t.stride(1) != 1) \
+    shape = getattr(t, "shape", ())
+    if len(shape) > 1 and (shape[-1] != pitch or rows < 2):
+        if len(shape) == 2 and not t.is_contiguous():
+            if shape[0] < rows or shape[1] < width or (width > 1 and t.stride(1) != 1) \
                     or (rows > 1 and t.stride(0) != pitch):
-                raise ValueError(f"{what}: shape {tuple(t.shape)} with strides {t.stride()}, the "
+                raise ValueError(f"{what}: shape {tuple(shape)} with strides {t.stride()}, the "
                                  f"call needs {rows} rows of {width} elements, {pitch} apart")
             # the checks of _ptr on its first row; the rows' extent is checked above
             return _ptr(t[0, :width], what, dtypes)
-        if pitch > 0 and t.dim() > 1 and t.shape[-1] != pitch \
-                and not _rows_fit(t.shape, rows, width, pitch):
-            raise ValueError(f"{what}: shape {tuple(t.shape)}, the call needs {rows} rows of "
+        if pitch > 0 and shape[-1] != pitch and not _rows_fit(shape, rows, width, pitch):
+            raise ValueError(f"{what}: shape {tuple(shape)}, the call needs {rows} rows of "
                              f"{width} elements, {pitch} apart")
     return _ptr(t, what, dtypes, (rows - 1) * pitch + width if rows > 0 else 0)
 
@@ -484,11 +484,12 @@ def _stream_on(stream, *tensors):
     return _stream(stream)
 
 
-def _sized(workspace, workspace_bytes, need: int):
-    """(address, bytes) of a workspace argument."""
+def _sized(workspace, workspace_bytes, size, desc):
+    """(address, bytes) of a workspace argument; an address without bytes is
+    taken to hold size(desc), what the call needs."""
     if workspace_bytes is None:
         workspace_bytes = (workspace.numel() * workspace.element_size()
-                           if hasattr(workspace, "numel") else need)
+                           if hasattr(workspace, "numel") else size(desc))
     return _bytes_ptr(workspace, "workspace", workspace_bytes), workspace_bytes
 
 
@@ -516,7 +517,7 @@ def embed_grad(e: zs_embed, ids, grad_out, grad_table, workspace, accumulate: bo
                stream=None, workspace_bytes=None) -> None:
     """The gradient of embed_lookup: grad_out are the T gradients of its rows,
     grad_table (of e.table_dtype) receives the table's."""
-    ws, nbytes = _sized(workspace, workspace_bytes, zs_embed_workspace_bytes(e))
+    ws, nbytes = _sized(workspace, workspace_bytes, zs_embed_workspace_bytes, e)
     _check(lib().embed_grad(
         C.byref(e), _ptr(ids, "ids", _IDS.get(e.id_dtype), e.tokens),
         _rows_ptr(grad_out, "grad_out", _ELEM.get(e.act_dtype), e.tokens, e.dim, e.act_pitch),
@@ -540,11 +541,11 @@ def zs_distill_workspace_bytes(d: zs_distill) -> int:
 
 
 def _targets(d: zs_distill, teacher_ids, teacher_logits, teacher_lse, labels) -> zs_targets:
-    ids = _IDS.get(d.id_dtype)
+    ids, rows, k = _IDS.get(d.id_dtype), d.rows, d.k
     return zs_targets(
-        _rows_ptr(teacher_ids, "teacher_ids", ids, d.rows, d.k, d.k),
-        _rows_ptr(teacher_logits, "teacher_logits", _ELEM.get(d.teacher_dtype), d.rows, d.k, d.k),
-        _ptr(teacher_lse, "teacher_lse", _F32, d.rows), _ptr(labels, "labels", ids, d.rows))
+        _rows_ptr(teacher_ids, "teacher_ids", ids, rows, k, k),
+        _rows_ptr(teacher_logits, "teacher_logits", _ELEM.get(d.teacher_dtype), rows, k, k),
+        _ptr(teacher_lse, "teacher_lse", _F32, rows), _ptr(labels, "labels", ids, rows))
 
 
 def _lse_ptr(d: zs_distill, t):
@@ -561,7 +562,7 @@ def distill_loss(d: zs_distill, logits, teacher_ids, teacher_logits, loss, lse, 
     """Row losses (loss: fp32[T], lse: fp32[T, 2]); loss_sum: one fp32 and
     counted: one int64, or None."""
     t = _targets(d, teacher_ids, teacher_logits, teacher_lse, labels)
-    ws, nbytes = _sized(workspace, workspace_bytes, zs_distill_workspace_bytes(d))
+    ws, nbytes = _sized(workspace, workspace_bytes, zs_distill_workspace_bytes, d)
     _check(lib().distill_loss(
         C.byref(d), _logits_ptr(d, logits, "logits", d.logits_pitch), C.byref(t),
         _ptr(loss, "loss", _F32, d.rows), _lse_ptr(d, lse),
@@ -589,7 +590,7 @@ def distill_loss_grad(d: zs_distill, logits, teacher_ids, teacher_logits, loss, 
                       workspace_bytes=None) -> None:
     """distill_loss and distill_grad in one call; grad may be logits."""
     t = _targets(d, teacher_ids, teacher_logits, teacher_lse, labels)
-    ws, nbytes = _sized(workspace, workspace_bytes, zs_distill_workspace_bytes(d))
+    ws, nbytes = _sized(workspace, workspace_bytes, zs_distill_workspace_bytes, d)
     _check(lib().distill_loss_grad(
         C.byref(d), _logits_ptr(d, logits, "logits", d.logits_pitch), C.byref(t),
         _ptr(loss, "loss", _F32, d.rows), _lse_ptr(d, lse),

@@ -43,6 +43,15 @@ def test_rows_of_another_pitch_are_refused(shape, rows, width, pitch):
         rows_ptr(shape, rows, width, pitch)
 
 
+@pytest.mark.parametrize("rows,pitch,ok", [(6, 56, True), (6, 50, False), (6, 64, False),
+                                           (1, 50, True), (1, 56, True), (0, 50, True)])
+def test_views_of_padded_rows(rows, pitch, ok):
+    """The first 50 of 56 columns: rows 56 apart, or one row."""
+    view = torch.zeros((6, 56), dtype=BF16)[:, :50]
+    with pytest.raises(ValueError, match=ACCEPTED if ok else "apart|contiguous"):
+        Z._rows_ptr(view, "rows", None, rows, 50, pitch)
+
+
 def test_padded_tables_and_logits_need_their_pitch():
     """Each tensor of rows of each call: 8 columns wider than the default
     pitch is refused, with the pitch named it is accepted."""
