@@ -323,9 +323,12 @@ __device__ __forceinline__ uint64_t same_row(bool in, int row, int bits)
 // handled 64 at a time.  A token's place is: its row's start, the tokens of
 // that row in earlier waves, those handled earlier by its wave, and those in
 // lower lanes (4096 tokens 7 us, 65536 23 us, 40 with a wait behind each
-// load: every CU looks at every id, some 20 instructions for 64).  Where a wave's list is too short for its tokens (one id in
-// most of them), all waves read the ids again and handle 64 whenever they
-// have them, once to count and once to place.
+// load: every CU looks at every id, some 20 instructions for 64).  Where a
+// wave's list is too short for its tokens (one id in most of them), all waves
+// read the ids again and handle 64 whenever they have them, once to count and
+// once to place.  Half of 65536 tokens with one id do that, as do 131072 with
+// ids that fall as 1/v: the gradient of 128256 rows of 64 in bf16 takes 129 and
+// 121 us then, 54 for 65536 such tokens without.
 template <typename ID>
 __global__ void __launch_bounds__(kSortThreads)
     k_embed_sort(EmbedArgs a, SortShape s, int32_t* order, int32_t* row_of, int32_t* starts)
@@ -714,8 +717,10 @@ __global__ void __launch_bounds__(kEmbedThreads)
 }
 
 // The runs that cross chunks (at 65536 tokens 11 us, most of it blocks that
-// find none): the block of the chunk a run begins in adds
-// its partials in order, each wave a contiguous part of them.
+// find none): the block of the chunk a run begins in adds its partials in
+// order, each wave a contiguous part of them.  So the longest run is one
+// block's work for its columns: with it, 65536 tokens of 4096 bf16 that all
+// have one id take 459 us, 340 with ids that fall as 1/v.
 template <typename GT, int N, bool ADD>
 __global__ void __launch_bounds__(kEmbedThreads)
     k_embed_join(EmbedArgs a, SumPlan p, int64_t b0)

@@ -241,7 +241,10 @@ class ShardRun:
 class TableBatch:
     """One rank's micro-batch: T token ids, the teacher's entries and the
     labels of its T positions (int64 on the GPU; -100: not trained on), and
-    how many labels count, which the program that made them knows."""
+    how many labels count, which the program that made them knows: the rank's
+    mean is over them, and they weigh the rank.  (The distillation counts its
+    rows on the device; at alpha = 1 a labelled row without a teacher entry has
+    loss 0 and is in `valid` but not in `counted`.)"""
     ids: torch.Tensor              # int64 [T]
     teacher_ids: torch.Tensor      # int64 [T, k]
     teacher_logits: torch.Tensor   # float32 [T, k]
@@ -261,6 +264,11 @@ class TableRun:
                        squared norms summed
             per shard  zero_shard_step into its slot of the gathered table,
                        from which the next step looks up.
+
+    f32_grads: the type in which a rank's gradient of the table is held, added
+    to and reduced.  The head's matrix product itself is one of bf16 operands
+    and leaves its kernel rounded to bf16, as a mixed-precision program's
+    products do; embed_grad adds to it in fp32.
 
     body: a differentiable function of the hidden states [T, dim] that stands
     for the model between the two uses of the table; None: the identity."""
@@ -325,6 +333,7 @@ class TableRun:
         distill_loss_grad(self.targets, self.logits, b.teacher_ids, b.teacher_logits,
                           self.loss[r], self.dlogits, labels=b.labels, loss_sum=self.loss_sum,
                           counted=self.counted, accumulate=r > 0, workspace=self.distill_ws)
+        # rounded to bf16 by the product
         self.grad_table(r).copy_(torch.mm(self.dlogits.t(), h))
         dh = torch.mm(self.dlogits, self.table)
         if self.body is None:

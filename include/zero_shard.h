@@ -342,12 +342,13 @@ int shard_grad_sqnorm_noalloc(const zs_shard* s, const uint16_t* const* grad_sli
  * The operators at the two ends of a training step, whose parameter is the
  * (often tied) vocabulary table of a sharded unit: embed_lookup reads rows of
  * the vector the all-gather filled, embed_grad writes the gradient whose
- * slices shard_grad_reduce reads, and the distillation loss counts the valid
- * tokens that zs_reduce.rank_tokens weighs the ranks by.  All conventions
- * above hold, except: the table, its gradient, activations, logits and their
- * gradient need only the alignment of their element (rows of odd length and
- * tables inside a flat vector are allowed), and fp32 sums here may use fused
- * multiply-add. */
+ * slices shard_grad_reduce reads, and the distillation loss makes the gradient
+ * both start from.  (It counts its rows on the device; zs_reduce.rank_tokens,
+ * by which the ranks are weighed, is host memory that the program fills.)  All
+ * conventions above hold, except: the table, its gradient, activations, logits
+ * and their gradient need only the alignment of their element (rows of odd
+ * length and tables inside a flat vector are allowed), and fp32 sums here may
+ * use fused multiply-add. */
 
 /* Element types of these calls, and the types of ids. */
 #define ZS_BF16   0
@@ -400,7 +401,9 @@ size_t zs_embed_workspace_bytes(const zs_embed* e);
  * there already).  Tokens are sorted by row, stably, and summed in fp32 in an
  * order that depends on the sizes and ids alone (run-to-run deterministic:
  * no floating-point atomics); the result is rounded once to table_dtype.  The
- * sort reads the ids once for every 512 rows of the table, at least 256 times.
+ * sort reads the ids once for every 512 rows of the table, at least 256 times:
+ * its cost is tokens times rows / 512.  Where one row has most of the tokens,
+ * a part of the sort reads them three times, and one block joins its sums.
  *   workspace  device, 16-byte aligned, >= zs_embed_workspace_bytes(e) bytes;
  *              contents on entry are ignored.
  * Errors: ZS_ENULL, ZS_EINVAL_EMBED, ZS_EALIGN, ZS_EUNSUPPORTED (more than
@@ -481,9 +484,9 @@ int distill_grad(const zs_distill* d, const void* logits, const zs_targets* t,
 /* Both in one call: the loss is usually the last operator of the forward
  * pass, so its gradient can be taken there.  From 128 rows on, and for rows of
  * at most 1024 16-byte vectors, the logits are read once (of a row, the first
- * 131072 in bf16, 65536 in fp32; all of it twice where its largest logit times
- * log2(e) / tau is beyond 65536).  Arguments and errors as above; lse_out may
- * be NULL.  The loss may differ from distill_loss's in its last bits, the
+ * 131072 in bf16, 65536 in fp32; where its largest logit times log2(e) / tau
+ * is beyond 65536 in size, it is read again for the sums and for the
+ * gradient).  Arguments and errors as above; lse_out may be NULL.  The loss may differ from distill_loss's in its last bits, the
  * gradient from distill_grad's by what rounding lse to fp32 takes. */
 int distill_loss_grad(const zs_distill* d, const void* logits, const zs_targets* t,
                       float* loss_out, float* lse_out, const float* row_grad, void* grad_out,
