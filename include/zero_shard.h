@@ -486,8 +486,9 @@ int distill_grad(const zs_distill* d, const void* logits, const zs_targets* t,
  * at most 1024 16-byte vectors, the logits are read once (of a row, the first
  * 131072 in bf16, 65536 in fp32; where its largest logit times log2(e) / tau
  * is beyond 65536 in size, it is read again for the sums and for the
- * gradient).  Arguments and errors as above; lse_out may be NULL.  The loss may differ from distill_loss's in its last bits, the
- * gradient from distill_grad's by what rounding lse to fp32 takes. */
+ * gradient).  Arguments and errors as above; lse_out may be NULL.  The loss
+ * may differ from distill_loss's in its last bits, the gradient from
+ * distill_grad's by what rounding lse to fp32 takes. */
 int distill_loss_grad(const zs_distill* d, const void* logits, const zs_targets* t,
                       float* loss_out, float* lse_out, const float* row_grad, void* grad_out,
                       float* loss_sum, int64_t* counted, int32_t accumulate, void* workspace,

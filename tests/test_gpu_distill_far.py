@@ -83,7 +83,8 @@ def test_bounds_are_narrow(dtype, tau, alpha):
         assert bool((off > 4 * r["loss_err"]).all())
         softmax = torch.exp(z - r["lse"][:, :1])
         at = softmax.argmax(1, keepdim=True)
-        moved = alpha * tau * softmax.gather(1, at)[:, 0] * torch.expm1((r["lse"][:, 0] - lse).abs())
+        top = softmax.gather(1, at)[:, 0]
+        moved = alpha * tau * top * torch.expm1((r["lse"][:, 0] - lse).abs())
         plain = ~torch.zeros_like(q, dtype=torch.bool).scatter_(1, p.ids, True).gather(1, at)[:, 0]
         assert bool(((moved > 4 * r["grad_err"].gather(1, at)[:, 0]) | ~plain).all())
 
