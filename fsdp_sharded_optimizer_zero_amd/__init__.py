@@ -37,6 +37,7 @@ ZS_EINVAL_UNITS = -14
 ZS_ESCRATCH = -15
 ZS_EINVAL_EMBED = -16
 ZS_EINVAL_DISTILL = -17
+ZS_EINVAL_TENSORS = -18
 ZS_SCRATCH_BYTES = 16 << 20
 ZS_GRAD_BF16 = 0
 ZS_GRAD_F32 = 1
@@ -49,6 +50,7 @@ ZS_ID_I32 = 0
 ZS_ID_I64 = 1
 ZS_EMBED_MAX = 1 << 24
 ZS_DISTILL_MAX_K = 1024
+ZS_TENSORS_MAX = 1 << 24
 
 
 class ZSError(RuntimeError):
@@ -95,6 +97,18 @@ class zs_distill(C.Structure):
 class zs_targets(C.Structure):
     _fields_ = [("teacher_ids", C.c_void_p), ("teacher_logits", C.c_void_p),
                 ("teacher_lse", C.c_void_p), ("labels", C.c_void_p)]
+
+
+class zs_tensor(C.Structure):
+    _fields_ = [("in_", C.c_void_p), ("out", C.c_void_p), ("rows", C.c_int64),
+                ("cols", C.c_int64), ("in_pitch", C.c_int64), ("out_pitch", C.c_int64),
+                ("in_dtype", C.c_int32), ("out_dtype", C.c_int32)]
+
+
+class zs_tensors(C.Structure):
+    _fields_ = [("count", C.c_int64), ("elements", C.c_int64), ("chunks", C.c_int64),
+                ("chunk_bytes", C.c_int64), ("plan_bytes", C.c_int64), ("has_out", C.c_int32),
+                ("reserved", C.c_int32)]
 
 
 _lib = None
@@ -150,6 +164,16 @@ def _open(path: str):
     L.distill_loss_grad.argtypes = [P(zs_distill), vp, P(zs_targets), vp, vp, vp, vp, vp, vp,
                                     i32, vp, C.c_size_t, vp]
     L.distill_loss_grad.restype = C.c_int
+    L.zs_tensors_layout.argtypes = [vp, i64, P(zs_tensors)]
+    L.zs_tensors_layout.restype = C.c_int
+    L.zs_tensors_plan.argtypes = [vp, P(zs_tensors), vp, C.c_size_t]
+    L.zs_tensors_plan.restype = C.c_int
+    L.tensors_sqnorm.argtypes = [P(zs_tensors), vp, vp, vp, i32, vp]
+    L.tensors_sqnorm.restype = C.c_int
+    L.tensors_clip.argtypes = [P(zs_tensors), vp, f64, vp, f64, vp]
+    L.tensors_clip.restype = C.c_int
+    L.tensors_clip_norm.argtypes = [P(zs_tensors), vp, f64, vp, vp, i32, vp]
+    L.tensors_clip_norm.restype = C.c_int
     L.zs_init.argtypes = []
     L.zs_init.restype = C.c_int
     return L
@@ -599,6 +623,140 @@ def distill_loss_grad(d: zs_distill, logits, teacher_ids, teacher_logits, loss, 
         _ptr(counted, "counted", _I64, 1), 1 if accumulate else 0, ws, nbytes,
         _stream_on(stream, logits, teacher_ids, teacher_logits, teacher_lse, labels, loss, lse,
                    row_grad, grad, loss_sum, counted, workspace)), "distill_loss_grad")
+
+
+# ---- many tensors: the global norm and the clip ---------------------------------------
+
+_TENSOR_TYPES = {"bfloat16": ZS_BF16, "float32": ZS_F32}
+
+
+def _rows_of(t):
+    """(rows, cols, pitch) of a tensor whose elements fill memory in any order of
+    its dimensions, or whose rows (the dimensions but the one of stride 1 or
+    those that are contiguous with it) are evenly apart; None for any other."""
+    dims = sorted(((st, n) for st, n in zip(t.stride(), t.shape) if n != 1))
+    if t.numel() == 0:
+        return 0, 0, 0
+    cols = 1
+    while dims and dims[0][0] == cols:
+        cols *= dims.pop(0)[1]
+    if not dims:
+        return 1, cols, cols
+    pitch, rows = dims[0][0], 1
+    for st, n in dims:
+        if st != pitch * rows:
+            return None
+        rows *= n
+    return (rows, cols, pitch) if pitch >= cols else None
+
+
+class Tensors:
+    """A list of tensors as tensors_sqnorm, tensors_clip and tensors_clip_norm
+    take it: the struct, its plan on the GPU, and the tensors themselves, whose
+    memory the plan names.  Make a new one where a tensor is replaced by another
+    (a gradient that was set to None and made anew)."""
+
+    def __init__(self, struct, plan, tensors, out, device):
+        self.struct, self.plan, self.tensors, self.out = struct, plan, tensors, out
+        self.device = device
+
+
+def _tensor_entry(i, t, o):
+    for what, x in (("tensors", t), ("out", o)):
+        if not hasattr(x, "data_ptr"):
+            raise TypeError(f"{what}[{i}]: a torch tensor is required")
+        if _dtype_name(x.dtype) not in _TENSOR_TYPES:
+            raise ValueError(f"{what}[{i}]: dtype {_dtype_name(x.dtype)}, expected bfloat16 or "
+                             "float32")
+        if not x.is_cuda:
+            raise ValueError(f"{what}[{i}]: a GPU tensor is required (got {x.device})")
+    rows = _rows_of(t)
+    if rows is None:
+        raise ValueError(f"tensors[{i}]: shape {tuple(t.shape)} with strides {t.stride()} is not "
+                         "rows of contiguous elements evenly apart")
+    other = rows
+    if o is not t:
+        if o.shape != t.shape:
+            raise ValueError(f"out[{i}]: shape {tuple(o.shape)}, the tensor's is {tuple(t.shape)}")
+        other = _rows_of(o)
+        if other is None or not _same_order(t, o) or (
+                other[:2] != rows[:2] and 1 not in (other[0], rows[0])):
+            raise ValueError(f"out[{i}]: strides {o.stride()}, the tensor's are {t.stride()}: not "
+                             "the same rows of elements in the same order")
+        # one without gaps is cut into the other's rows
+        if rows[0] < other[0]:
+            rows = (other[0], other[1], other[1])
+        elif other[0] < rows[0]:
+            other = (rows[0], rows[1], rows[1])
+    return zs_tensor(t.data_ptr(), o.data_ptr(), rows[0], rows[1], rows[2], other[2],
+                     _TENSOR_TYPES[_dtype_name(t.dtype)], _TENSOR_TYPES[_dtype_name(o.dtype)])
+
+
+def _same_order(t, o) -> bool:
+    """Whether the dimensions larger than 1 have their strides in the same order."""
+    dims = [d for d, n in enumerate(t.shape) if n != 1]
+    return (sorted(dims, key=lambda d: t.stride(d)) == sorted(dims, key=lambda d: o.stride(d)))
+
+
+def make_tensors(tensors, out=None) -> Tensors:
+    """The list of GPU tensors (bfloat16 or float32, of any sizes) whose global
+    norm is taken; out: where each goes when it is clipped, a list of tensors of
+    the same shapes (views of a flat buffer, say), or None: in place.
+
+    A tensor's elements may be in any order in memory as long as they fill it
+    (a transposed gradient), or its rows may be evenly apart."""
+    tensors = list(tensors)
+    out = tensors if out is None else list(out)
+    if len(out) != len(tensors):
+        raise ValueError(f"{len(tensors)} tensors, {len(out)} out")
+    arr = (zs_tensor * max(len(tensors), 1))(*[_tensor_entry(i, t, o) for i, (t, o)
+                                               in enumerate(zip(tensors, out))])
+    device = _cuda().current_device()
+    for i, t in enumerate(tensors + out):
+        if t.get_device() != device:
+            raise ValueError(f"a tensor on GPU {t.get_device()}: the current device is {device}")
+    struct = zs_tensors()
+    _check(lib().zs_tensors_layout(arr, len(tensors), C.byref(struct)), "zs_tensors_layout")
+    host = _torch.empty(struct.plan_bytes, dtype=_torch.uint8)
+    _check(lib().zs_tensors_plan(arr, C.byref(struct), host.data_ptr(), struct.plan_bytes),
+           "zs_tensors_plan")
+    # pageable memory: the copy has ended when .to returns
+    return Tensors(struct, host.to(f"cuda:{device}"), tensors, out, device)
+
+
+def _tensors_on(t: Tensors, stream, *scalars):
+    stream = _stream_on(stream, t.plan, *scalars)
+    return C.byref(t.struct), t.plan.data_ptr(), stream
+
+
+def tensors_sqnorm(t: Tensors, sqnorm_out, tensor_sqnorms=None, accumulate: bool = False,
+                   stream=None) -> None:
+    """The squared norm of the whole list into sqnorm_out (one float64);
+    tensor_sqnorms: float64[count] for each tensor's own, or None."""
+    struct, plan, stream = _tensors_on(t, stream, sqnorm_out, tensor_sqnorms)
+    _check(lib().tensors_sqnorm(
+        struct, plan, _ptr(sqnorm_out, "sqnorm_out", _F64, 1),
+        _ptr(tensor_sqnorms, "tensor_sqnorms", _F64, t.struct.count),
+        1 if accumulate else 0, stream), "tensors_sqnorm")
+
+
+def tensors_clip(t: Tensors, max_norm: float, sqnorm, other_sqnorm: float = 0.0,
+                 stream=None) -> None:
+    """Every tensor times the coefficient of the global squared norm *sqnorm +
+    other_sqnorm, as zero_shard_step takes it."""
+    struct, plan, stream = _tensors_on(t, stream, sqnorm)
+    _check(lib().tensors_clip(struct, plan, float(max_norm), _ptr(sqnorm, "sqnorm", _F64, 1),
+                              float(other_sqnorm), stream), "tensors_clip")
+
+
+def tensors_clip_norm(t: Tensors, max_norm: float, sqnorm_out, tensor_sqnorms=None,
+                      accumulate: bool = False, stream=None) -> None:
+    """tensors_sqnorm, then tensors_clip by what it left in sqnorm_out."""
+    struct, plan, stream = _tensors_on(t, stream, sqnorm_out, tensor_sqnorms)
+    _check(lib().tensors_clip_norm(
+        struct, plan, float(max_norm), _ptr(sqnorm_out, "sqnorm_out", _F64, 1),
+        _ptr(tensor_sqnorms, "tensor_sqnorms", _F64, t.struct.count),
+        1 if accumulate else 0, stream), "tensors_clip_norm")
 
 
 def build(verbose: bool = False) -> str:

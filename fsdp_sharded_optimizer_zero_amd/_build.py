@@ -40,13 +40,16 @@ def build(verbose: bool = False) -> str:
     abi_o = os.path.join(BUILD, "zs_abi.o")
     kern_o = os.path.join(BUILD, "zs_kernels.o")
     vocab_o = os.path.join(BUILD, "zs_vocab.o")
+    tensors_o = os.path.join(BUILD, "zs_tensors.o")
     _run(["g++", *HOST_FLAGS, "-c", os.path.join(CSRC, "zs_host.cpp"), "-o", host_o], verbose)
     _run(["g++", *HOST_FLAGS, "-c", os.path.join(CSRC, "zs_abi.cpp"), "-o", abi_o], verbose)
     _run(["hipcc", *HIP_FLAGS, "-c", os.path.join(CSRC, "zs_kernels.hip"), "-o", kern_o],
          verbose)
     _run(["hipcc", *HIP_FLAGS, "-c", os.path.join(CSRC, "zs_vocab.hip"), "-o", vocab_o], verbose)
+    _run(["hipcc", *HIP_FLAGS, "-c", os.path.join(CSRC, "zs_tensors.hip"), "-o", tensors_o],
+         verbose)
     _run(["hipcc", "--offload-arch=gfx950", "-shared", "-fPIC", "-o", LIB + ".tmp", host_o,
-          abi_o, kern_o, vocab_o], verbose)
+          abi_o, kern_o, vocab_o, tensors_o], verbose)
     os.replace(LIB + ".tmp", LIB)
     small_o = os.path.join(BUILD, "zs_kernels_smallgrid.o")
     _run(["hipcc", *HIP_FLAGS, *SMALLGRID_DEFS, "-c",
@@ -54,8 +57,11 @@ def build(verbose: bool = False) -> str:
     small_vocab_o = os.path.join(BUILD, "zs_vocab_smallgrid.o")
     _run(["hipcc", *HIP_FLAGS, *SMALLGRID_DEFS, "-c", os.path.join(CSRC, "zs_vocab.hip"), "-o",
           small_vocab_o], verbose)
+    small_tensors_o = os.path.join(BUILD, "zs_tensors_smallgrid.o")
+    _run(["hipcc", *HIP_FLAGS, *SMALLGRID_DEFS, "-c", os.path.join(CSRC, "zs_tensors.hip"), "-o",
+          small_tensors_o], verbose)
     _run(["hipcc", "--offload-arch=gfx950", "-shared", "-fPIC", "-o", SMALLGRID_LIB + ".tmp",
-          host_o, abi_o, small_o, small_vocab_o], verbose)
+          host_o, abi_o, small_o, small_vocab_o, small_tensors_o], verbose)
     os.replace(SMALLGRID_LIB + ".tmp", SMALLGRID_LIB)
     # bench-only copy kernel (not part of the ABI)
     _run(["hipcc", *HIP_FLAGS, "-shared", "-o", BENCH_LIB + ".tmp",

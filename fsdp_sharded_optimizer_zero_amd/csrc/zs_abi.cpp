@@ -82,8 +82,9 @@ int sqnorm_pass(const zs_shard* s, const uint16_t* const* grad_slices, float* me
 
 extern "C" int zs_init(void)
 {
-    const int rc = prepare_device();
-    return rc != ZS_OK ? rc : prepare_vocab();
+    int rc = prepare_device();
+    if (rc == ZS_OK) rc = prepare_vocab();
+    return rc != ZS_OK ? rc : prepare_tensors();
 }
 
 extern "C" int shard_grad_sqnorm(const zs_shard* s, const uint16_t* const* grad_slices,
@@ -430,4 +431,86 @@ extern "C" int distill_loss_grad(const zs_distill* d, const void* logits, const 
     rc = set_loss(d, loss_out, lse_out, loss_sum, counted, accumulate, workspace, workspace_bytes,
                   &a);
     return rc != ZS_OK ? rc : enqueue_distill_loss(a, true, stream);
+}
+
+// ---- many tensors -------------------------------------------------------------------
+
+namespace zs {
+namespace {
+
+int tensors_args(const zs_tensors* t, void* plan, TensorsArgs* a)
+{
+    const int rc = check_tensors(t);
+    if (rc != ZS_OK) return rc;
+    if (!plan) return ZS_ENULL;
+    if (!aligned16(plan)) return ZS_EALIGN;
+    const TensorsSpace w = tensors_space(t->count, t->chunks);
+    char* base = static_cast<char*>(plan);
+    *a = TensorsArgs{};
+    a->arrived = reinterpret_cast<uint32_t*>(base + w.arrived);
+    a->table = reinterpret_cast<const TensorChunk*>(base + w.table);
+    a->first = reinterpret_cast<const int64_t*>(base + w.first);
+    a->partials = reinterpret_cast<double*>(base + w.partials);
+    a->count = t->count;
+    a->chunks = t->chunks;
+    return ZS_OK;
+}
+
+int set_sqnorm(double* sqnorm_out, double* tensor_sqnorms, int32_t accumulate, TensorsArgs* a)
+{
+    if (!sqnorm_out) return ZS_ENULL;
+    if (!aligned8(sqnorm_out) || !aligned8(tensor_sqnorms)) return ZS_EALIGN;
+    a->sqnorm_out = sqnorm_out;
+    a->each = tensor_sqnorms;
+    a->accumulate = accumulate ? 1 : 0;
+    return ZS_OK;
+}
+
+int set_clip(const zs_tensors* t, double max_norm, const double* sqnorm, double other_sqnorm,
+             TensorsArgs* a)
+{
+    if (!(max_norm > 0.0 && max_norm <= 1.7976931348623157e308) || other_sqnorm < 0.0)
+        return ZS_EINVAL_HPARAM;
+    if (!sqnorm || !t->has_out) return ZS_ENULL;
+    if (!aligned8(sqnorm)) return ZS_EALIGN;
+    a->sqnorm = sqnorm;
+    a->other = other_sqnorm;
+    a->max_norm = max_norm;
+    return ZS_OK;
+}
+
+}  // namespace
+}  // namespace zs
+
+extern "C" int tensors_sqnorm(const zs_tensors* t, void* plan, double* sqnorm_out,
+                              double* tensor_sqnorms, int32_t accumulate, void* stream)
+{
+    TensorsArgs a;
+    int rc = tensors_args(t, plan, &a);
+    if (rc != ZS_OK) return rc;
+    if ((rc = set_sqnorm(sqnorm_out, tensor_sqnorms, accumulate, &a)) != ZS_OK) return rc;
+    return enqueue_tensors_sqnorm(a, stream);
+}
+
+extern "C" int tensors_clip(const zs_tensors* t, void* plan, double max_norm, const double* sqnorm,
+                            double other_sqnorm, void* stream)
+{
+    TensorsArgs a;
+    int rc = tensors_args(t, plan, &a);
+    if (rc != ZS_OK) return rc;
+    if ((rc = set_clip(t, max_norm, sqnorm, other_sqnorm, &a)) != ZS_OK) return rc;
+    return enqueue_tensors_clip(a, stream);
+}
+
+extern "C" int tensors_clip_norm(const zs_tensors* t, void* plan, double max_norm,
+                                 double* sqnorm_out, double* tensor_sqnorms, int32_t accumulate,
+                                 void* stream)
+{
+    TensorsArgs a;
+    int rc = tensors_args(t, plan, &a);
+    if (rc != ZS_OK) return rc;
+    if ((rc = set_sqnorm(sqnorm_out, tensor_sqnorms, accumulate, &a)) != ZS_OK) return rc;
+    if ((rc = set_clip(t, max_norm, sqnorm_out, 0.0, &a)) != ZS_OK) return rc;
+    if ((rc = enqueue_tensors_sqnorm(a, stream)) != ZS_OK) return rc;
+    return enqueue_tensors_clip(a, stream);
 }

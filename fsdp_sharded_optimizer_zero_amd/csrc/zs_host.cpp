@@ -11,6 +11,7 @@
 // "Distributed Training Basics -- DDP and FSDP" (Memory accounting).
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "zs_internal.h"
 
@@ -110,6 +111,77 @@ DistillSpace distill_space(int64_t rows, int64_t vocab, int32_t k, bool f32)
     w.bytes = w.picked + (s.rows_loss_grad ? 0 : round_up(rows * (k + 1) * int64_t(4), 256));
     return w;
 }
+
+TensorsSpace tensors_space(int64_t count, int64_t chunks)
+{
+    TensorsSpace w;
+    w.arrived = 0;
+    w.table = 256;
+    w.first = w.table + round_up(chunks * static_cast<int64_t>(sizeof(TensorChunk)), 256);
+    w.partials = w.first + round_up((count + 1) * 8, 256);
+    w.bytes = w.partials + round_up(chunks > 0 ? chunks * 8 : 8, 256);
+    return w;
+}
+
+int check_tensors(const zs_tensors* t)
+{
+    if (!t) return ZS_ENULL;
+    if (t->count < 0 || t->count > ZS_TENSORS_MAX || t->chunks < 0 || t->elements < t->chunks ||
+        t->chunks > (int64_t(1) << 40) || t->reserved != 0 ||
+        t->plan_bytes != tensors_space(t->count, t->chunks).bytes)
+        return ZS_EINVAL_TENSORS;
+    return ZS_OK;
+}
+
+namespace {
+
+int64_t elem_size(int32_t dtype) { return dtype == ZS_F32 ? 4 : 2; }
+
+int check_tensor(const zs_tensor& t)
+{
+    const int64_t most = int64_t(1) << 60;
+    if (t.rows < 0 || t.cols < 0) return ZS_EINVAL_TENSORS;
+    if ((t.in_dtype != ZS_BF16 && t.in_dtype != ZS_F32) ||
+        (t.out_dtype != ZS_BF16 && t.out_dtype != ZS_F32))
+        return ZS_EINVAL_TENSORS;
+    if (t.rows == 0 || t.cols == 0) return ZS_OK;
+    if (t.cols > most / t.rows) return ZS_EINVAL_TENSORS;
+    if (t.rows > 1 && (t.in_pitch < t.cols || t.in_pitch > most / t.rows)) return ZS_EINVAL_TENSORS;
+    if (!t.in) return ZS_ENULL;
+    if (reinterpret_cast<uintptr_t>(t.in) % elem_size(t.in_dtype)) return ZS_EALIGN;
+    if (!t.out) return ZS_OK;
+    if (t.rows > 1 && (t.out_pitch < t.cols || t.out_pitch > most / t.rows))
+        return ZS_EINVAL_TENSORS;
+    if (reinterpret_cast<uintptr_t>(t.out) % elem_size(t.out_dtype)) return ZS_EALIGN;
+    if (t.in == t.out &&
+        (t.in_dtype != t.out_dtype || (t.rows > 1 && t.in_pitch != t.out_pitch)))
+        return ZS_EINVAL_TENSORS;
+    return ZS_OK;
+}
+
+// A tensor as it is cut: its rows are one where nothing lies between them, and
+// a piece has `take` elements of one row, or `take` whole rows.
+struct Cut {
+    int64_t rows, cols, take, pieces;
+    bool whole_rows;
+};
+Cut cut_tensor(const zs_tensor& t, int64_t chunk_bytes)
+{
+    Cut c{t.rows, t.cols, 0, 0, false};
+    if (c.rows == 0 || c.cols == 0) return Cut{0, 0, 1, 0, false};
+    if (c.rows > 1 && t.in_pitch == c.cols && (!t.out || t.out_pitch == c.cols)) {
+        c.cols *= c.rows;
+        c.rows = 1;
+    }
+    const int64_t elems = chunk_bytes / elem_size(t.in_dtype);
+    c.whole_rows = c.rows > 1 && c.cols <= elems;
+    c.take = c.whole_rows ? elems / c.cols : elems;
+    c.pieces = c.whole_rows ? (c.rows + c.take - 1) / c.take
+                            : c.rows * ((c.cols + c.take - 1) / c.take);
+    return c;
+}
+
+}  // namespace
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -212,6 +284,88 @@ size_t zs_distill_workspace_bytes(const zs_distill* d)
     return static_cast<size_t>(zs::distill_space(d->rows, d->vocab, d->k, d->logits_dtype == ZS_F32).bytes);
 }
 
+int zs_tensors_layout(const zs_tensor* list, int64_t count, zs_tensors* t)
+{
+    if (!t || (count > 0 && !list)) return ZS_ENULL;
+    if (count < 0) return ZS_EINVAL_TENSORS;
+    if (count > ZS_TENSORS_MAX) return ZS_EUNSUPPORTED;
+    zs_tensors r{};
+    r.count = count;
+    r.has_out = 1;
+    int64_t bytes = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const int rc = zs::check_tensor(list[i]);
+        if (rc != ZS_OK) return rc;
+        const int64_t n = list[i].rows * list[i].cols;
+        if (n == 0) continue;
+        r.elements += n;
+        bytes += n * zs::elem_size(list[i].in_dtype);
+        // (each is at most 2^62: the sum is looked at before it can overflow)
+        if (bytes > (int64_t(1) << 60)) return ZS_EINVAL_TENSORS;
+        if (!list[i].out) r.has_out = 0;
+    }
+    // 32 KB a piece; fewer bytes where that makes too few pieces to fill the
+    // GPU, more (a multiple) where one block would have too many to join
+    r.chunk_bytes = zs::kTensorChunk;
+    while (r.chunk_bytes > zs::kTensorChunkMin && bytes / r.chunk_bytes < zs::kTensorChunksMin)
+        r.chunk_bytes /= 2;
+    if (bytes / r.chunk_bytes > zs::kTensorChunks) {
+        r.chunk_bytes = zs::round_up(bytes / zs::kTensorChunks, zs::kTensorChunk);
+        if (r.chunk_bytes > zs::kTensorChunkMax) r.chunk_bytes = zs::kTensorChunkMax;
+    }
+    for (int64_t i = 0; i < count; ++i)
+        r.chunks += zs::cut_tensor(list[i], r.chunk_bytes).pieces;
+    r.plan_bytes = zs::tensors_space(r.count, r.chunks).bytes;
+    *t = r;
+    return ZS_OK;
+}
+
+int zs_tensors_plan(const zs_tensor* list, const zs_tensors* t, void* plan, size_t plan_bytes)
+{
+    if (!t || !plan) return ZS_ENULL;
+    zs_tensors ref;
+    const int rc = zs_tensors_layout(list, t->count, &ref);
+    if (rc != ZS_OK) return rc;
+    if (std::memcmp(&ref, t, sizeof ref) != 0) return ZS_EINVAL_TENSORS;
+    if (plan_bytes < static_cast<size_t>(t->plan_bytes)) return ZS_EWORKSPACE;
+    const zs::TensorsSpace w = zs::tensors_space(t->count, t->chunks);
+    char* base = static_cast<char*>(plan);
+    std::memset(base, 0, static_cast<size_t>(t->plan_bytes));
+    char* at = base + w.table;
+    int64_t pieces = 0;
+    for (int64_t i = 0; i < t->count; ++i) {
+        std::memcpy(base + w.first + i * 8, &pieces, 8);
+        const zs_tensor& x = list[i];
+        const zs::Cut c = zs::cut_tensor(x, t->chunk_bytes);
+        const int64_t is = zs::elem_size(x.in_dtype), os = zs::elem_size(x.out_dtype);
+        const auto put = [&](int64_t row, int64_t col, int64_t rows, int64_t cols) {
+            zs::TensorChunk k{};
+            k.in = reinterpret_cast<uint64_t>(x.in) + (row * x.in_pitch + col) * is;
+            k.out = x.out ? reinterpret_cast<uint64_t>(x.out) + (row * x.out_pitch + col) * os : 0;
+            k.in_pitch = x.in_pitch;
+            k.out_pitch = x.out_pitch;
+            k.rows = static_cast<int32_t>(rows);
+            k.cols = static_cast<int32_t>(cols);
+            k.kind = (x.in_dtype == ZS_F32 ? zs::kChunkInF32 : 0) |
+                     (x.out_dtype == ZS_F32 ? zs::kChunkOutF32 : 0);
+            k.tensor = static_cast<int32_t>(i);
+            std::memcpy(at, &k, sizeof k);
+            at += sizeof k;
+            ++pieces;
+        };
+        if (c.whole_rows) {
+            for (int64_t r = 0; r < c.rows; r += c.take)
+                put(r, 0, c.rows - r < c.take ? c.rows - r : c.take, c.cols);
+        } else {
+            for (int64_t r = 0; r < c.rows; ++r)
+                for (int64_t col = 0; col < c.cols; col += c.take)
+                    put(r, col, 1, c.cols - col < c.take ? c.cols - col : c.take);
+        }
+    }
+    std::memcpy(base + w.first + t->count * 8, &pieces, 8);
+    return ZS_OK;
+}
+
 double zs_state_bytes(double psi, int32_t n_d, int32_t stage, double K)
 {
     if (!(psi > 0.0) || n_d < 1) return -1.0;
@@ -256,6 +410,9 @@ const char* zs_strerror(int code)
     case ZS_EINVAL_EMBED: return "invalid zs_embed (a size, pitch, type or scale out of range)";
     case ZS_EINVAL_DISTILL:
         return "invalid zs_distill (a size, pitch, type, temperature, alpha or scale out of range)";
+    case ZS_EINVAL_TENSORS:
+        return "invalid zs_tensor (a size, pitch or type out of range, or in place with another), "
+               "or zs_tensors not as zs_tensors_layout left it";
     default: return "unknown error";
     }
 }

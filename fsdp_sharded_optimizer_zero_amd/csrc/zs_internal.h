@@ -271,6 +271,58 @@ int enqueue_distill_grad(DistillArgs a, void* stream);
 // may be captured); ZS_OK or ZS_ELAUNCH.
 int prepare_vocab();
 
+// ---- many tensors (zs_tensors.hip) -------------------------------------------------
+
+// A piece of a list, one block's work: `rows` rows of `cols` elements of one
+// tensor (of a contiguous tensor: one row).
+struct TensorChunk {
+    uint64_t in, out;
+    int64_t in_pitch, out_pitch;
+    int32_t rows, cols;
+    int32_t kind;           // kChunkInF32 | kChunkOutF32
+    int32_t tensor;
+};
+static_assert(sizeof(TensorChunk) == 48, "the plan's layout");
+constexpr int32_t kChunkInF32 = 1, kChunkOutF32 = 2;
+
+constexpr int kTensorThreads = 256;
+// A block has 32 KB of its piece under way: 8 16-byte vectors a thread.
+constexpr int64_t kTensorChunk = int64_t(kTensorThreads) * 8 * 16;
+constexpr int64_t kTensorChunkMin = int64_t(kTensorThreads) * 16;
+constexpr int64_t kTensorChunkMax = int64_t(1) << 30;   // elements fit 32 bits
+// Pieces a list of few large tensors is cut into, at most and at least.
+constexpr int64_t kTensorChunks = 8192;
+constexpr int64_t kTensorChunksMin = 1024;
+// Up to here one launch makes the norm: the last block joins the partials.
+constexpr int64_t kTensorOneLaunch = 256;
+
+// The plan, in bytes from its start.
+struct TensorsSpace {
+    int64_t arrived;    // uint32: blocks that have ended (one launch); 0 between calls
+    int64_t table;      // TensorChunk[chunks]
+    int64_t first;      // int64[count + 1]: each tensor's first piece
+    int64_t partials;   // double[chunks]
+    int64_t bytes;
+};
+TensorsSpace tensors_space(int64_t count, int64_t chunks);
+
+struct TensorsArgs {
+    const TensorChunk* table;
+    const int64_t* first;
+    double* partials;
+    uint32_t* arrived;
+    int64_t count, chunks;
+    double* sqnorm_out;
+    double* each;
+    int32_t accumulate;
+    const double* sqnorm;
+    double other, max_norm;
+};
+int enqueue_tensors_sqnorm(const TensorsArgs& a, void* stream);
+int enqueue_tensors_clip(const TensorsArgs& a, void* stream);
+int prepare_tensors();
+int check_tensors(const zs_tensors* t);
+
 int check_embed(const zs_embed* e);
 int check_distill(const zs_distill* d);
 

@@ -53,8 +53,8 @@
  *    are updated in place.  Calls that write the same buffers must not run
  *    concurrently on different streams.
  *
- * The calls on the vocabulary table (embed_*, distill_*) state their own
- * conventions where they differ.
+ * The calls on the vocabulary table (embed_*, distill_*) and on many tensors
+ * (tensors_*) state their own conventions where they differ.
  */
 #ifndef ZERO_SHARD_H
 #define ZERO_SHARD_H
@@ -98,6 +98,9 @@ extern "C" {
                                     range, or reserved != 0 */
 #define ZS_EINVAL_DISTILL (-17)  /* zs_distill: a size, pitch, type, temperature,
                                     alpha or scale out of range */
+#define ZS_EINVAL_TENSORS (-18)  /* zs_tensor: a size, pitch or type out of range,
+                                    or in place with another type or pitch;
+                                    zs_tensors: not as zs_tensors_layout left it */
 
 #define ZS_MAX_RANKS 64          /* gradient slices one call can reduce */
 /* Bytes of the per-device static scratch array of shard_grad_sqnorm_noalloc:
@@ -493,6 +496,91 @@ int distill_loss_grad(const zs_distill* d, const void* logits, const zs_targets*
                       float* loss_out, float* lse_out, const float* row_grad, void* grad_out,
                       float* loss_sum, int64_t* counted, int32_t accumulate, void* workspace,
                       size_t workspace_bytes, void* stream);
+
+/* ---- many tensors: the global norm and the clip ------------------------------------
+ *
+ * Gradients that lie tensor by tensor and not in a flat shard: parameters kept
+ * whole on every rank (norm weights, biases, small tables) beside the sharded
+ * ones, or a unit's gradients before they are flattened.  The clip at the update
+ * boundary ("Distributed Training Basics -- DDP and FSDP", the DDP reference
+ * program: clip_grad_norm_ over the model's parameters) takes one norm over all
+ * of them, and over sharded ones it sums the squared norms ("Data parallelism,
+ * ZeRO and FSDP", section 7 "Common mistakes"): tensors_sqnorm adds to the same
+ * scalar as shard_grad_sqnorm, and zero_shard_step and tensors_clip read it.
+ * All conventions above hold, except: tensors need only the alignment of their
+ * element, and a tensor may be clipped in place. */
+
+/* One tensor of a list: `rows` rows of `cols` elements, `pitch` elements apart
+ * (a contiguous tensor: one row, or pitches equal to cols). */
+typedef struct zs_tensor {
+    const void* in;        /* device; unused where rows * cols == 0 */
+    void* out;             /* device: where the clipped tensor goes; `in` itself: in
+                              place; NULL: the list is for norms only */
+    int64_t rows, cols;    /* >= 0 */
+    int64_t in_pitch;      /* >= cols where rows > 1 */
+    int64_t out_pitch;
+    int32_t in_dtype;      /* ZS_BF16 or ZS_F32 */
+    int32_t out_dtype;     /* the same; in place as in_dtype */
+} zs_tensor;
+
+/* Tensors one list holds at most. */
+#define ZS_TENSORS_MAX ((int64_t)1 << 24)
+
+/* A list as the device calls take it, filled by zs_tensors_layout. */
+typedef struct zs_tensors {
+    int64_t count;         /* tensors */
+    int64_t elements;      /* in all of them */
+    int64_t chunks;        /* pieces the list is cut into: one block each */
+    int64_t chunk_bytes;   /* bytes of a piece at most */
+    int64_t plan_bytes;    /* of the plan */
+    int32_t has_out;       /* every tensor with elements has an `out` */
+    int32_t reserved;      /* 0 */
+} zs_tensors;
+
+/* Checks a list of `count` tensors and fills *t.  Host only.
+ * Errors: ZS_ENULL (list, with count > 0; out; a tensor's `in`), ZS_EALIGN,
+ * ZS_EINVAL_TENSORS, ZS_EUNSUPPORTED (count > ZS_TENSORS_MAX). */
+int zs_tensors_layout(const zs_tensor* list, int64_t count, zs_tensors* t);
+
+/* Fills `plan`, t->plan_bytes bytes of HOST memory, with the list cut into
+ * pieces; the caller copies it to the device (16-byte aligned) and hands that
+ * copy to the calls below, for as long as the tensors stay where they are: the
+ * plan holds their addresses.  The device copy is the calls' workspace too: one
+ * call at a time uses it, and nothing else writes it.  Host only.
+ * Errors: as zs_tensors_layout, ZS_EINVAL_TENSORS (t is not this list's),
+ * ZS_EWORKSPACE (plan_bytes < t->plan_bytes). */
+int zs_tensors_plan(const zs_tensor* list, const zs_tensors* t, void* plan, size_t plan_bytes);
+
+/* The squared L2 norm of the whole list: the sum of (double)x^2 over every
+ * element of every tensor, in fp64 in an order fixed by the list's sizes
+ * (run-to-run deterministic).
+ *   plan            device, t->plan_bytes bytes as zs_tensors_plan filled them.
+ *   sqnorm_out      device, one double; accumulate != 0 adds to it (to a
+ *                   shard's squared norm, or another list's).
+ *   tensor_sqnorms  device double[count] or NULL: each tensor's own (set, also
+ *                   where `accumulate` is given; 0 for one without elements).
+ * NaN and Inf propagate.  Errors: ZS_ENULL, ZS_EALIGN, ZS_EINVAL_TENSORS,
+ * ZS_ELAUNCH. */
+int tensors_sqnorm(const zs_tensors* t, void* plan, double* sqnorm_out, double* tensor_sqnorms,
+                   int32_t accumulate, void* stream);
+
+/* out = coef * in for every element of every tensor, the product in fp32 and
+ * rounded once to out_dtype, with the coefficient of zero_shard_step: Q =
+ * *sqnorm + other_sqnorm, coef = f32(min(1, max_norm / (sqrt(Q) + 1e-6))) in
+ * double, NaN kept.  A coefficient of 1 leaves a tensor that is clipped in place
+ * untouched.  Elements between cols and the pitch are not read or written.
+ * `out` may be part of a flat buffer (the fp32 gradient zero_shard_step reads as
+ * mean_in), at any element.
+ * Errors: ZS_ENULL (also: a tensor without `out`), ZS_EALIGN, ZS_EINVAL_TENSORS,
+ * ZS_EINVAL_HPARAM (max_norm not positive and finite, other_sqnorm < 0),
+ * ZS_ELAUNCH. */
+int tensors_clip(const zs_tensors* t, void* plan, double max_norm, const double* sqnorm,
+                 double other_sqnorm, void* stream);
+
+/* Both in one call: tensors_sqnorm into sqnorm_out (added to it if accumulate),
+ * then tensors_clip by it.  Errors: as above. */
+int tensors_clip_norm(const zs_tensors* t, void* plan, double max_norm, double* sqnorm_out,
+                      double* tensor_sqnorms, int32_t accumulate, void* stream);
 
 /* Per-device set-up for the current HIP device: queries its LDS size, raises
  * the kernels' dynamic-LDS limits and takes the address of the static
