@@ -38,6 +38,7 @@ ZS_ESCRATCH = -15
 ZS_EINVAL_EMBED = -16
 ZS_EINVAL_DISTILL = -17
 ZS_EINVAL_TENSORS = -18
+ZS_EINVAL_RELPOS = -19
 ZS_SCRATCH_BYTES = 16 << 20
 ZS_GRAD_BF16 = 0
 ZS_GRAD_F32 = 1
@@ -51,6 +52,8 @@ ZS_ID_I64 = 1
 ZS_EMBED_MAX = 1 << 24
 ZS_DISTILL_MAX_K = 1024
 ZS_TENSORS_MAX = 1 << 24
+ZS_RELPOS_MAX_BUCKETS = 256
+ZS_RELPOS_FAR = 1 << 29
 
 
 class ZSError(RuntimeError):
@@ -109,6 +112,15 @@ class zs_tensors(C.Structure):
     _fields_ = [("count", C.c_int64), ("elements", C.c_int64), ("chunks", C.c_int64),
                 ("chunk_bytes", C.c_int64), ("plan_bytes", C.c_int64), ("has_out", C.c_int32),
                 ("reserved", C.c_int32)]
+
+
+class zs_relpos(C.Structure):
+    _fields_ = [("batch", C.c_int64), ("heads", C.c_int64), ("queries", C.c_int64),
+                ("keys", C.c_int64), ("in_pitch", C.c_int64 * 3), ("out_pitch", C.c_int64 * 3),
+                ("table_pitch", C.c_int64), ("query_start", C.c_int64),
+                ("max_distance", C.c_int64), ("buckets", C.c_int32),
+                ("bidirectional", C.c_int32), ("causal", C.c_int32), ("dtype", C.c_int32),
+                ("table_dtype", C.c_int32), ("id_dtype", C.c_int32), ("scale", C.c_double)]
 
 
 _lib = None
@@ -174,6 +186,12 @@ def _open(path: str):
     L.tensors_clip.restype = C.c_int
     L.tensors_clip_norm.argtypes = [P(zs_tensors), vp, f64, vp, vp, i32, vp]
     L.tensors_clip_norm.restype = C.c_int
+    L.relpos_bias.argtypes = [P(zs_relpos), vp, vp, vp, vp, vp, vp]
+    L.relpos_bias.restype = C.c_int
+    L.zs_relpos_workspace_bytes.argtypes = [P(zs_relpos)]
+    L.zs_relpos_workspace_bytes.restype = C.c_size_t
+    L.relpos_bias_grad.argtypes = [P(zs_relpos), vp, vp, vp, vp, vp, i32, vp, C.c_size_t, vp]
+    L.relpos_bias_grad.restype = C.c_int
     L.zs_init.argtypes = []
     L.zs_init.restype = C.c_int
     return L
@@ -623,6 +641,91 @@ def distill_loss_grad(d: zs_distill, logits, teacher_ids, teacher_logits, loss, 
         _ptr(counted, "counted", _I64, 1), 1 if accumulate else 0, ws, nbytes,
         _stream_on(stream, logits, teacher_ids, teacher_logits, teacher_lse, labels, loss, lse,
                    row_grad, grad, loss_sum, counted, workspace)), "distill_loss_grad")
+
+
+# ---- the position-bias table: bias by buckets, and its gradient ------------------------
+
+def make_relpos(heads: int, queries: int, keys: int, buckets: int = 32, max_distance: int = 128,
+                batch: int = 1, bidirectional: bool = True, causal: bool = False,
+                query_start: int = 0, scale: float = 1.0, dtype: int = ZS_BF16,
+                table_dtype: int = ZS_F32, id_dtype: int = ZS_ID_I64, in_pitch=None,
+                out_pitch=None, table_pitch=None) -> zs_relpos:
+    """in_pitch, out_pitch: elements from one sequence, head, query to the next
+    ([batch, heads, queries, keys] without gaps if not given)."""
+    plain = (heads * queries * keys, queries * keys, keys)
+    triple = C.c_int64 * 3
+    return zs_relpos(batch, heads, queries, keys, triple(*(in_pitch or plain)),
+                     triple(*(out_pitch or plain)),
+                     heads if table_pitch is None else table_pitch, query_start, max_distance,
+                     buckets, 1 if bidirectional else 0, 1 if causal else 0, dtype, table_dtype,
+                     id_dtype, float(scale))
+
+
+def zs_relpos_workspace_bytes(r: zs_relpos) -> int:
+    return lib().zs_relpos_workspace_bytes(C.byref(r))
+
+
+def _places_ptr(r: zs_relpos, t, what: str, pitch):
+    """Address of a [batch, heads, queries, keys] tensor with these pitches (a
+    batch of one may be left out), or of a flat buffer that holds them."""
+    if t is None or isinstance(t, int):
+        return t
+    sizes = (r.batch, r.heads, r.queries, r.keys)
+    need = 0
+    if min(sizes) > 0:
+        need = r.keys + sum((n - 1) * p for n, p in zip(sizes, pitch))
+    shape, strides = getattr(t, "shape", ()), ()
+    if len(shape) == 4 or (len(shape) == 3 and r.batch == 1):
+        strides = t.stride()
+        if len(shape) == 3:
+            shape, strides = (1, *shape), (0, *strides)
+        if tuple(shape) != sizes or any(
+                n > 1 and s != p for n, s, p in zip(sizes, strides, (*pitch, 1))):
+            raise ValueError(f"{what}: shape {tuple(t.shape)} with strides {t.stride()}, the call "
+                             f"needs {sizes} with strides {(*pitch, 1)}")
+        if need == 0 or t.is_contiguous():
+            return _ptr(t, what, _ELEM.get(r.dtype))
+        # the checks of _ptr on its first place; the extent is the shape's
+        return _ptr(t[(slice(0, 1),) * t.dim()], what, _ELEM.get(r.dtype))
+    if len(shape) != 1:
+        raise ValueError(f"{what}: shape {tuple(shape)}, the call needs {sizes}")
+    return _ptr(t, what, _ELEM.get(r.dtype), need)
+
+
+def _relpos_table(r: zs_relpos, t, what: str):
+    return _rows_ptr(t, what, _ELEM.get(r.table_dtype), r.buckets, r.heads, r.table_pitch)
+
+
+def relpos_bias(r: zs_relpos, table, out, scores=None, key_lengths=None, query_starts=None,
+                stream=None) -> None:
+    """The bias of every place of [batch, heads, queries, keys] into out, added to
+    scale * scores where they are given (out may be scores); -Inf where a key is
+    not seen.  table: [buckets, heads]."""
+    ids = _IDS.get(r.id_dtype)
+    _check(lib().relpos_bias(
+        C.byref(r), _relpos_table(r, table, "table"),
+        _places_ptr(r, scores, "scores", r.in_pitch),
+        _ptr(key_lengths, "key_lengths", ids, r.batch),
+        _ptr(query_starts, "query_starts", ids, r.batch),
+        _places_ptr(r, out, "out", r.out_pitch),
+        _stream_on(stream, table, scores, key_lengths, query_starts, out)), "relpos_bias")
+
+
+def relpos_bias_grad(r: zs_relpos, grad, grad_table, workspace, grad_scores=None,
+                     key_lengths=None, query_starts=None, accumulate: bool = False, stream=None,
+                     workspace_bytes=None) -> None:
+    """The gradient of relpos_bias: grad is that of its output, grad_table (of
+    r.table_dtype) receives the table's, grad_scores (may be grad) the scores'."""
+    ws, nbytes = _sized(workspace, workspace_bytes, zs_relpos_workspace_bytes, r)
+    ids = _IDS.get(r.id_dtype)
+    _check(lib().relpos_bias_grad(
+        C.byref(r), _places_ptr(r, grad, "grad", r.in_pitch),
+        _ptr(key_lengths, "key_lengths", ids, r.batch),
+        _ptr(query_starts, "query_starts", ids, r.batch),
+        _relpos_table(r, grad_table, "grad_table"),
+        _places_ptr(r, grad_scores, "grad_scores", r.out_pitch), 1 if accumulate else 0, ws,
+        nbytes, _stream_on(stream, grad, key_lengths, query_starts, grad_table, grad_scores,
+                           workspace)), "relpos_bias_grad")
 
 
 # ---- many tensors: the global norm and the clip ---------------------------------------

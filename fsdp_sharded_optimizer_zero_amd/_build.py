@@ -41,6 +41,7 @@ def build(verbose: bool = False) -> str:
     kern_o = os.path.join(BUILD, "zs_kernels.o")
     vocab_o = os.path.join(BUILD, "zs_vocab.o")
     tensors_o = os.path.join(BUILD, "zs_tensors.o")
+    relpos_o = os.path.join(BUILD, "zs_relpos.o")
     _run(["g++", *HOST_FLAGS, "-c", os.path.join(CSRC, "zs_host.cpp"), "-o", host_o], verbose)
     _run(["g++", *HOST_FLAGS, "-c", os.path.join(CSRC, "zs_abi.cpp"), "-o", abi_o], verbose)
     _run(["hipcc", *HIP_FLAGS, "-c", os.path.join(CSRC, "zs_kernels.hip"), "-o", kern_o],
@@ -48,8 +49,10 @@ def build(verbose: bool = False) -> str:
     _run(["hipcc", *HIP_FLAGS, "-c", os.path.join(CSRC, "zs_vocab.hip"), "-o", vocab_o], verbose)
     _run(["hipcc", *HIP_FLAGS, "-c", os.path.join(CSRC, "zs_tensors.hip"), "-o", tensors_o],
          verbose)
+    _run(["hipcc", *HIP_FLAGS, "-c", os.path.join(CSRC, "zs_relpos.hip"), "-o", relpos_o],
+         verbose)
     _run(["hipcc", "--offload-arch=gfx950", "-shared", "-fPIC", "-o", LIB + ".tmp", host_o,
-          abi_o, kern_o, vocab_o, tensors_o], verbose)
+          abi_o, kern_o, vocab_o, tensors_o, relpos_o], verbose)
     os.replace(LIB + ".tmp", LIB)
     small_o = os.path.join(BUILD, "zs_kernels_smallgrid.o")
     _run(["hipcc", *HIP_FLAGS, *SMALLGRID_DEFS, "-c",
@@ -60,8 +63,12 @@ def build(verbose: bool = False) -> str:
     small_tensors_o = os.path.join(BUILD, "zs_tensors_smallgrid.o")
     _run(["hipcc", *HIP_FLAGS, *SMALLGRID_DEFS, "-c", os.path.join(CSRC, "zs_tensors.hip"), "-o",
           small_tensors_o], verbose)
+    small_relpos_o = os.path.join(BUILD, "zs_relpos_smallgrid.o")
+    _run(["hipcc", *HIP_FLAGS, *SMALLGRID_DEFS, "-c", os.path.join(CSRC, "zs_relpos.hip"), "-o",
+          small_relpos_o], verbose)
     _run(["hipcc", "--offload-arch=gfx950", "-shared", "-fPIC", "-o", SMALLGRID_LIB + ".tmp",
-          host_o, abi_o, small_o, small_vocab_o, small_tensors_o], verbose)
+          host_o, abi_o, small_o, small_vocab_o, small_tensors_o, small_relpos_o],
+         verbose)
     os.replace(SMALLGRID_LIB + ".tmp", SMALLGRID_LIB)
     # bench-only copy kernel (not part of the ABI)
     _run(["hipcc", *HIP_FLAGS, "-shared", "-o", BENCH_LIB + ".tmp",

@@ -84,6 +84,7 @@ extern "C" int zs_init(void)
 {
     int rc = prepare_device();
     if (rc == ZS_OK) rc = prepare_vocab();
+    if (rc == ZS_OK) rc = prepare_relpos();
     return rc != ZS_OK ? rc : prepare_tensors();
 }
 
@@ -431,6 +432,89 @@ extern "C" int distill_loss_grad(const zs_distill* d, const void* logits, const 
     rc = set_loss(d, loss_out, lse_out, loss_sum, counted, accumulate, workspace, workspace_bytes,
                   &a);
     return rc != ZS_OK ? rc : enqueue_distill_loss(a, true, stream);
+}
+
+// ---- the position-bias table ---------------------------------------------------------
+
+namespace zs {
+namespace {
+
+// What both calls share: the struct into the kernel arguments, and the checks
+// of what lies on the device.
+int relpos_args(const zs_relpos* r, const void* in, void* out, const void* key_lengths,
+                const void* query_starts, RelposArgs* a)
+{
+    const int rc = check_relpos(r);
+    if (rc != ZS_OK) return rc;
+    const uintptr_t size = elem_bytes(r->dtype);
+    if (!aligned_to(in, size) || !aligned_to(out, size) ||
+        !aligned_to(key_lengths, id_bytes(r->id_dtype)) ||
+        !aligned_to(query_starts, id_bytes(r->id_dtype)))
+        return ZS_EALIGN;
+    const int64_t n[3] = {r->batch, r->heads, r->queries};
+    *a = RelposArgs{};
+    for (int k = 0; k < 3; ++k) {
+        if (in && in == out && n[k] > 1 && r->in_pitch[k] != r->out_pitch[k])
+            return ZS_EINVAL_RELPOS;
+        a->in_pitch[k] = n[k] > 1 ? r->in_pitch[k] : 0;
+        a->out_pitch[k] = n[k] > 1 ? r->out_pitch[k] : 0;
+    }
+    a->in = in;
+    a->out = out;
+    a->lengths = key_lengths;
+    a->starts = query_starts;
+    a->batch = r->batch;
+    a->heads = r->heads;
+    a->queries = r->queries;
+    a->keys = r->keys;
+    a->table_pitch = r->table_pitch;
+    a->start = r->query_start;
+    a->causal = r->causal;
+    a->f32 = r->dtype == ZS_F32;
+    a->table_f32 = r->table_dtype == ZS_F32;
+    a->id64 = r->id_dtype == ZS_ID_I64;
+    a->scale = static_cast<float>(r->scale);
+    relpos_buckets(r, a);
+    return ZS_OK;
+}
+
+bool relpos_empty(const zs_relpos* r) { return r->batch == 0 || r->queries == 0 || r->keys == 0; }
+
+}  // namespace
+}  // namespace zs
+
+extern "C" int relpos_bias(const zs_relpos* r, const void* table, const void* scores,
+                           const void* key_lengths, const void* query_starts, void* out,
+                           void* stream)
+{
+    RelposArgs a;
+    const int rc = relpos_args(r, scores, out, key_lengths, query_starts, &a);
+    if (rc != ZS_OK) return rc;
+    if (relpos_empty(r)) return ZS_OK;
+    if (!table || !out) return ZS_ENULL;
+    if (!aligned_to(table, elem_bytes(r->table_dtype))) return ZS_EALIGN;
+    a.table = table;
+    relpos_bias_shape(&a);
+    return enqueue_relpos_bias(a, stream);
+}
+
+extern "C" int relpos_bias_grad(const zs_relpos* r, const void* grad, const void* key_lengths,
+                                const void* query_starts, void* grad_table, void* grad_scores,
+                                int32_t accumulate, void* workspace, size_t workspace_bytes,
+                                void* stream)
+{
+    RelposArgs a;
+    const int rc = relpos_args(r, grad, grad_scores, key_lengths, query_starts, &a);
+    if (rc != ZS_OK) return rc;
+    if (!grad_table || !workspace || (!grad && !relpos_empty(r))) return ZS_ENULL;
+    if (!aligned16(workspace) || !aligned_to(grad_table, elem_bytes(r->table_dtype)))
+        return ZS_EALIGN;
+    relpos_grad_shape(&a);
+    if (workspace_bytes < static_cast<size_t>(relpos_parts_bytes(a))) return ZS_EWORKSPACE;
+    a.table_grad = grad_table;
+    a.parts = static_cast<float*>(workspace);
+    a.accumulate = accumulate ? 1 : 0;
+    return enqueue_relpos_grad(a, stream);
 }
 
 // ---- many tensors -------------------------------------------------------------------

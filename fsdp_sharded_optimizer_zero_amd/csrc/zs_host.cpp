@@ -183,6 +183,144 @@ Cut cut_tensor(const zs_tensor& t, int64_t chunk_bytes)
 
 }  // namespace
 
+int check_relpos(const zs_relpos* r)
+{
+    if (!r) return ZS_ENULL;
+    const int64_t far = ZS_RELPOS_FAR;
+    if (r->batch < 0 || r->batch > far || r->heads < 1 || r->heads > 65536 || r->queries < 0 ||
+        r->queries > far || r->keys < 0 || r->keys > far)
+        return ZS_EINVAL_RELPOS;
+    // every place and every tile has a number of 62 bits
+    const int64_t most = int64_t(1) << 56;
+    const int64_t n[3] = {r->batch, r->heads, r->queries};
+    int64_t places = r->keys > 0 ? r->keys : 1;
+    for (int k = 0; k < 3; ++k) {
+        const int64_t size = n[k] > 0 ? n[k] : 1;
+        if (places > most / size) return ZS_EINVAL_RELPOS;
+        places *= size;
+        if (n[k] < 2) continue;
+        if (r->in_pitch[k] < r->keys || r->out_pitch[k] < r->keys ||
+            r->in_pitch[k] > most / n[k] || r->out_pitch[k] > most / n[k])
+            return ZS_EINVAL_RELPOS;
+    }
+    if (r->table_pitch < r->heads || r->table_pitch > most) return ZS_EINVAL_RELPOS;
+    if (r->query_start < -far || r->query_start > far) return ZS_EINVAL_RELPOS;
+    if ((r->bidirectional != 0 && r->bidirectional != 1) || (r->causal != 0 && r->causal != 1))
+        return ZS_EINVAL_RELPOS;
+    if (r->buckets < (r->bidirectional ? 4 : 2) || r->buckets > ZS_RELPOS_MAX_BUCKETS)
+        return ZS_EINVAL_RELPOS;
+    const int64_t exact = (r->bidirectional ? r->buckets / 2 : r->buckets) / 2;
+    if (r->max_distance <= exact || r->max_distance > far) return ZS_EINVAL_RELPOS;
+    if ((r->dtype != ZS_BF16 && r->dtype != ZS_F32) ||
+        (r->table_dtype != ZS_BF16 && r->table_dtype != ZS_F32) ||
+        (r->id_dtype != ZS_ID_I32 && r->id_dtype != ZS_ID_I64))
+        return ZS_EINVAL_RELPOS;
+    if (!std::isfinite(static_cast<float>(r->scale))) return ZS_EINVAL_RELPOS;
+    return ZS_OK;
+}
+
+namespace {
+
+// A whole number of up to 4096 bits, little end first.
+struct Whole {
+    uint32_t w[129];
+    int n = 1;
+    Whole() { w[0] = 1; }
+    void times(uint32_t x)
+    {
+        uint64_t carry = 0;
+        for (int i = 0; i < n; ++i) {
+            carry += static_cast<uint64_t>(w[i]) * x;
+            w[i] = static_cast<uint32_t>(carry);
+            carry >>= 32;
+        }
+        if (carry) w[n++] = static_cast<uint32_t>(carry);
+    }
+    bool at_least(const Whole& o) const
+    {
+        if (n != o.n) return n > o.n;
+        for (int i = n - 1; i >= 0; --i)
+            if (w[i] != o.w[i]) return w[i] > o.w[i];
+        return true;
+    }
+};
+
+// Whether n^m >= exact^(m-k) far^k (each at most 2^29, m at most 128: 3712 bits).
+bool reaches(uint32_t n, uint32_t exact, uint32_t far, int m, int k)
+{
+    Whole a, b;
+    for (int i = 0; i < m; ++i) a.times(n);
+    for (int i = 0; i < m; ++i) b.times(i < k ? far : exact);
+    return a.at_least(b);
+}
+
+}  // namespace
+
+void relpos_buckets(const zs_relpos* r, RelposArgs* a)
+{
+    a->buckets = r->buckets;
+    a->two_sided = r->bidirectional;
+    a->half = r->bidirectional ? r->buckets / 2 : r->buckets;
+    a->exact = a->half / 2;
+    const int m = a->half - a->exact;
+    a->edge_count = m - 1;
+    a->edge_span = 1;
+    while (a->edge_span * 2 <= a->edge_count) a->edge_span *= 2;
+    const double step = std::log(static_cast<double>(r->max_distance) / a->exact) / m;
+    for (int k = 1; k < m; ++k) {
+        // where the step is reached, in fp64 (off by at most some 1e-14 of it);
+        // next to a whole number the whole numbers decide
+        const double x = a->exact * std::exp(k * step), near = std::round(x);
+        int64_t edge = static_cast<int64_t>(std::ceil(x));
+        if (std::fabs(x - near) <= 1e-12 * x) {
+            const int64_t c = static_cast<int64_t>(near);
+            edge = reaches(static_cast<uint32_t>(c), static_cast<uint32_t>(a->exact),
+                           static_cast<uint32_t>(r->max_distance), m, k)
+                       ? c
+                       : c + 1;
+        }
+        a->edges[k - 1] = static_cast<int32_t>(edge);
+    }
+}
+
+void relpos_bias_shape(RelposArgs* a)
+{
+    const int64_t n = a->f32 ? 4 : 8;
+    a->lane_shift = 3;
+    while (a->lane_shift < 8 && (n << a->lane_shift) < a->keys + n - 1) ++a->lane_shift;
+    const int64_t lanes = int64_t(1) << a->lane_shift, side = kRelposThreads / lanes;
+    a->col_tiles = a->keys > 0 ? (a->keys + n - 1 + lanes * n - 1) / (lanes * n) : 0;
+    const int64_t planes = a->batch * a->heads;
+    int64_t rows = side * 16 < kRelposRows ? side * 16 : kRelposRows;
+    while (rows > side && planes * a->col_tiles * ((a->queries + rows - 1) / rows) < 2048) rows /= 2;
+    if (rows > a->queries) rows = a->queries > 0 ? a->queries : 1;
+    a->rows = static_cast<int32_t>(rows);
+    a->row_tiles = (a->queries + rows - 1) / rows;
+    a->tiles = planes * a->row_tiles * a->col_tiles;
+}
+
+void relpos_grad_shape(RelposArgs* a)
+{
+    const int64_t n = a->f32 ? 4 : 8;
+    a->lane_shift = 3;
+    while (a->lane_shift < 6 && (n << a->lane_shift) < a->keys) ++a->lane_shift;
+    const int64_t lanes = int64_t(1) << a->lane_shift, groups = 64 / lanes;
+    a->col_tiles = (a->keys + lanes * n - 1) / (lanes * n);
+    const int64_t planes = a->batch * a->heads;
+    int64_t rows = kRelposRows / groups;
+    while (rows > n && planes * a->col_tiles * ((a->queries + rows * groups - 1) / (rows * groups)) < 4096)
+        rows /= 2;
+    a->rows = static_cast<int32_t>(rows);
+    a->row_tiles = (a->queries + rows * groups - 1) / (rows * groups);
+    a->tiles = planes * a->row_tiles * a->col_tiles;
+}
+
+int64_t relpos_parts_bytes(const RelposArgs& a)
+{
+    const int64_t bytes = a.tiles * a.buckets * 4;
+    return round_up(bytes > 0 ? bytes : 1, 256);
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // The section 5 simulator's adamw evaluates 1 - beta and 1 - beta**t in
@@ -276,6 +414,20 @@ size_t zs_embed_workspace_bytes(const zs_embed* e)
 {
     if (zs::check_embed(e) != ZS_OK || e->tokens > ZS_EMBED_MAX || e->rows > ZS_EMBED_MAX) return 0;
     return static_cast<size_t>(zs::embed_space(e->tokens, e->rows, e->dim).bytes);
+}
+
+size_t zs_relpos_workspace_bytes(const zs_relpos* r)
+{
+    if (zs::check_relpos(r) != ZS_OK) return 0;
+    zs::RelposArgs a{};
+    a.batch = r->batch;
+    a.heads = r->heads;
+    a.queries = r->queries;
+    a.keys = r->keys;
+    a.buckets = r->buckets;
+    a.f32 = r->dtype == ZS_F32;
+    zs::relpos_grad_shape(&a);
+    return static_cast<size_t>(zs::relpos_parts_bytes(a));
 }
 
 size_t zs_distill_workspace_bytes(const zs_distill* d)
@@ -413,6 +565,9 @@ const char* zs_strerror(int code)
     case ZS_EINVAL_TENSORS:
         return "invalid zs_tensor (a size, pitch or type out of range, or in place with another), "
                "or zs_tensors not as zs_tensors_layout left it";
+    case ZS_EINVAL_RELPOS:
+        return "invalid zs_relpos (a size, pitch, type, position, bucket count, distance or scale "
+               "out of range)";
     default: return "unknown error";
     }
 }

@@ -323,6 +323,49 @@ int enqueue_tensors_clip(const TensorsArgs& a, void* stream);
 int prepare_tensors();
 int check_tensors(const zs_tensors* t);
 
+// ---- the position-bias table (zs_relpos.hip) ---------------------------------------
+
+constexpr int kRelposThreads = 256;
+constexpr int kRelposRows = 128;            // of a tile, at most
+constexpr int kRelposMaxBuckets = ZS_RELPOS_MAX_BUCKETS;
+constexpr int kRelposMaxEdges = kRelposMaxBuckets / 2;
+constexpr int64_t kRelposFar = ZS_RELPOS_FAR;
+
+struct RelposArgs {
+    const void* in;         // scores (null: the bias alone) or the gradient
+    void* out;              // bias or scores; the scores' gradient (null: none)
+    const void* table;
+    void* table_grad;
+    const void* lengths;
+    const void* starts;
+    float* parts;           // workspace: fp32[heads][batch][row tiles][col tiles][buckets]
+    int64_t batch, heads, queries, keys;
+    int64_t in_pitch[3], out_pitch[3], table_pitch;
+    int64_t start;
+    int64_t row_tiles, col_tiles, tiles;
+    int32_t lane_shift;     // log2 of the lanes along the keys
+    int32_t rows;           // of a tile (gradient: of a group of lanes)
+    int32_t buckets, two_sided, causal;
+    int32_t half, exact;    // buckets of a side; those of single distances
+    int32_t edge_count;
+    int32_t edge_span;      // largest power of two up to edge_count
+    int32_t f32, table_f32, id64, accumulate;
+    float scale;
+    int32_t edges[kRelposMaxEdges];     // where the buckets behind `exact` begin
+};
+
+// How a call cuts its work (fills the tile fields).
+void relpos_bias_shape(RelposArgs* a);
+void relpos_grad_shape(RelposArgs* a);
+// The bucket fields from r.
+void relpos_buckets(const zs_relpos* r, RelposArgs* a);
+int64_t relpos_parts_bytes(const RelposArgs& a);
+
+int enqueue_relpos_bias(const RelposArgs& a, void* stream);
+int enqueue_relpos_grad(const RelposArgs& a, void* stream);
+int prepare_relpos();
+int check_relpos(const zs_relpos* r);
+
 int check_embed(const zs_embed* e);
 int check_distill(const zs_distill* d);
 

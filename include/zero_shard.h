@@ -53,8 +53,9 @@
  *    are updated in place.  Calls that write the same buffers must not run
  *    concurrently on different streams.
  *
- * The calls on the vocabulary table (embed_*, distill_*) and on many tensors
- * (tensors_*) state their own conventions where they differ.
+ * The calls on the vocabulary table (embed_*, distill_*), on the position table
+ * (relpos_*) and on many tensors (tensors_*) state their own conventions where
+ * they differ.
  */
 #ifndef ZERO_SHARD_H
 #define ZERO_SHARD_H
@@ -101,6 +102,8 @@ extern "C" {
 #define ZS_EINVAL_TENSORS (-18)  /* zs_tensor: a size, pitch or type out of range,
                                     or in place with another type or pitch;
                                     zs_tensors: not as zs_tensors_layout left it */
+#define ZS_EINVAL_RELPOS  (-19)  /* zs_relpos: a size, pitch, type, position, bucket
+                                    count, distance or scale out of range */
 
 #define ZS_MAX_RANKS 64          /* gradient slices one call can reduce */
 /* Bytes of the per-device static scratch array of shard_grad_sqnorm_noalloc:
@@ -496,6 +499,80 @@ int distill_loss_grad(const zs_distill* d, const void* logits, const zs_targets*
                       float* loss_out, float* lse_out, const float* row_grad, void* grad_out,
                       float* loss_sum, int64_t* counted, int32_t accumulate, void* workspace,
                       size_t workspace_bytes, void* stream);
+
+/* ---- the position-bias table: bias by buckets, and its gradient --------------------
+ *
+ * A learned bias of attention scores by the distance between query and key, a
+ * table of one row a bucket of distances and one column a head: the small table
+ * beside the vocabulary's, kept whole on every rank, whose gradient is one of
+ * the tensors of a list (tensors_*).  All conventions above hold, except:
+ * tensors need only the alignment of their element, and fp32 sums here may use
+ * fused multiply-add.
+ *
+ * Buckets, decided in whole numbers.  Key j and query i of a sequence are d =
+ * j - (start + i) apart.  Two-sided: S = buckets / 2 for each side, n = |d|, and
+ * a key behind the query (d > 0) has bucket S + side(n); one-sided: S = buckets
+ * and n = max(-d, 0).  With E = S / 2 (rounded down) and m = S - E:
+ *   side(n) = n                                              for n < E
+ *   side(n) = E + floor(m log(n / E) / log(max_distance / E)), at most S - 1
+ * that is, E plus the number of k in 1..m-1 with n^m >= E^(m-k) max_distance^k. */
+
+#define ZS_RELPOS_MAX_BUCKETS 256
+/* Largest number of queries and of keys, position and max_distance. */
+#define ZS_RELPOS_FAR ((int64_t)1 << 29)
+
+typedef struct zs_relpos {
+    int64_t batch, heads, queries, keys;   /* B, Q, K >= 0, 1 <= H <= 65536 */
+    int64_t in_pitch[3];   /* scores or gradient: elements from one sequence, head,
+                              query to the next (a pitch of a dimension of one is
+                              not looked at); keys are adjacent */
+    int64_t out_pitch[3];  /* the same of the output */
+    int64_t table_pitch;   /* elements from one bucket's row to the next, >= heads */
+    int64_t query_start;   /* position of query 0, key 0 being at 0 */
+    int64_t max_distance;  /* from here on a distance is in its side's last bucket;
+                              > E */
+    int32_t buckets;       /* 2..256, two-sided 4..256 */
+    int32_t bidirectional; /* 1: two-sided */
+    int32_t causal;        /* 1: a query sees keys up to its own position */
+    int32_t dtype;         /* ZS_BF16 or ZS_F32: scores, bias and their gradients */
+    int32_t table_dtype;   /* ZS_BF16 or ZS_F32: the table and its gradient */
+    int32_t id_dtype;      /* ZS_ID_I32 or ZS_ID_I64: key_lengths and query_starts */
+    double scale;          /* of the scores; rounded once to fp32; finite */
+} zs_relpos;
+
+/* out[b,h,i,j] = scale * scores[b,h,i,j] + table[bucket(d)][h], in fp32 and rounded
+ * once to dtype, where query i sees key j; -Inf where not, whatever scores hold.
+ *   table         device, `buckets` rows of `heads` elements.
+ *   scores        device or NULL (the bias alone); may be `out`, of its pitches.
+ *   key_lengths   device int[B] or NULL: sequence b has keys [0, key_lengths[b])
+ *                 (held to 0..K); a length of 0 leaves rows of -Inf.
+ *   query_starts  device int[B] or NULL: each sequence's own query_start (held to
+ *                 +-ZS_RELPOS_FAR); one token a sequence is queries = 1.
+ * Errors: ZS_ENULL, ZS_EINVAL_RELPOS (also: in place with other pitches),
+ * ZS_EALIGN, ZS_ELAUNCH. */
+int relpos_bias(const zs_relpos* r, const void* table, const void* scores,
+                const void* key_lengths, const void* query_starts, void* out, void* stream);
+
+/* Bytes of device workspace relpos_bias_grad needs: a row of buckets (fp32) for
+ * each tile of the scores (at least 128 places), rounded up to 256.  0 for a NULL
+ * or invalid r.  Host only. */
+size_t zs_relpos_workspace_bytes(const zs_relpos* r);
+
+/* The gradient of relpos_bias.  With g = grad[b,h,i,j] (in_pitch):
+ *   grad_table[u][h] = [grad_table[u][h] +] the sum of g over every b, i, j that
+ *                      is seen and whose bucket is u (+0 without any); accumulate
+ *                      != 0 adds.  A bias without a batch dimension that was
+ *                      broadcast over it has its gradient summed over b.
+ *   grad_scores      = scale * g where seen, +0 where not (out_pitch), or NULL;
+ *                      may be `grad`, of its pitches.
+ * g is not read where it is not seen.  Summed in fp32 along the diagonals of a
+ * tile and in fp64 over the tiles, in an order that depends on the sizes alone.
+ *   workspace  16-byte aligned, >= zs_relpos_workspace_bytes(r) bytes; contents
+ *              on entry are ignored.
+ * Errors: ZS_ENULL, ZS_EINVAL_RELPOS, ZS_EALIGN, ZS_EWORKSPACE, ZS_ELAUNCH. */
+int relpos_bias_grad(const zs_relpos* r, const void* grad, const void* key_lengths,
+                     const void* query_starts, void* grad_table, void* grad_scores,
+                     int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- many tensors: the global norm and the clip ------------------------------------
  *
