@@ -111,7 +111,7 @@ class zs_tensor(C.Structure):
 class zs_tensors(C.Structure):
     _fields_ = [("count", C.c_int64), ("elements", C.c_int64), ("chunks", C.c_int64),
                 ("chunk_bytes", C.c_int64), ("plan_bytes", C.c_int64), ("has_out", C.c_int32),
-                ("reserved", C.c_int32)]
+                ("stamp", C.c_uint32)]
 
 
 class zs_relpos(C.Structure):
@@ -679,7 +679,7 @@ def _places_ptr(r: zs_relpos, t, what: str, pitch):
         strides = t.stride()
         if len(shape) == 3:
             shape, strides = (1, *shape), (0, *strides)
-        if tuple(shape) != sizes or any(
+        if tuple(shape) != sizes or need and any(
                 n > 1 and s != p for n, s, p in zip(sizes, strides, (*pitch, 1))):
             raise ValueError(f"{what}: shape {tuple(t.shape)} with strides {t.stride()}, the call "
                              f"needs {sizes} with strides {(*pitch, 1)}")

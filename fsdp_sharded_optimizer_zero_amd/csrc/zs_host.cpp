@@ -10,6 +10,7 @@
 // and proof); the error convention follows the state_bytes helper of
 // "Distributed Training Basics -- DDP and FSDP" (Memory accounting).
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 #include <cstring>
 
@@ -123,11 +124,21 @@ TensorsSpace tensors_space(int64_t count, int64_t chunks)
     return w;
 }
 
+// FNV-1a over the fields before the stamp.
+static uint32_t tensors_stamp(const zs_tensors& t)
+{
+    unsigned char bytes[offsetof(zs_tensors, stamp)];
+    std::memcpy(bytes, &t, sizeof bytes);
+    uint32_t h = 2166136261u;
+    for (unsigned char b : bytes) h = (h ^ b) * 16777619u;
+    return h;
+}
+
 int check_tensors(const zs_tensors* t)
 {
     if (!t) return ZS_ENULL;
     if (t->count < 0 || t->count > ZS_TENSORS_MAX || t->chunks < 0 || t->elements < t->chunks ||
-        t->chunks > (int64_t(1) << 40) || t->reserved != 0 ||
+        t->chunks > (int64_t(1) << 40) || t->stamp != tensors_stamp(*t) ||
         t->plan_bytes != tensors_space(t->count, t->chunks).bytes)
         return ZS_EINVAL_TENSORS;
     return ZS_OK;
@@ -194,11 +205,12 @@ int check_relpos(const zs_relpos* r)
     const int64_t most = int64_t(1) << 56;
     const int64_t n[3] = {r->batch, r->heads, r->queries};
     int64_t places = r->keys > 0 ? r->keys : 1;
+    const bool empty = r->batch == 0 || r->queries == 0 || r->keys == 0;
     for (int k = 0; k < 3; ++k) {
         const int64_t size = n[k] > 0 ? n[k] : 1;
         if (places > most / size) return ZS_EINVAL_RELPOS;
         places *= size;
-        if (n[k] < 2) continue;
+        if (n[k] < 2 || empty) continue;
         if (r->in_pitch[k] < r->keys || r->out_pitch[k] < r->keys ||
             r->in_pitch[k] > most / n[k] || r->out_pitch[k] > most / n[k])
             return ZS_EINVAL_RELPOS;
@@ -468,6 +480,7 @@ int zs_tensors_layout(const zs_tensor* list, int64_t count, zs_tensors* t)
     for (int64_t i = 0; i < count; ++i)
         r.chunks += zs::cut_tensor(list[i], r.chunk_bytes).pieces;
     r.plan_bytes = zs::tensors_space(r.count, r.chunks).bytes;
+    r.stamp = zs::tensors_stamp(r);
     *t = r;
     return ZS_OK;
 }

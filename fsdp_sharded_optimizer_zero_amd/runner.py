@@ -24,7 +24,12 @@ the library calls of one optimizer step on one stream:
 own, its gradients made by the library's table operators instead of the
 generator: every simulated rank looks its tokens up, is held to a teacher's
 top logits, and leaves the table's gradient; then every rank's shard is
-reduced, weighted by the ranks' valid tokens, clipped and updated.
+reduced, weighted by the ranks' valid tokens, clipped and updated.  Parameters
+of the model between that are too small to shard (``whole``) are kept on every
+rank, tensor by tensor; their norm joins the shards'.
+
+``RelposBias`` is the position-bias table's call in such a model, with its
+gradient.
 """
 from __future__ import annotations
 
@@ -38,9 +43,10 @@ from zsgen.workloads import (STREAM_EXP_AVG, STREAM_EXP_AVG_SQ, STREAM_MASTER, W
 
 from . import (ZS_F32, ZS_GRAD_BF16, ZS_GRAD_F32, ZS_OUT_GATHER, ZS_OUT_SHARD, adamw,
                distill_loss_grad, embed_grad, embed_lookup, make_distill, make_embed, make_reduce,
-               shard_grad_reduce, shard_grad_sqnorm, shard_grad_sqnorm_units, shard_pack_gather,
+               make_tensors, relpos_bias, relpos_bias_grad, shard_grad_reduce, shard_grad_sqnorm,
+               shard_grad_sqnorm_units, shard_pack_gather, tensors_clip, tensors_sqnorm,
                zero_shard_step, zs_distill_workspace_bytes, zs_embed_workspace_bytes, zs_layout,
-               zs_workspace_bytes, zs_workspace_bytes_units)
+               zs_relpos_workspace_bytes, zs_workspace_bytes, zs_workspace_bytes_units)
 
 
 def _empty(n, dtype, device):
@@ -237,6 +243,35 @@ class ShardRun:
         return red * self.units, upd * self.units
 
 
+class RelposBias(torch.autograd.Function):
+    """RelposBias.apply(r, table, scores, key_lengths, query_starts): relpos_bias
+    of make_relpos's r (pitches without gaps), differentiable in table and
+    scores; scores None: the bias alone, [batch, heads, queries, keys]."""
+
+    @staticmethod
+    def forward(ctx, r, table, scores=None, key_lengths=None, query_starts=None):
+        shape = (r.batch, r.heads, r.queries, r.keys)
+        dtype = torch.float32 if r.dtype == ZS_F32 else torch.bfloat16
+        out = torch.empty(shape, dtype=dtype, device=table.device)
+        relpos_bias(r, table.contiguous(), out, None if scores is None else scores.contiguous(),
+                    key_lengths, query_starts)
+        ctx.r, ctx.scores = r, scores is not None and ctx.needs_input_grad[2]
+        ctx.save_for_backward(table, key_lengths, query_starts)
+        return out
+
+    @staticmethod
+    def backward(ctx, grad):
+        table, key_lengths, query_starts = ctx.saved_tensors
+        dtable = torch.empty(table.shape, dtype=table.dtype, device=table.device)
+        dscores = torch.empty_like(grad, memory_format=torch.contiguous_format) \
+            if ctx.scores else None
+        workspace = torch.empty(zs_relpos_workspace_bytes(ctx.r), dtype=torch.uint8,
+                                device=grad.device)
+        relpos_bias_grad(ctx.r, grad.contiguous(), dtable, workspace, dscores, key_lengths,
+                         query_starts)
+        return None, dtable, dscores, None, None
+
+
 @dataclass
 class TableBatch:
     """One rank's micro-batch: T token ids, the teacher's entries and the
@@ -271,12 +306,20 @@ class TableRun:
     products do; embed_grad adds to it in fp32.
 
     body: a differentiable function of the hidden states [T, dim] that stands
-    for the model between the two uses of the table; None: the identity."""
+    for the model between the two uses of the table; None: the identity.
+
+    whole: parameters of body (fp32 initial values; body is called with their
+    bf16 copies behind the hidden states) that every rank keeps whole.  Their
+    gradients, tensor by tensor, are averaged over the ranks by valid tokens (the
+    all-reduce's stand-in), their squared norm is added to the shards', and the
+    same coefficient clips them into the flat fp32 gradient of their own step:
+            tensors_sqnorm(accumulate), tensors_clip, zero_shard_step (stage 0)
+    """
 
     def __init__(self, rows: int, dim: int, n_d: int, tokens: int, k: int, scale: float = 1.0,
                  temperature: float = 1.0, alpha: float = 1.0, f32_grads: bool = True, body=None,
                  lr: float = 1e-3, weight_decay: float = 0.01, max_grad_norm: float = 1.0,
-                 device: str = "cuda"):
+                 whole=(), device: str = "cuda"):
         self.rows, self.dim, self.n_d, self.tokens = rows, dim, n_d, tokens
         self.body, self.f32_grads = body, f32_grads
         self.lr, self.weight_decay, self.max_grad_norm = lr, weight_decay, max_grad_norm
@@ -308,6 +351,29 @@ class TableRun:
         self.distill_ws = torch.empty(zs_distill_workspace_bytes(self.targets), dtype=torch.uint8,
                                       device=device)
 
+        self.whole = []
+        if whole:
+            self._keep_whole(list(whole), device)
+
+    def _keep_whole(self, values, device):
+        numel = [v.numel() for v in values]
+        self.whole_shard = s = zs_layout(sum(numel), 1, 0, 8, 0)     # stage 0: all of it
+        self.whole_state = [torch.zeros(max(s.valid_len, 8), device=device) for _ in range(3)]
+        self.whole_gather = torch.zeros(s.shard_len, dtype=torch.bfloat16, device=device)
+        self.whole_mean = torch.empty(max(s.valid_len, 8), device=device)
+
+        def views(flat):
+            return [p.view(v.shape) for p, v in zip(flat[:sum(numel)].split(numel), values)]
+
+        for w, v in zip(views(self.whole_state[0]), values):
+            w.copy_(v)
+        shard_pack_gather(s, self.whole_state[0], self.whole_gather)
+        self.whole = views(self.whole_gather)                         # what body reads
+        # each rank's gradients, and their mean as an all-reduce leaves it
+        self.rank_grads = [[torch.zeros_like(w) for w in self.whole] for _ in range(self.n_d)]
+        self.whole_grads = [torch.zeros(w.shape, device=device) for w in self.whole]
+        self.whole_list = make_tensors(self.whole_grads, views(self.whole_mean))
+
     def load(self, table: torch.Tensor):
         """Set the fp32 master table [rows, dim] and publish its bf16 copy."""
         flat = table.reshape(-1)
@@ -325,7 +391,8 @@ class TableRun:
             out = self.hidden
         else:
             leaf = self.hidden.detach().requires_grad_()
-            out = self.body(leaf)
+            kept = [w.detach().requires_grad_() for w in self.whole]
+            out = self.body(leaf, *kept)
         h = out.detach()
         torch.mm(h, self.table.t(), out=self.logits)
         # the gradient of the rank's mean loss over its valid tokens
@@ -339,7 +406,10 @@ class TableRun:
         if self.body is None:
             self.dhidden.copy_(dh)
         else:
-            self.dhidden.copy_(torch.autograd.grad(out, leaf, dh)[0])
+            dhidden, *dwhole = torch.autograd.grad(out, [leaf, *kept], dh)
+            self.dhidden.copy_(dhidden)
+            for g, d in zip(self.rank_grads[r] if kept else (), dwhole):
+                g.copy_(d)
         embed_grad(self.back, b.ids, self.dhidden, self.grad_table(r), self.embed_ws,
                    accumulate=True)
 
@@ -351,11 +421,31 @@ class TableRun:
                     for r in range(self.n_d)]
             shard_grad_reduce(s, spec, ptrs, self.mean[k], self.reduce_ws, self.sqnorm,
                               accumulate=k > 0)
+        if self.whole:
+            self._reduce_whole(valid)
         h = adamw(lr=self.lr, weight_decay=self.weight_decay, step=t,
                   max_grad_norm=self.max_grad_norm)
         for s, mean, (w, m, v) in zip(self.shards, self.mean, self.state):
             zero_shard_step(s, h, mean_in=mean, sqnorm=self.sqnorm, master=w, exp_avg=m,
                             exp_avg_sq=v, param_out=self.gather)
+
+        if self.whole:
+            w, m, v = self.whole_state
+            # clipped already: no clip in the step
+            plain = adamw(lr=self.lr, weight_decay=self.weight_decay, step=t)
+            zero_shard_step(self.whole_shard, plain, mean_in=self.whole_mean, master=w, exp_avg=m,
+                            exp_avg_sq=v, param_out=self.whole_gather)
+
+    def _reduce_whole(self, valid):
+        """The whole parameters' mean gradients; their norm into the shards', and
+        the clipped gradients into the flat buffer of their step."""
+        total = sum(valid)
+        for k, g in enumerate(self.whole_grads):
+            g.zero_()
+            for r in range(self.n_d):
+                g.add_(self.rank_grads[r][k].float(), alpha=valid[r] / total)
+        tensors_sqnorm(self.whole_list, self.sqnorm, accumulate=True)
+        tensors_clip(self.whole_list, self.max_grad_norm, self.sqnorm)
 
     def step(self, t: int, batches):
         """One optimizer step at bias-correction step t from one batch a rank."""

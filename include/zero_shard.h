@@ -611,7 +611,7 @@ typedef struct zs_tensors {
     int64_t chunk_bytes;   /* bytes of a piece at most */
     int64_t plan_bytes;    /* of the plan */
     int32_t has_out;       /* every tensor with elements has an `out` */
-    int32_t reserved;      /* 0 */
+    uint32_t stamp;        /* of the fields above, by which a changed one is seen */
 } zs_tensors;
 
 /* Checks a list of `count` tensors and fills *t.  Host only.

@@ -1,0 +1,136 @@
+"""Host-side checks of the position-bias calls (no GPU needed): every documented
+argument error before anything is enqueued, workspace sizes, and what the
+binding holds a tensor's shape against.  Fake device addresses are used, so the
+calls run only where no GPU is visible."""
+import ctypes as C
+
+import pytest
+import torch
+
+import fsdp_sharded_optimizer_zero_amd as Z
+
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(),
+                            reason="fake-address error paths run only without a GPU")
+FAKE = 0x7F0000000000
+
+
+def relpos(**kw):
+    r = Z.make_relpos(4, 10, 20, batch=3)
+    for k, v in kw.items():
+        if k[:2] in ("in", "ou") and isinstance(v, tuple):
+            v = (C.c_int64 * 3)(*v)
+        setattr(r, k, v)
+    return r
+
+
+def bias(r, table=FAKE, scores=None, lengths=None, starts=None, out=FAKE):
+    return Z.lib().relpos_bias(None if r is None else C.byref(r), table, scores, lengths, starts,
+                               out, None)
+
+
+def grad(r, g=FAKE, lengths=None, starts=None, table=FAKE, scores=None, ws=FAKE, nbytes=None):
+    if nbytes is None:
+        nbytes = Z.zs_relpos_workspace_bytes(r)
+    return Z.lib().relpos_bias_grad(None if r is None else C.byref(r), g, lengths, starts, table,
+                                    scores, 0, ws, nbytes, None)
+
+
+FAR = Z.ZS_RELPOS_FAR
+BAD = [dict(batch=-1), dict(heads=0), dict(heads=65537), dict(queries=-1), dict(keys=-1),
+       dict(keys=FAR + 1), dict(queries=FAR + 1), dict(batch=FAR + 1), dict(table_pitch=3),
+       dict(in_pitch=(800, 200, 19)), dict(in_pitch=(800, 19, 20)), dict(out_pitch=(19, 200, 20)),
+       dict(out_pitch=(1 << 60, 200, 20)), dict(query_start=FAR + 1), dict(query_start=-FAR - 1),
+       dict(bidirectional=2), dict(causal=-1), dict(buckets=3), dict(buckets=257),
+       dict(buckets=1, bidirectional=0), dict(max_distance=8), dict(max_distance=FAR + 1),
+       dict(max_distance=16, bidirectional=0), dict(dtype=2), dict(table_dtype=-1),
+       dict(id_dtype=2), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=1e39),
+       dict(batch=FAR, queries=FAR, keys=FAR)]
+
+
+@no_gpu
+@pytest.mark.parametrize("bad", BAD)
+def test_struct_is_refused(bad):
+    r = relpos(**bad)
+    assert bias(r) == Z.ZS_EINVAL_RELPOS
+    assert grad(r, nbytes=1 << 60) == Z.ZS_EINVAL_RELPOS
+    assert Z.zs_relpos_workspace_bytes(r) == 0
+
+
+@no_gpu
+def test_pointers_are_refused():
+    r = relpos()
+    assert bias(None) == Z.ZS_ENULL and grad(None, nbytes=0) == Z.ZS_ENULL
+    assert Z.lib().zs_relpos_workspace_bytes(None) == 0
+    for name in ("table", "out"):
+        assert bias(r, **{name: None}) == Z.ZS_ENULL
+    for name in ("g", "table", "ws"):
+        assert grad(r, **{name: None}) == Z.ZS_ENULL
+    for name, off in (("table", 2), ("scores", 1), ("lengths", 4), ("starts", 4), ("out", 1)):
+        assert bias(r, **{name: FAKE + off}) == Z.ZS_EALIGN, name
+    for name, off in (("g", 1), ("lengths", 4), ("starts", 4), ("table", 2), ("scores", 1),
+                      ("ws", 8)):
+        assert grad(r, **{name: FAKE + off}) == Z.ZS_EALIGN, name
+    assert grad(r, nbytes=Z.zs_relpos_workspace_bytes(r) - 1) == Z.ZS_EWORKSPACE
+    # in place only at the same pitches
+    other = relpos(out_pitch=(800, 200, 24))
+    assert bias(other, scores=FAKE) == Z.ZS_EINVAL_RELPOS
+    assert grad(other, scores=FAKE) == Z.ZS_EINVAL_RELPOS
+    assert "zs_relpos" in Z.zs_strerror(Z.ZS_EINVAL_RELPOS)
+
+
+@no_gpu
+@pytest.mark.parametrize("empty", [dict(batch=0), dict(queries=0), dict(keys=0)])
+def test_no_places_is_no_launch(empty):
+    assert bias(relpos(**empty), table=None, out=None) == Z.ZS_OK
+
+
+@pytest.mark.parametrize("dtype", [Z.ZS_BF16, Z.ZS_F32])
+@pytest.mark.parametrize("batch,heads,queries,keys", [(1, 1, 1, 1), (0, 3, 5, 5), (2, 8, 300, 300),
+                                                      (64, 16, 1, 100000), (1, 48, 4096, 4096),
+                                                      (8, 16, 2048, 2048), (1, 1, 100000, 3)])
+def test_workspace_is_small(batch, heads, queries, keys, dtype):
+    """A row of buckets (fp32) for each tile of at least N rows and 8 N columns,
+    and as many columns as 64 N where there are so many keys."""
+    r = Z.make_relpos(heads, queries, keys, batch=batch, dtype=dtype)
+    width = 8 if dtype == Z.ZS_BF16 else 4
+    columns = min(64 * width, max(8 * width, keys))
+    tiles = batch * heads * (queries // width + 1) * (keys // columns + 1)
+    n = Z.zs_relpos_workspace_bytes(r)
+    assert n % 256 == 0 and 256 <= n <= 256 + 32 * 4 * tiles
+
+
+# ---- the binding ------------------------------------------------------------------------
+
+def places(t, **kw):
+    r = Z.make_relpos(4, 10, 20, batch=3, dtype=Z.ZS_F32, **kw)
+    return Z._places_ptr(r, t, "scores", r.in_pitch)
+
+
+def test_binding_holds_shapes():
+    full = torch.zeros((3, 4, 10, 20))
+    wide = torch.zeros((3, 4, 10, 24))
+    by_query = torch.zeros((3, 10, 4, 20))
+    accepted = [(full, {}), (full.reshape(-1), {}), (torch.zeros(5000), {}),
+                (wide[..., :20], dict(in_pitch=(960, 240, 24))),
+                (by_query.transpose(1, 2), dict(in_pitch=(800, 20, 80)))]
+    for t, kw in accepted:
+        with pytest.raises(ValueError, match="GPU tensor is required"):
+            places(t, **kw)
+    refused = [(wide[..., :20], {}), (by_query.transpose(1, 2), {}), (wide, {}),
+               (full, dict(in_pitch=(960, 240, 24))), (torch.zeros((12, 10, 20)), {}),
+               (torch.zeros((4, 3, 10, 20)), {}), (torch.zeros((3, 4, 20, 10)).mT, {}),
+               (torch.zeros((3, 4, 10, 40))[..., ::2], dict(in_pitch=(1600, 400, 40)))]
+    for t, kw in refused:
+        with pytest.raises(ValueError, match="the call needs"):
+            places(t, **kw)
+    with pytest.raises(ValueError, match="2399 elements"):
+        places(torch.zeros(2399))
+    with pytest.raises(ValueError, match="dtype"):
+        places(full.to(torch.bfloat16))
+    r = Z.make_relpos(4, 10, 20, dtype=Z.ZS_F32)
+    with pytest.raises(ValueError, match="GPU tensor is required"):
+        Z._places_ptr(r, torch.zeros((4, 10, 20)), "scores", r.in_pitch)
+    with pytest.raises(ValueError, match="apart|elements"):
+        Z._relpos_table(r, torch.zeros((31, 4)), "table")
+    with pytest.raises(ValueError, match="apart|elements"):
+        Z._relpos_table(r, torch.zeros((32, 5)), "table")
