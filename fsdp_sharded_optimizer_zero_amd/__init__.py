@@ -109,9 +109,9 @@ class zs_tensor(C.Structure):
 
 
 class zs_tensors(C.Structure):
-    _fields_ = [("count", C.c_int64), ("elements", C.c_int64), ("chunks", C.c_int64),
-                ("chunk_bytes", C.c_int64), ("plan_bytes", C.c_int64), ("has_out", C.c_int32),
-                ("stamp", C.c_uint32)]
+    _fields_ = [("count", C.c_int64), ("elements", C.c_int64), ("bytes", C.c_int64),
+                ("chunks", C.c_int64), ("chunk_bytes", C.c_int64), ("plan_bytes", C.c_int64),
+                ("has_out", C.c_int32), ("stamp", C.c_uint32)]
 
 
 class zs_relpos(C.Structure):

@@ -537,6 +537,8 @@ int tensors_args(const zs_tensors* t, void* plan, TensorsArgs* a)
     a->partials = reinterpret_cast<double*>(base + w.partials);
     a->count = t->count;
     a->chunks = t->chunks;
+    a->chunk_bytes = t->chunk_bytes;
+    a->bytes = t->bytes;
     return ZS_OK;
 }
 
@@ -560,6 +562,9 @@ int set_clip(const zs_tensors* t, double max_norm, const double* sqnorm, double 
     a->sqnorm = sqnorm;
     a->other = other_sqnorm;
     a->max_norm = max_norm;
+    // sqrt(Q) + 1e-6 <= max_norm, with room for the roundings on both sides
+    const double most = max_norm - 1e-6;
+    a->quiet = t->has_out == 2 && most > 0.0 ? most * most * (1.0 - 1e-9) : -1.0;
     return ZS_OK;
 }
 
@@ -595,6 +600,7 @@ extern "C" int tensors_clip_norm(const zs_tensors* t, void* plan, double max_nor
     if (rc != ZS_OK) return rc;
     if ((rc = set_sqnorm(sqnorm_out, tensor_sqnorms, accumulate, &a)) != ZS_OK) return rc;
     if ((rc = set_clip(t, max_norm, sqnorm_out, 0.0, &a)) != ZS_OK) return rc;
+    a.clip = 1;
     if ((rc = enqueue_tensors_sqnorm(a, stream)) != ZS_OK) return rc;
     return enqueue_tensors_clip(a, stream);
 }

@@ -170,6 +170,13 @@ int check_tensor(const zs_tensor& t)
     return ZS_OK;
 }
 
+// Bytes an element has in the wider of a tensor's types, by which pieces are
+// measured.
+int64_t wide_size(const zs_tensor& t)
+{
+    return t.in_dtype == ZS_F32 || (t.out && t.out_dtype == ZS_F32) ? 4 : 2;
+}
+
 // A tensor as it is cut: its rows are one where nothing lies between them, and
 // a piece has `take` elements of one row, or `take` whole rows.
 struct Cut {
@@ -184,7 +191,7 @@ Cut cut_tensor(const zs_tensor& t, int64_t chunk_bytes)
         c.cols *= c.rows;
         c.rows = 1;
     }
-    const int64_t elems = chunk_bytes / elem_size(t.in_dtype);
+    const int64_t elems = chunk_bytes * (t.in == t.out ? kTensorPlace : 1) / wide_size(t);
     c.whole_rows = c.rows > 1 && c.cols <= elems;
     c.take = c.whole_rows ? elems / c.cols : elems;
     c.pieces = c.whole_rows ? (c.rows + c.take - 1) / c.take
@@ -455,6 +462,7 @@ int zs_tensors_layout(const zs_tensor* list, int64_t count, zs_tensors* t)
     if (count > ZS_TENSORS_MAX) return ZS_EUNSUPPORTED;
     zs_tensors r{};
     r.count = count;
+    bool place = true;
     r.has_out = 1;
     int64_t bytes = 0;
     for (int64_t i = 0; i < count; ++i) {
@@ -463,18 +471,21 @@ int zs_tensors_layout(const zs_tensor* list, int64_t count, zs_tensors* t)
         const int64_t n = list[i].rows * list[i].cols;
         if (n == 0) continue;
         r.elements += n;
-        bytes += n * zs::elem_size(list[i].in_dtype);
+        const bool here = list[i].in == list[i].out;
+        bytes += n * zs::wide_size(list[i]) / (here ? zs::kTensorPlace : 1);
+        r.bytes += n * zs::elem_size(list[i].in_dtype);
+        place = place && here;
         // (each is at most 2^62: the sum is looked at before it can overflow)
         if (bytes > (int64_t(1) << 60)) return ZS_EINVAL_TENSORS;
         if (!list[i].out) r.has_out = 0;
     }
-    // 32 KB a piece; fewer bytes where that makes too few pieces to fill the
-    // GPU, more (a multiple) where one block would have too many to join
-    r.chunk_bytes = zs::kTensorChunk;
-    while (r.chunk_bytes > zs::kTensorChunkMin && bytes / r.chunk_bytes < zs::kTensorChunksMin)
-        r.chunk_bytes /= 2;
+    if (r.has_out && place) r.has_out = 2;
+    // as many pieces as fill the GPU, and no more than one block can join
+    r.chunk_bytes = zs::kTensorChunkMin;
+    while (r.chunk_bytes < 4 * zs::kTensorPart && bytes / r.chunk_bytes > zs::kTensorChunksMin)
+        r.chunk_bytes *= 2;
     if (bytes / r.chunk_bytes > zs::kTensorChunks) {
-        r.chunk_bytes = zs::round_up(bytes / zs::kTensorChunks, zs::kTensorChunk);
+        r.chunk_bytes = zs::round_up(bytes / zs::kTensorChunks, zs::kTensorPart);
         if (r.chunk_bytes > zs::kTensorChunkMax) r.chunk_bytes = zs::kTensorChunkMax;
     }
     for (int64_t i = 0; i < count; ++i)
@@ -512,7 +523,8 @@ int zs_tensors_plan(const zs_tensor* list, const zs_tensors* t, void* plan, size
             k.rows = static_cast<int32_t>(rows);
             k.cols = static_cast<int32_t>(cols);
             k.kind = (x.in_dtype == ZS_F32 ? zs::kChunkInF32 : 0) |
-                     (x.out_dtype == ZS_F32 ? zs::kChunkOutF32 : 0);
+                     (x.out_dtype == ZS_F32 ? zs::kChunkOutF32 : 0) |
+                     (x.in == x.out ? zs::kChunkPlace : 0);
             k.tensor = static_cast<int32_t>(i);
             std::memcpy(at, &k, sizeof k);
             at += sizeof k;

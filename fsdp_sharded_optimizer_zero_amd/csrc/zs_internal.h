@@ -279,22 +279,30 @@ struct TensorChunk {
     uint64_t in, out;
     int64_t in_pitch, out_pitch;
     int32_t rows, cols;
-    int32_t kind;           // kChunkInF32 | kChunkOutF32
+    int32_t kind;           // kChunkInF32 | kChunkOutF32 | kChunkPlace
     int32_t tensor;
 };
 static_assert(sizeof(TensorChunk) == 48, "the plan's layout");
-constexpr int32_t kChunkInF32 = 1, kChunkOutF32 = 2;
+constexpr int32_t kChunkInF32 = 1, kChunkOutF32 = 2, kChunkPlace = 4;
 
+// Pieces are measured in bytes of the wider of a tensor's types, in place in
+// half of them, so that a block of the clip has the same share of every piece.
 constexpr int kTensorThreads = 256;
-// A block has 32 KB of its piece under way: 8 16-byte vectors a thread.
-constexpr int64_t kTensorChunk = int64_t(kTensorThreads) * 8 * 16;
-constexpr int64_t kTensorChunkMin = int64_t(kTensorThreads) * 16;
-constexpr int64_t kTensorChunkMax = int64_t(1) << 30;   // elements fit 32 bits
-// Pieces a list of few large tensors is cut into, at most and at least.
-constexpr int64_t kTensorChunks = 8192;
+constexpr int32_t kTensorPlace = 2;
+constexpr int64_t kTensorPart = int64_t(kTensorThreads) * 32;
+constexpr int64_t kTensorChunkMin = kTensorPart / 2;
+constexpr int64_t kTensorChunkMax = int64_t(1) << 28;   // elements fit 32 bits
+// Pieces a list of few tensors is cut into, at least (as long as they are more
+// than kTensorChunkMin) and at most.
 constexpr int64_t kTensorChunksMin = 1024;
+constexpr int64_t kTensorChunks = 4096;
 // Up to here one launch makes the norm: the last block joins the partials.
-constexpr int64_t kTensorOneLaunch = 256;
+constexpr int64_t kTensorOneLaunch = 64;
+// The norm's loads bypass the caches' reuse from here on: where a clip follows
+// in the same call, what does not fit the 256 MB Infinity Cache (512 MB: 337 us
+// and 347; 384: 254 and 247), else what is larger than it pays (192 MB: 34.2 us
+// and 38.4; 128: 24.5 and 24.7).
+constexpr int64_t kTensorNt = int64_t(160) << 20, kTensorNtClip = int64_t(448) << 20;
 
 // The plan, in bytes from its start.
 struct TensorsSpace {
@@ -312,11 +320,15 @@ struct TensorsArgs {
     double* partials;
     uint32_t* arrived;
     int64_t count, chunks;
+    int64_t chunk_bytes;            // of a piece at most, as pieces are measured
+    int64_t bytes;                  // of the list (fp32: 4 an element)
+    int32_t clip;                   // the clip follows in the same call
     double* sqnorm_out;
     double* each;
     int32_t accumulate;
     const double* sqnorm;
     double other, max_norm;
+    double quiet;           // all in place: up to this Q the coefficient is 1 (else < 0)
 };
 int enqueue_tensors_sqnorm(const TensorsArgs& a, void* stream);
 int enqueue_tensors_clip(const TensorsArgs& a, void* stream);

@@ -607,10 +607,12 @@ typedef struct zs_tensor {
 typedef struct zs_tensors {
     int64_t count;         /* tensors */
     int64_t elements;      /* in all of them */
-    int64_t chunks;        /* pieces the list is cut into: one block each */
-    int64_t chunk_bytes;   /* bytes of a piece at most */
+    int64_t bytes;         /* of all `in` */
+    int64_t chunks;        /* pieces the list is cut into */
+    int64_t chunk_bytes;   /* of a piece at most, in its wider type (in place: half) */
     int64_t plan_bytes;    /* of the plan */
-    int32_t has_out;       /* every tensor with elements has an `out` */
+    int32_t has_out;       /* 1: every tensor with elements has an `out`; 2: and it is
+                              the tensor itself */
     uint32_t stamp;        /* of the fields above, by which a changed one is seen */
 } zs_tensors;
 
@@ -629,8 +631,8 @@ int zs_tensors_layout(const zs_tensor* list, int64_t count, zs_tensors* t);
 int zs_tensors_plan(const zs_tensor* list, const zs_tensors* t, void* plan, size_t plan_bytes);
 
 /* The squared L2 norm of the whole list: the sum of (double)x^2 over every
- * element of every tensor, in fp64 in an order fixed by the list's sizes
- * (run-to-run deterministic).
+ * element of every tensor, in fp64 in an order fixed by the list's sizes and
+ * types and by which tensors are clipped in place (run-to-run deterministic).
  *   plan            device, t->plan_bytes bytes as zs_tensors_plan filled them.
  *   sqnorm_out      device, one double; accumulate != 0 adds to it (to a
  *                   shard's squared norm, or another list's).

@@ -52,6 +52,7 @@ LISTS = [
     [entry(rows=7, cols=771, in_pitch=771, out_pitch=800, in_dtype=Z.ZS_F32)],
     [entry(rows=3, cols=50000, in_pitch=60000, out_pitch=50001)],
     [entry(rows=1000, cols=3, in_pitch=4, in_dtype=Z.ZS_F32, out_dtype=Z.ZS_BF16)],
+    [entry(cols=100000, out=FAKE, out_dtype=Z.ZS_BF16), entry(cols=5000)],
     [entry(cols=1 << 31), entry(cols=(1 << 33) + 5, in_dtype=Z.ZS_F32)],
     [entry(rows=1 << 20, cols=1 << 12, in_pitch=1 << 13)],
     [entry(cols=1 + 37 * i % 500) for i in range(9000)],
@@ -62,15 +63,19 @@ LISTS = [
 def test_pieces_cover_every_element_once(entries):
     t, pieces, first = plan(entries)
     assert t.count == len(entries) and t.chunks == len(pieces) == first[-1]
-    assert t.elements == sum(e.rows * e.cols for e in entries) and t.has_out == 1
+    assert t.elements == sum(e.rows * e.cols for e in entries) and t.has_out == (
+        2 if all(e.in_ == e.out or e.rows * e.cols == 0 for e in entries) else 1)
+    assert t.bytes == sum(e.rows * e.cols * SIZE[e.in_dtype] for e in entries)
     for i, e in enumerate(entries):
         mine = pieces[first[i]:first[i + 1]]
         assert (mine["tensor"] == i).all()
         isz, osz = SIZE[e.in_dtype], SIZE[e.out_dtype]
-        assert (mine["kind"] == (e.in_dtype == Z.ZS_F32) + 2 * (e.out_dtype == Z.ZS_F32)).all()
+        assert (mine["kind"] == (e.in_dtype == Z.ZS_F32) + 2 * (e.out_dtype == Z.ZS_F32)
+                + 4 * (e.in_ == e.out)).all()
         n = mine["rows"].astype(np.int64) * mine["cols"]
         assert n.sum() == e.rows * e.cols and (n > 0).all()
-        assert (n * isz <= max(t.chunk_bytes, 4096)).all()
+        wide = max(isz, osz) if e.out else isz
+        assert (n * wide <= t.chunk_bytes * (2 if e.in_ == e.out else 1)).all()
         if e.rows * e.cols == 0:
             continue
         # pieces follow one another without a gap or an overlap, in both buffers
