@@ -671,6 +671,10 @@ def _places_ptr(r: zs_relpos, t, what: str, pitch):
     if t is None or isinstance(t, int):
         return t
     sizes = (r.batch, r.heads, r.queries, r.keys)
+    if getattr(t, "shape", None) == sizes and t.stride() == (*pitch, 1):
+        # the usual tensor: what _ptr checks beside its extent
+        if t.is_cuda and _dtype_name(t.dtype) in _ELEM.get(r.dtype, ()):
+            return t.data_ptr()
     need = 0
     if min(sizes) > 0:
         need = r.keys + sum((n - 1) * p for n, p in zip(sizes, pitch))

@@ -306,15 +306,17 @@ void relpos_bias_shape(RelposArgs* a)
 {
     const int64_t n = a->f32 ? 4 : 8;
     a->lane_shift = 3;
-    while (a->lane_shift < 8 && (n << a->lane_shift) < a->keys + n - 1) ++a->lane_shift;
+    while (a->lane_shift < 8 && (n << a->lane_shift) < a->keys) ++a->lane_shift;
     const int64_t lanes = int64_t(1) << a->lane_shift, side = kRelposThreads / lanes;
-    a->col_tiles = a->keys > 0 ? (a->keys + n - 1 + lanes * n - 1) / (lanes * n) : 0;
     const int64_t planes = a->batch * a->heads;
-    int64_t rows = side * 16 < kRelposRows ? side * 16 : kRelposRows;
-    while (rows > side && planes * a->col_tiles * ((a->queries + rows - 1) / rows) < 2048) rows /= 2;
-    if (rows > a->queries) rows = a->queries > 0 ? a->queries : 1;
-    a->rows = static_cast<int32_t>(rows);
-    a->row_tiles = (a->queries + rows - 1) / rows;
+    a->col_tiles = (a->keys + lanes * n - 1) / (lanes * n);
+    a->lane_vectors = 1;
+    if (a->queries == 1 && planes * a->col_tiles >= kRelposManyTiles) {
+        a->lane_vectors = kRelposLaneVectors;
+        a->col_tiles = (a->col_tiles + kRelposLaneVectors - 1) / kRelposLaneVectors;
+    }
+    a->rows = static_cast<int32_t>(side * (a->queries == 1 ? 1 : kRelposLaneRows));
+    a->row_tiles = (a->queries + a->rows - 1) / a->rows;
     a->tiles = planes * a->row_tiles * a->col_tiles;
 }
 

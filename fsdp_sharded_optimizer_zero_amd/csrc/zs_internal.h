@@ -338,7 +338,10 @@ int check_tensors(const zs_tensors* t);
 // ---- the position-bias table (zs_relpos.hip) ---------------------------------------
 
 constexpr int kRelposThreads = 256;
-constexpr int kRelposRows = 128;            // of a tile, at most
+constexpr int kRelposRows = 128;            // of a gradient's tile, at most
+constexpr int kRelposLaneRows = 4;          // of the bias a lane has, and for one
+constexpr int kRelposLaneVectors = 4;       // query vectors, from so many tiles on
+constexpr int64_t kRelposManyTiles = 2048;
 constexpr int kRelposMaxBuckets = ZS_RELPOS_MAX_BUCKETS;
 constexpr int kRelposMaxEdges = kRelposMaxBuckets / 2;
 constexpr int64_t kRelposFar = ZS_RELPOS_FAR;
@@ -356,6 +359,7 @@ struct RelposArgs {
     int64_t start;
     int64_t row_tiles, col_tiles, tiles;
     int32_t lane_shift;     // log2 of the lanes along the keys
+    int32_t lane_vectors;   // of the bias a lane has along the keys
     int32_t rows;           // of a tile (gradient: of a group of lanes)
     int32_t buckets, two_sided, causal;
     int32_t half, exact;    // buckets of a side; those of single distances

@@ -31,6 +31,7 @@ constexpr int kSumThreads = 1024;
 __device__ __forceinline__ int side_bucket(const RelposArgs& a, const int32_t* edges, int n)
 {
     if (n < a.exact) return n;
+    if (a.edge_count == 0 || n >= edges[a.edge_count - 1]) return a.exact + a.edge_count;
     int at = 0;
     for (int half = a.edge_span; half > 0; half >>= 1)
         if (at + half <= a.edge_count && edges[at + half - 1] <= n) at += half;
@@ -85,69 +86,153 @@ __device__ __forceinline__ int64_t row_limit(const RelposArgs& a, const Sequence
 
 // ---- bias -------------------------------------------------------------------------
 
-// A block: `a.lanes` lanes along the keys, N a lane, and kThreads / lanes rows
-// at a time, a.rows in all.  A row's vectors begin at its own 16-byte boundary.
-template <typename T, typename TT, int N, bool SCORES>
+// Block b of n in an order in which each of the 8 XCDs, to which consecutive
+// blocks are dealt in turn, has one stretch of the work: neighbours that share
+// a cache line are then in one L2.
+__device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t n)
+{
+    const int64_t per = n / 8;
+    return b < per * 8 ? (b & 7) * per + (b >> 3) : b;
+}
+
+constexpr int kFewEdges = 16;
+// The buckets of W diagonals d0, d0 + 1, ...: for few edges by looking at all
+// of them (scalars), else by search in LDS.
+template <int W>
+__device__ __forceinline__ void buckets_of(const RelposArgs& a, const int32_t* edges, int d0, int u[W])
+{
+    if (a.edge_count > kFewEdges) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) u[k] = bucket_of(a, edges, d0 + k);
+        return;
+    }
+    int n[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        const int d = d0 + k;
+        n[k] = d < 0 ? -d : (a.two_sided ? d : 0);
+        u[k] = n[k] < a.exact ? n[k] : a.exact;
+    }
+    for (int e = 0; e < a.edge_count; ++e) {
+        const int edge = a.edges[e];
+#pragma unroll
+        for (int k = 0; k < W; ++k) u[k] += n[k] >= edge ? 1 : 0;
+    }
+    if (a.two_sided) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) u[k] += d0 + k > 0 ? a.half : 0;
+    }
+}
+
+// One block a tile of `lanes` lanes along the keys and kThreads / lanes groups of R
+// rows.  A lane holds N + R - 1 diagonals in registers for R rows of N keys, from
+// one read of the table where they are all in a far bucket, which most are; it
+// stores R times and ends.  32 heads of 4096 x 4096 bf16 in 174 us, 6.2 TB/s (a
+// bare fill in this pattern 166, in one row a block 153; two rows a lane 199, eight
+// 184; diagonals built once in LDS for 16 rows and more 202-260).  Blocks in the
+// order of xcd_order, by which also rows that begin anywhere cost nothing (a fill
+// 2 bytes off 153 us, 211 in the plain order).
+// V > 1, for one query: vectors a tile's lanes apart (64 x 16 x 1 x 8192 onto
+// scores: 12 us, one vector a lane 13; but 32 x 4099 alone 5.2 us and 4.4).
+template <typename T, typename TT, int N, bool SCORES, int R, int V>
 __global__ void __launch_bounds__(kThreads) k_relpos_bias(RelposArgs a, int64_t b0)
 {
-    __shared__ float column[kRelposMaxBuckets];
     __shared__ int32_t edges[kRelposMaxEdges];
-    __shared__ float diag[kThreads * N + kRelposRows + 2 * N];
-    int64_t blk = b0 + blockIdx.x;
-    const int64_t ct = blk % a.col_tiles;
-    blk /= a.col_tiles;
-    const int64_t rt = blk % a.row_tiles;
-    blk /= a.row_tiles;
-    const int64_t h = blk % a.heads, b = blk / a.heads;
-    const Sequence s = sequence(a, b);
-    const int lanes = 1 << a.lane_shift;
-    const int64_t i0 = rt * a.rows, c0 = ct * (static_cast<int64_t>(lanes) * N);
-    const int rows = a.queries - i0 < a.rows ? static_cast<int>(a.queries - i0) : a.rows;
+    int64_t ct, rt, h, b;
+    const int64_t blk = xcd_order(b0 + blockIdx.x, a.tiles);
+    if (a.tiles <= INT32_MAX) {
+        const uint32_t x = static_cast<uint32_t>(blk), cts = static_cast<uint32_t>(a.col_tiles),
+                       rts = static_cast<uint32_t>(a.row_tiles),
+                       hs = static_cast<uint32_t>(a.heads);
+        const uint32_t y = x / cts, z = y / rts, w = z / hs;
+        ct = x - y * cts;
+        rt = y - z * rts;
+        h = z - w * hs;
+        b = w;
+    } else {
+        const int64_t y = blk / a.col_tiles, z = y / a.row_tiles;
+        ct = blk % a.col_tiles;
+        rt = y % a.row_tiles;
+        h = z % a.heads;
+        b = z / a.heads;
+    }
     const TT* table = static_cast<const TT*>(a.table) + h;
-    for (int u = threadIdx.x; u < a.buckets; u += kThreads) column[u] = widen(table[u * a.table_pitch]);
-    for (int e = threadIdx.x; e < a.edge_count; e += kThreads) edges[e] = a.edges[e];
-    __syncthreads();
-    // diag[x]: of key c0 + c and query i0 + r at x = c - r + rows - 1 + N, for
-    // c from -N (a row's first vector) on
-    const int span = lanes * N + rows - 1 + N;
-    const int64_t d0 = c0 - i0 - s.start - (rows - 1) - N;
-    for (int x = threadIdx.x; x < span; x += kThreads)
-        diag[x] = column[bucket_of(a, edges, static_cast<int>(d0 + x))];
-    __syncthreads();
-    const int lane = threadIdx.x & (lanes - 1);
-    const T* in = static_cast<const T*>(a.in) + b * a.in_pitch[0] + h * a.in_pitch[1];
-    T* out = static_cast<T*>(a.out) + b * a.out_pitch[0] + h * a.out_pitch[1];
-    for (int r = threadIdx.x >> a.lane_shift; r < rows; r += kThreads >> a.lane_shift) {
-        const int64_t i = i0 + r;
-        T* o = out + i * a.out_pitch[2];
-        const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(o) / sizeof(T)) % N);
-        const int c = lane * N - skew;              // column in the tile
-        const int64_t j = c0 + c;
-        if (j >= a.keys) continue;
-        const int64_t limit = row_limit(a, s, i);
-        const float* w = diag + c - r + rows - 1 + N;
-        const T* p = in + i * a.in_pitch[2];
-        if (j >= 0 && j + N <= a.keys) {
-            float x[N], v[N];
-            if constexpr (SCORES) {
-                if (j < limit) load_n<N>(p + j, x);
+    if (a.edge_count > kFewEdges) {
+        for (int e = threadIdx.x; e < a.edge_count; e += kThreads) edges[e] = a.edges[e];
+        __syncthreads();
+    }
+    const Sequence s = sequence(a, b);
+    const int lane = threadIdx.x & ((1 << a.lane_shift) - 1);
+    const int step = N << a.lane_shift;             // keys of a tile's V-th part
+    const int keys = static_cast<int>(a.keys);
+    const int j0 = static_cast<int>(ct) * (step * V) + lane * N;
+    const int64_t i0 = rt * a.rows + (threadIdx.x >> a.lane_shift) * R;
+    const int rows = a.queries - i0 < R ? static_cast<int>(a.queries - i0) : R;
+    if (j0 >= keys || rows <= 0) return;
+    const T* in = static_cast<const T*>(a.in) + b * a.in_pitch[0] + h * a.in_pitch[1] + i0 * a.in_pitch[2];
+    T* out = static_cast<T*>(a.out) + b * a.out_pitch[0] + h * a.out_pitch[1] + i0 * a.out_pitch[2];
+    int limit[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) limit[r] = static_cast<int>(row_limit(a, s, i0 + r));
+    float x[V][R][N];
+    if constexpr (SCORES) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int j = j0 + v * step;
+                if (r >= rows) continue;
+                const T* p = in + r * a.in_pitch[2] + j;
+                if (j + N <= limit[r]) {
+                    load_n<N>(p, x[v][r]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < N; ++k)
+                        x[v][r][k] = j + k < limit[r] ? widen(p[k]) : 0.0f;
+                }
             }
+    }
+    const int far = a.edge_count > 0 ? a.edges[a.edge_count - 1] : a.exact;
+    constexpr int W = N + R - 1;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int j = j0 + v * step;
+        if (j >= keys) continue;
+        // w[k - r + R - 1]: the bias of place (i0 + r, j + k)
+        float w[W];
+        const int d0 = static_cast<int>(j - i0 - s.start) - (R - 1);
+        // far away on one side, or all behind a one-sided query: one bucket
+        if (d0 + W - 1 <= -far || (a.two_sided ? d0 >= far : d0 >= 0)) {
+            const int u = d0 < 0 ? a.half - 1 : a.two_sided ? 2 * a.half - 1 : 0;
+            const float q = widen(table[u * a.table_pitch]);
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[k] = q;
+        } else {
+            int u[W];
+            buckets_of<W>(a, edges, d0, u);
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[k] = widen(table[u[k] * a.table_pitch]);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (r >= rows) continue;
+            T* o = out + r * a.out_pitch[2] + j;
+            float q[N];
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-                v[k] = w[k];
-                if constexpr (SCORES) v[k] = __builtin_fmaf(a.scale, x[k], v[k]);
-                if (j + k >= limit) v[k] = -INFINITY;
+                q[k] = w[k - r + R - 1];
+                if constexpr (SCORES) q[k] = __builtin_fmaf(a.scale, x[v][r][k], q[k]);
             }
-            store_n<N>(o + j, v);
-        } else {
-            for (int k = 0; k < N; ++k) {
-                if (j + k < 0 || j + k >= a.keys) continue;
-                float v = -INFINITY;
-                if (j + k < limit) {
-                    v = w[k];
-                    if constexpr (SCORES) v = __builtin_fmaf(a.scale, widen(p[j + k]), v);
-                }
-                put(o + j + k, v);
+            if (j + N > limit[r]) {
+#pragma unroll
+                for (int k = 0; k < N; ++k) q[k] = j + k < limit[r] ? q[k] : -INFINITY;
+            }
+            if (j + N <= keys) {
+                store_n<N>(o, q);
+            } else {
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    if (j + k < keys) put(o + k, q[k]);
             }
         }
     }
@@ -340,13 +425,21 @@ __global__ void __launch_bounds__(kSumThreads) k_relpos_sum(RelposArgs a)
     }
 }
 
+template <typename T, typename TT, int N, bool SCORES>
+void bias_launch(const RelposArgs& a, int64_t b0, uint32_t n, hipStream_t st)
+{
+    if (a.lane_vectors > 1)
+        k_relpos_bias<T, TT, N, SCORES, 1, kRelposLaneVectors><<<n, kThreads, 0, st>>>(a, b0);
+    else if (a.queries == 1)
+        k_relpos_bias<T, TT, N, SCORES, 1, 1><<<n, kThreads, 0, st>>>(a, b0);
+    else
+        k_relpos_bias<T, TT, N, SCORES, kRelposLaneRows, 1><<<n, kThreads, 0, st>>>(a, b0);
+}
 template <typename T, typename TT, int N>
 void bias_launch(const RelposArgs& a, int64_t b0, uint32_t n, hipStream_t st)
 {
-    if (a.in)
-        k_relpos_bias<T, TT, N, true><<<n, kThreads, 0, st>>>(a, b0);
-    else
-        k_relpos_bias<T, TT, N, false><<<n, kThreads, 0, st>>>(a, b0);
+    if (a.in) bias_launch<T, TT, N, true>(a, b0, n, st);
+    else bias_launch<T, TT, N, false>(a, b0, n, st);
 }
 
 }  // namespace
