@@ -494,7 +494,7 @@ extern "C" int relpos_bias(const zs_relpos* r, const void* table, const void* sc
     if (!table || !out) return ZS_ENULL;
     if (!aligned_to(table, elem_bytes(r->table_dtype))) return ZS_EALIGN;
     a.table = table;
-    relpos_bias_shape(&a);
+    if (!relpos_bias_shape(&a)) return ZS_EUNSUPPORTED;
     return enqueue_relpos_bias(a, stream);
 }
 
@@ -509,7 +509,7 @@ extern "C" int relpos_bias_grad(const zs_relpos* r, const void* grad, const void
     if (!grad_table || !workspace || (!grad && !relpos_empty(r))) return ZS_ENULL;
     if (!aligned16(workspace) || !aligned_to(grad_table, elem_bytes(r->table_dtype)))
         return ZS_EALIGN;
-    relpos_grad_shape(&a);
+    if (!relpos_grad_shape(&a)) return ZS_EUNSUPPORTED;
     if (workspace_bytes < static_cast<size_t>(relpos_parts_bytes(a))) return ZS_EWORKSPACE;
     a.table_grad = grad_table;
     a.parts = static_cast<float*>(workspace);

@@ -302,12 +302,23 @@ void relpos_buckets(const zs_relpos* r, RelposArgs* a)
     }
 }
 
-void relpos_bias_shape(RelposArgs* a)
+namespace {
+
+constexpr int64_t kRelposWaves = kRelposThreads / 64;
+
+bool past_caches(const RelposArgs& a)
+{
+    return a.batch * a.heads * a.queries * a.keys * (a.f32 ? 4 : 2) >= kRelposNt;
+}
+
+}  // namespace
+
+bool relpos_bias_shape(RelposArgs* a)
 {
     const int64_t n = a->f32 ? 4 : 8;
     a->lane_shift = 3;
-    while (a->lane_shift < 8 && (n << a->lane_shift) < a->keys) ++a->lane_shift;
-    const int64_t lanes = int64_t(1) << a->lane_shift, side = kRelposThreads / lanes;
+    while (a->lane_shift < 6 && (n << a->lane_shift) < a->keys) ++a->lane_shift;
+    const int64_t lanes = int64_t(1) << a->lane_shift, groups = 64 / lanes;
     const int64_t planes = a->batch * a->heads;
     a->col_tiles = (a->keys + lanes * n - 1) / (lanes * n);
     a->lane_vectors = 1;
@@ -315,12 +326,15 @@ void relpos_bias_shape(RelposArgs* a)
         a->lane_vectors = kRelposLaneVectors;
         a->col_tiles = (a->col_tiles + kRelposLaneVectors - 1) / kRelposLaneVectors;
     }
-    a->rows = static_cast<int32_t>(side * (a->queries == 1 ? 1 : kRelposLaneRows));
+    a->rows = static_cast<int32_t>(groups * (a->queries == 1 ? 1 : kRelposLaneRows));
     a->row_tiles = (a->queries + a->rows - 1) / a->rows;
     a->tiles = planes * a->row_tiles * a->col_tiles;
+    a->blocks = (a->tiles + kRelposWaves - 1) / kRelposWaves;
+    a->nt = past_caches(*a);
+    return a->blocks <= INT32_MAX / kRelposWaves;
 }
 
-void relpos_grad_shape(RelposArgs* a)
+bool relpos_grad_shape(RelposArgs* a)
 {
     const int64_t n = a->f32 ? 4 : 8;
     a->lane_shift = 3;
@@ -328,17 +342,22 @@ void relpos_grad_shape(RelposArgs* a)
     const int64_t lanes = int64_t(1) << a->lane_shift, groups = 64 / lanes;
     a->col_tiles = (a->keys + lanes * n - 1) / (lanes * n);
     const int64_t planes = a->batch * a->heads;
+    // a multiple of 8 rows: two batches of the kernel's
     int64_t rows = kRelposRows / groups;
-    while (rows > n && planes * a->col_tiles * ((a->queries + rows * groups - 1) / (rows * groups)) < 4096)
-        rows /= 2;
+    const auto row_tiles = [&] { return (a->queries + rows * groups - 1) / (rows * groups); };
+    while (rows > 8 && planes * a->col_tiles * row_tiles() < kRelposGradTiles) rows /= 2;
     a->rows = static_cast<int32_t>(rows);
-    a->row_tiles = (a->queries + rows * groups - 1) / (rows * groups);
-    a->tiles = planes * a->row_tiles * a->col_tiles;
+    a->row_tiles = row_tiles();
+    a->plane_blocks = (a->row_tiles * a->col_tiles + kRelposWaves - 1) / kRelposWaves;
+    a->blocks = planes * a->plane_blocks;
+    a->tiles = kRelposWaves * a->blocks;
+    a->nt = past_caches(*a);
+    return a->blocks <= INT32_MAX / kRelposWaves;
 }
 
 int64_t relpos_parts_bytes(const RelposArgs& a)
 {
-    const int64_t bytes = a.tiles * a.buckets * 4;
+    const int64_t bytes = a.blocks * a.buckets * 4;
     return round_up(bytes > 0 ? bytes : 1, 256);
 }
 
@@ -447,7 +466,7 @@ size_t zs_relpos_workspace_bytes(const zs_relpos* r)
     a.keys = r->keys;
     a.buckets = r->buckets;
     a.f32 = r->dtype == ZS_F32;
-    zs::relpos_grad_shape(&a);
+    if (!zs::relpos_grad_shape(&a)) return 0;
     return static_cast<size_t>(zs::relpos_parts_bytes(a));
 }
 

@@ -341,7 +341,14 @@ constexpr int kRelposThreads = 256;
 constexpr int kRelposRows = 128;            // of a gradient's tile, at most
 constexpr int kRelposLaneRows = 4;          // of the bias a lane has, and for one
 constexpr int kRelposLaneVectors = 4;       // query vectors, from so many tiles on
-constexpr int64_t kRelposManyTiles = 2048;
+constexpr int64_t kRelposManyTiles = 8192;
+// Waves a gradient is cut into, if its rows allow it: as many as the GPU holds
+// (8 of 4 SIMDs of 256 CUs).
+constexpr int64_t kRelposGradTiles = 8192;
+// From so many bytes of scores on, loads bypass the caches' reuse (gradient of 1.07
+// GB: 168 us and 193, 403 MB 66 and 79; bias onto 201 MB 62 and 78, 100 MB 37 and
+// 32; both scores' gradients of 100 MB 45 and 43).
+constexpr int64_t kRelposNt = int64_t(160) << 20;
 constexpr int kRelposMaxBuckets = ZS_RELPOS_MAX_BUCKETS;
 constexpr int kRelposMaxEdges = kRelposMaxBuckets / 2;
 constexpr int64_t kRelposFar = ZS_RELPOS_FAR;
@@ -353,11 +360,13 @@ struct RelposArgs {
     void* table_grad;
     const void* lengths;
     const void* starts;
-    float* parts;           // workspace: fp32[heads][batch][row tiles][col tiles][buckets]
+    float* parts;           // workspace: fp32[heads][batch][plane_blocks][buckets]
     int64_t batch, heads, queries, keys;
     int64_t in_pitch[3], out_pitch[3], table_pitch;
     int64_t start;
     int64_t row_tiles, col_tiles, tiles;
+    int64_t plane_blocks;   // gradient: blocks of one sequence and head
+    int64_t blocks;
     int32_t lane_shift;     // log2 of the lanes along the keys
     int32_t lane_vectors;   // of the bias a lane has along the keys
     int32_t rows;           // of a tile (gradient: of a group of lanes)
@@ -366,13 +375,15 @@ struct RelposArgs {
     int32_t edge_count;
     int32_t edge_span;      // largest power of two up to edge_count
     int32_t f32, table_f32, id64, accumulate;
+    int32_t nt;             // loads bypass the caches' reuse
     float scale;
     int32_t edges[kRelposMaxEdges];     // where the buckets behind `exact` begin
 };
 
-// How a call cuts its work (fills the tile fields).
-void relpos_bias_shape(RelposArgs* a);
-void relpos_grad_shape(RelposArgs* a);
+// How a call cuts its work (fills the tile fields); false where the tiles are
+// more than 31 bits number.
+bool relpos_bias_shape(RelposArgs* a);
+bool relpos_grad_shape(RelposArgs* a);
 // The bucket fields from r.
 void relpos_buckets(const zs_relpos* r, RelposArgs* a);
 int64_t relpos_parts_bytes(const RelposArgs& a);

@@ -9,6 +9,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "zs_elements.h"
 #include "zs_internal.h"
@@ -22,6 +23,7 @@ namespace {
 constexpr int64_t max_blocks(int threads) { return ZS_MAX_LAUNCH_THREADS / threads; }
 
 constexpr int kThreads = kRelposThreads;
+constexpr int kWaves = kThreads / 64;
 constexpr int kSumThreads = 1024;
 
 // ---- buckets ----------------------------------------------------------------------
@@ -45,17 +47,30 @@ __device__ __forceinline__ int bucket_of(const RelposArgs& a, const int32_t* edg
     return a.two_sided && d > 0 ? a.half + u : u;
 }
 
-// Where bucket u of one side begins, as a distance.
-__device__ __forceinline__ int side_begin(const RelposArgs& a, const int32_t* edges, int u)
+// The differences d from lo to hi that bucket u holds (none: lo > hi).
+__device__ __forceinline__ void bucket_range(const RelposArgs& a, int u, int& lo, int& hi)
 {
-    return u <= a.exact ? u : edges[u - a.exact - 1];
+    const bool behind = u >= a.half;
+    const int v = behind ? u - a.half : u;
+    constexpr int kAll = 1 << 30;
+    // distances of one side, from begin up to before end
+    const int begin = v <= a.exact ? v : a.edges[v - a.exact - 1];
+    const int end = v == a.half - 1 ? kAll : v < a.exact ? v + 1 : a.edges[v - a.exact];
+    if (behind) {
+        lo = begin > 1 ? begin : 1;
+        hi = end - 1;
+    } else {
+        lo = 1 - end;
+        hi = v == 0 && !a.two_sided ? kAll : -begin;
+    }
+    if (u >= 2 * a.half) lo = 1, hi = 0;            // the odd bucket of a two-sided table
 }
 
 // ---- what a row sees ----------------------------------------------------------------
 
 struct Sequence {
-    int64_t start;      // position of the first query
-    int64_t length;     // keys that are there
+    int start;          // position of the first query
+    int length;         // keys that are there
 };
 __device__ __forceinline__ int64_t read_int(const void* p, int id64, int64_t i)
 {
@@ -64,35 +79,172 @@ __device__ __forceinline__ int64_t read_int(const void* p, int id64, int64_t i)
 }
 __device__ __forceinline__ Sequence sequence(const RelposArgs& a, int64_t b)
 {
-    Sequence s{a.start, a.keys};
+    constexpr int kFar = static_cast<int>(kRelposFar);
+    Sequence s{static_cast<int>(a.start), static_cast<int>(a.keys)};
     if (a.starts) {
         // positions past the range a call may name are held to it
         const int64_t x = read_int(a.starts, a.id64, b);
-        s.start = x < -kRelposFar ? -kRelposFar : x > kRelposFar ? kRelposFar : x;
+        s.start = x < -kFar ? -kFar : x > kFar ? kFar : static_cast<int>(x);
     }
     if (a.lengths) {
         const int64_t x = read_int(a.lengths, a.id64, b);
-        s.length = x < 0 ? 0 : x < a.keys ? x : a.keys;
+        s.length = x < 0 ? 0 : x < s.length ? static_cast<int>(x) : s.length;
     }
     return s;
 }
 // Query i sees keys [0, limit).
-__device__ __forceinline__ int64_t row_limit(const RelposArgs& a, const Sequence& s, int64_t i)
+__device__ __forceinline__ int row_limit(const RelposArgs& a, const Sequence& s, int i)
 {
     if (!a.causal) return s.length;
-    const int64_t n = i + s.start + 1;
+    const int n = i + s.start + 1;
     return n < 0 ? 0 : n < s.length ? n : s.length;
 }
+
+// A value all lanes of the wave hold, in a scalar register.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// x = q d + r: returns q.
+__device__ __forceinline__ uint32_t div_mod(uint32_t x, int64_t d, int& r)
+{
+    const uint32_t n = static_cast<uint32_t>(d), q = x / n;
+    r = static_cast<int>(x - q * n);
+    return q;
+}
+
+// ---- a row's vectors ----------------------------------------------------------------
+
+// N elements as loaded, bf16 packed.
+template <typename T>
+struct Row;
+template <>
+struct Row<uint16_t> {
+    static constexpr int N = 8;
+    u32x4 b;
+    __device__ __forceinline__ float at(int k) const
+    {
+        return k & 1 ? bf16_hi(b[k / 2]) : bf16_lo(b[k / 2]);
+    }
+    template <bool NT>
+    __device__ __forceinline__ void load(const uint16_t* p)
+    {
+        const auto m = reinterpret_cast<const u32x4_u*>(p);
+        b = NT ? __builtin_nontemporal_load(m) : *m;
+    }
+    // its first n elements
+    __device__ __forceinline__ void part(const uint16_t* p, int n)
+    {
+        uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+        for (int k = 0; k < n; ++k) {
+            const uint64_t e = static_cast<uint64_t>(p[k]) << (16 * (k & 3));
+            lo |= k < 4 ? e : 0;
+            hi |= k < 4 ? 0 : e;
+        }
+        b = u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32),
+                  static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)};
+    }
+    // keeps the first n elements, the others 0 whatever they were
+    __device__ __forceinline__ void keep(int n)
+    {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t mask = n >= 2 * k + 2 ? 0xFFFFFFFFu : n == 2 * k + 1 ? 0xFFFFu : 0u;
+            b[k] &= mask;
+        }
+    }
+    // without its first n elements
+    __device__ __forceinline__ void drop(int n)
+    {
+        if (n & 1) b = u32x4{b[0] >> 16 | b[1] << 16, b[1] >> 16 | b[2] << 16,
+                             b[2] >> 16 | b[3] << 16, b[3] >> 16};
+        if (n & 2) b = u32x4{b[1], b[2], b[3], 0u};
+        if (n & 4) b = u32x4{b[2], b[3], 0u, 0u};
+    }
+};
+template <>
+struct Row<float> {
+    static constexpr int N = 4;
+    f32x4 b;
+    __device__ __forceinline__ float at(int k) const { return b[k]; }
+    template <bool NT>
+    __device__ __forceinline__ void load(const float* p)
+    {
+        const auto m = reinterpret_cast<const f32x4_u*>(p);
+        b = NT ? __builtin_nontemporal_load(m) : *m;
+    }
+    __device__ __forceinline__ void part(const float* p, int n)
+    {
+        b = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+        for (int k = 0; k < n; ++k) {
+            b[0] = k == 0 ? p[k] : b[0];
+            b[1] = k == 1 ? p[k] : b[1];
+            b[2] = k == 2 ? p[k] : b[2];
+            b[3] = k == 3 ? p[k] : b[3];
+        }
+    }
+    __device__ __forceinline__ void keep(int n)
+    {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) b[k] = k < n ? b[k] : 0.0f;
+    }
+    __device__ __forceinline__ void drop(int n)
+    {
+        if (n & 1) b = f32x4{b[1], b[2], b[3], 0.0f};
+        if (n & 2) b = f32x4{b[2], b[3], 0.0f, 0.0f};
+    }
+};
+
+// A lane's N places of a row of `keys`, from column j on.  Those that reach
+// past the row are loaded as the row's last N and moved down at use (element by
+// element, a wave waits for each of its rows: 48 x 1024 x 2047 bf16, the gradient
+// 79 us and 40); a row of fewer than N goes element by element.
+template <typename T>
+struct Span {
+    static constexpr int N = Row<T>::N;
+    int j, keys;
+    int at;             // where the load begins
+    int shift;          // elements of it before j
+    __device__ __forceinline__ Span(int j, int keys)
+        : j(j), keys(keys), at(j + N <= keys || keys < N ? j : keys - N), shift(j - at)
+    {
+    }
+    // row: the row's first element
+    template <bool NT>
+    __device__ __forceinline__ Row<T> load(const T* row) const
+    {
+        Row<T> x;
+        if (keys >= N) x.template load<NT>(row + at);
+        else x.part(row + j, keys - j);
+        return x;
+    }
+    __device__ __forceinline__ void align(Row<T>& x) const
+    {
+        if (shift > 0) x.drop(shift);
+    }
+    __device__ __forceinline__ void store(T* row, const float (&v)[N]) const
+    {
+        if (j + N <= keys) {
+            store_n<N>(row + j, v);
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < N - 1; ++k)
+            if (j + k < keys) put(row + j + k, v[k]);
+    }
+};
 
 // ---- bias -------------------------------------------------------------------------
 
 // Block b of n in an order in which each of the 8 XCDs, to which consecutive
-// blocks are dealt in turn, has one stretch of the work: neighbours that share
-// a cache line are then in one L2.
-__device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t n)
+// blocks are dealt in turn, has stretches of kStretch blocks: neighbours that
+// share a cache line are then mostly in one L2, and sequences of different
+// lengths still fall to all.
+constexpr uint32_t kStretch = 256;
+__device__ __forceinline__ uint32_t xcd_order(uint32_t b, int64_t n)
 {
-    const int64_t per = n / 8;
-    return b < per * 8 ? (b & 7) * per + (b >> 3) : b;
+    const uint32_t in = b % (8 * kStretch), first = b - in;
+    return first + 8 * kStretch <= n ? first + (in & 7) * kStretch + (in >> 3) : b;
 }
 
 constexpr int kFewEdges = 16;
@@ -124,83 +276,66 @@ __device__ __forceinline__ void buckets_of(const RelposArgs& a, const int32_t* e
     }
 }
 
-// One block a tile of `lanes` lanes along the keys and kThreads / lanes groups of R
-// rows.  A lane holds N + R - 1 diagonals in registers for R rows of N keys, from
-// one read of the table where they are all in a far bucket, which most are; it
-// stores R times and ends.  32 heads of 4096 x 4096 bf16 in 174 us, 6.2 TB/s (a
-// bare fill in this pattern 166, in one row a block 153; two rows a lane 199, eight
-// 184; diagonals built once in LDS for 16 rows and more 202-260).  Blocks in the
-// order of xcd_order, by which also rows that begin anywhere cost nothing (a fill
-// 2 bytes off 153 us, 211 in the plain order).
+// One wave a tile: `lanes` lanes along the keys, N keys each, and 64 / lanes groups
+// of R rows.  A lane holds N + R - 1 diagonals in registers for R rows, from one
+// read of the table where they are all in a far bucket, which most are; it
+// stores R times and ends.  Bound by HBM: 32 heads of 4096 x 4096 bf16 in 173 us,
+// 6.2 TB/s (a bare fill in this pattern 166, in one row a block 153; two rows a
+// lane 199, eight 184; diagonals built once in LDS for 16 rows and more 202-260).
+// In the plain order of blocks 187 us, and rows that begin anywhere cost more (a
+// fill 2 bytes off 211 us, in this order 153).  Waves and not blocks have tiles, so
+// that a row's last few keys cost a wave (48 x 1024 x 2051: 37 us, with tiles of
+// 256 lanes 53; 2048 keys 33).
 // V > 1, for one query: vectors a tile's lanes apart (64 x 16 x 1 x 8192 onto
 // scores: 12 us, one vector a lane 13; but 32 x 4099 alone 5.2 us and 4.4).
-template <typename T, typename TT, int N, bool SCORES, int R, int V>
+template <typename T, typename TT, bool SCORES, bool NT, int R, int V>
 __global__ void __launch_bounds__(kThreads) k_relpos_bias(RelposArgs a, int64_t b0)
 {
+    constexpr int N = Row<T>::N;
     __shared__ int32_t edges[kRelposMaxEdges];
-    int64_t ct, rt, h, b;
-    const int64_t blk = xcd_order(b0 + blockIdx.x, a.tiles);
-    if (a.tiles <= INT32_MAX) {
-        const uint32_t x = static_cast<uint32_t>(blk), cts = static_cast<uint32_t>(a.col_tiles),
-                       rts = static_cast<uint32_t>(a.row_tiles),
-                       hs = static_cast<uint32_t>(a.heads);
-        const uint32_t y = x / cts, z = y / rts, w = z / hs;
-        ct = x - y * cts;
-        rt = y - z * rts;
-        h = z - w * hs;
-        b = w;
-    } else {
-        const int64_t y = blk / a.col_tiles, z = y / a.row_tiles;
-        ct = blk % a.col_tiles;
-        rt = y % a.row_tiles;
-        h = z % a.heads;
-        b = z / a.heads;
-    }
-    const TT* table = static_cast<const TT*>(a.table) + h;
     if (a.edge_count > kFewEdges) {
         for (int e = threadIdx.x; e < a.edge_count; e += kThreads) edges[e] = a.edges[e];
         __syncthreads();
     }
+    const uint32_t block = xcd_order(static_cast<uint32_t>(b0) + blockIdx.x, a.blocks);
+    const uint32_t tile = block * kWaves + uniform(threadIdx.x >> 6);
+    if (tile >= a.tiles) return;
+    int ct, rt, h;
+    const int64_t b = div_mod(div_mod(div_mod(tile, a.col_tiles, ct), a.row_tiles, rt), a.heads, h);
+    const TT* table = static_cast<const TT*>(a.table) + h;
     const Sequence s = sequence(a, b);
-    const int lane = threadIdx.x & ((1 << a.lane_shift) - 1);
+    const int lane = threadIdx.x & 63, l = lane & ((1 << a.lane_shift) - 1);
     const int step = N << a.lane_shift;             // keys of a tile's V-th part
     const int keys = static_cast<int>(a.keys);
-    const int j0 = static_cast<int>(ct) * (step * V) + lane * N;
-    const int64_t i0 = rt * a.rows + (threadIdx.x >> a.lane_shift) * R;
-    const int rows = a.queries - i0 < R ? static_cast<int>(a.queries - i0) : R;
+    const int j0 = ct * (step * V) + l * N;
+    const int i0 = rt * a.rows + (lane >> a.lane_shift) * R;
+    const int rows = static_cast<int>(a.queries) - i0 < R ? static_cast<int>(a.queries) - i0 : R;
     if (j0 >= keys || rows <= 0) return;
     const T* in = static_cast<const T*>(a.in) + b * a.in_pitch[0] + h * a.in_pitch[1] + i0 * a.in_pitch[2];
     T* out = static_cast<T*>(a.out) + b * a.out_pitch[0] + h * a.out_pitch[1] + i0 * a.out_pitch[2];
     int limit[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) limit[r] = static_cast<int>(row_limit(a, s, i0 + r));
-    float x[V][R][N];
+    for (int r = 0; r < R; ++r) limit[r] = row_limit(a, s, i0 + r);
+    Row<T> x[V][R];
     if constexpr (SCORES) {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) {
+            const Span<T> span(j0 + v * step, keys);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int j = j0 + v * step;
-                if (r >= rows) continue;
-                const T* p = in + r * a.in_pitch[2] + j;
-                if (j + N <= limit[r]) {
-                    load_n<N>(p, x[v][r]);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < N; ++k)
-                        x[v][r][k] = j + k < limit[r] ? widen(p[k]) : 0.0f;
-                }
-            }
+            for (int r = 0; r < R; ++r)
+                if (r < rows && span.j < limit[r]) x[v][r] = span.template load<NT>(in + r * a.in_pitch[2]);
+        }
     }
     const int far = a.edge_count > 0 ? a.edges[a.edge_count - 1] : a.exact;
     constexpr int W = N + R - 1;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int j = j0 + v * step;
+        const Span<T> span(j0 + v * step, keys);
+        const int j = span.j;
         if (j >= keys) continue;
         // w[k - r + R - 1]: the bias of place (i0 + r, j + k)
         float w[W];
-        const int d0 = static_cast<int>(j - i0 - s.start) - (R - 1);
+        const int d0 = j - i0 - s.start - (R - 1);
         // far away on one side, or all behind a one-sided query: one bucket
         if (d0 + W - 1 <= -far || (a.two_sided ? d0 >= far : d0 >= 0)) {
             const int u = d0 < 0 ? a.half - 1 : a.two_sided ? 2 * a.half - 1 : 0;
@@ -216,174 +351,226 @@ __global__ void __launch_bounds__(kThreads) k_relpos_bias(RelposArgs a, int64_t 
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (r >= rows) continue;
-            T* o = out + r * a.out_pitch[2] + j;
+            if constexpr (SCORES) span.align(x[v][r]);
             float q[N];
 #pragma unroll
             for (int k = 0; k < N; ++k) {
                 q[k] = w[k - r + R - 1];
-                if constexpr (SCORES) q[k] = __builtin_fmaf(a.scale, x[v][r][k], q[k]);
+                if constexpr (SCORES) q[k] = __builtin_fmaf(a.scale, x[v][r].at(k), q[k]);
             }
             if (j + N > limit[r]) {
 #pragma unroll
                 for (int k = 0; k < N; ++k) q[k] = j + k < limit[r] ? q[k] : -INFINITY;
             }
-            if (j + N <= keys) {
-                store_n<N>(o, q);
-            } else {
-#pragma unroll
-                for (int k = 0; k < N; ++k)
-                    if (j + k < keys) put(o + k, q[k]);
-            }
+            span.store(out + r * a.out_pitch[2], q);
         }
     }
 }
 
 // ---- gradient ---------------------------------------------------------------------
 
+// x of another lane by DPP control.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float lane_of(float x, int lane)
+{
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
+}
+// The sum over the wave, in every lane, in a fixed order: quad partners 1 and 2
+// apart, rotations by 4 and 8 in a row of 16, the rows in order.
 __device__ __forceinline__ float wave_sum(float q)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) q += __shfl_xor(q, d);
-    return q;
+    q += dpp<0xB1>(q);
+    q += dpp<0x4E>(q);
+    q += dpp<0x124>(q);
+    q += dpp<0x128>(q);
+    return ((lane_of(q, 0) + lane_of(q, 16)) + lane_of(q, 32)) + lane_of(q, 48);
 }
 
-// One wave a tile, kThreads / 64 tiles a block.  Of a wave, `lanes` lanes take
-// N columns each of one row, and 64 / lanes groups take a.rows rows each, one
-// below the other.  N rows at a time, a lane's N x N places lie on 2N - 1
-// diagonals, summed in registers; N of them get nothing more from this lane and
-// are added to the group's diagonals in LDS, where the lane to the left adds N
-// rows later.  (A wave's LDS accesses are done in order, and in one access no
-// two lanes have the same diagonal.)
-template <typename T, int N, bool SCORES>
+// The value of the lane below (0 in lane 0): a DPP move of the whole wave by one.
+__device__ __forceinline__ float from_below(float x)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x138, 0xF, 0xF, true));
+}
+
+// One wave a tile: of a wave, `lanes` lanes take N columns each of one row, and
+// 64 / lanes groups take a.rows rows each, one below the other.  N rows at a time,
+// a lane's N x N places lie on 2N - 1 diagonals, summed in registers; N of them
+// get nothing more from this lane and pass to the lane to the right, which meets
+// them N rows later.  So each diagonal's sum leaves the wave once, at its right
+// edge or below its last row, into LDS, where it is added to its bucket.  Bound
+// by HBM: 8 x 16 x 2048 x 2048 bf16 in 168 us, 6.4 TB/s, 606 MB of them seen in
+// sequences of 0 to 2048 keys 118 (with the diagonals added to LDS every N rows
+// 486 and 428; all of a bucket's diagonals by the whole wave, one bucket after the
+// other, 20 us more a call).  The two loads of kBatch rows in turn keep one under way; 8
+// rows loaded, then summed, 187 us; what is said of a row is worked out for all
+// rows at once where they see the same (partly filled tiles are bound by that).
+constexpr int kBatch = 4;
+constexpr int kFewDiagonals = 16;   // of a bucket, up to which one lane sums them
+template <typename T, bool SCORES, bool NT>
 __global__ void __launch_bounds__(kThreads) k_relpos_grad(RelposArgs a, int64_t b0)
 {
-    __shared__ int32_t edges[kRelposMaxEdges];
-    // per wave: 64 N columns and, for each group, its rows and N
-    __shared__ float sums[kThreads / 64][64 * N + kRelposRows + 8 * N];
-    for (int e = threadIdx.x; e < a.edge_count; e += kThreads) edges[e] = a.edges[e];
+    constexpr int N = Row<T>::N;
+    __shared__ float sums[kWaves][64 * N + kRelposRows];
+    __shared__ float totals[kWaves][kRelposMaxBuckets];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float* mine = sums[wave];
-    for (int x = lane; x < 64 * N + kRelposRows + 8 * N; x += 64) mine[x] = 0.0f;
-    __syncthreads();
-    const int64_t tile = (b0 + blockIdx.x) * (kThreads / 64) + wave;
-    if (tile >= a.tiles) return;
-    int64_t rest = tile;
-    const int64_t ct = rest % a.col_tiles;
-    rest /= a.col_tiles;
-    const int64_t rt = rest % a.row_tiles;
-    rest /= a.row_tiles;
-    const int64_t h = rest % a.heads, b = rest / a.heads;
-    const Sequence s = sequence(a, b);
+    int in_plane, h, ct;
+    const uint32_t plane = div_mod(static_cast<uint32_t>(b0) + blockIdx.x, a.plane_blocks, in_plane);
+    const int64_t b = div_mod(plane, a.heads, h);
+    const int rt = div_mod(uniform(in_plane * kWaves + wave), a.col_tiles, ct);
     const int lanes = 1 << a.lane_shift, groups = 64 >> a.lane_shift;
     const int group = lane >> a.lane_shift, l = lane & (lanes - 1);
-    const int pitch = lanes * N + a.rows + N;       // of a group's diagonals
-    const int64_t i0 = (rt * groups + group) * a.rows, c0 = ct * (static_cast<int64_t>(lanes) * N);
-    const int64_t j = c0 + l * N;
-    const T* in = static_cast<const T*>(a.in) + b * a.in_pitch[0] + h * a.in_pitch[1];
-    T* out = static_cast<T*>(a.out) + b * a.out_pitch[0] + h * a.out_pitch[1];
-    float* diag = mine + group * pitch;
-    // diag[c - r + a.rows]: of column c0 + c and row i0 + r
-    float acc[2 * N - 1];
+    const int pitch = lanes * N + a.rows;           // of a group's diagonals
+    const int keys = static_cast<int>(a.keys), queries = static_cast<int>(a.queries);
+    const Sequence s = sequence(a, b);
+    // a tile without a place that is seen leaves nothing (its last row sees most)
+    const int rows_end = (rt + 1) * groups * a.rows;
+    const bool here = rt < a.row_tiles && (SCORES || ct * lanes * N < row_limit(a, s, (rows_end < queries ? rows_end : queries) - 1));
+    if (here) {
+        const int i0 = (rt * groups + group) * a.rows, j = (ct * lanes + l) * N;
+        const Span<T> span(j, keys);
+        const T* in = static_cast<const T*>(a.in) + b * a.in_pitch[0] + h * a.in_pitch[1] +
+                      i0 * a.in_pitch[2];
+        T* out = static_cast<T*>(a.out) + b * a.out_pitch[0] + h * a.out_pitch[1] +
+                 i0 * a.out_pitch[2];
+        float* diag = mine + group * pitch;
+        float acc[2 * N - 1], carry[N];
 #pragma unroll
-    for (int k = 0; k < 2 * N - 1; ++k) acc[k] = 0.0f;
-    for (int r0 = 0; r0 < a.rows; r0 += N) {
-        float x[N][N];
+        for (int k = 0; k < 2 * N - 1; ++k) acc[k] = 0.0f;
 #pragma unroll
-        for (int r = 0; r < N; ++r) {
-            const int64_t i = i0 + r0 + r;
-            const int64_t limit = i < a.queries ? row_limit(a, s, i) : 0;
-            const T* p = in + i * a.in_pitch[2] + j;
-            if (j + N <= limit) {
-                load_n<N>(p, x[r]);
-            } else {
+        for (int k = 0; k < N; ++k) carry[k] = 0.0f;
+        // elements of row i0 + r that this lane's vector has and sees
+        const auto seen = [&](int r) {
+            const int i = i0 + r;
+            const int n = (i < queries ? row_limit(a, s, i) : 0) - j;
+            return n < 0 ? 0 : n < N ? n : N;
+        };
+        const int fixed = seen(0);
+        const bool odd = span.shift > 0 || fixed < N;
+        const T* next = in;
+        // VARIES: rows see different numbers of keys, or are not there
+        const auto load = [&](auto varies, Row<T>(&x)[kBatch], int r0) {
 #pragma unroll
-                for (int k = 0; k < N; ++k) x[r][k] = j + k < limit ? widen(p[k]) : 0.0f;
+            for (int r = 0; r < kBatch; ++r) {
+                x[r] = Row<T>{};
+                if ((varies ? seen(r0 + r) : fixed) > 0) x[r] = span.template load<NT>(next);
+                next += a.in_pitch[2];
             }
-        }
-        if constexpr (SCORES) {
+        };
+        T* left = out;
+        // PLACE: the batch's place among the N rows of the accumulators
+        const auto work = [&](auto varies, auto place, Row<T>(&x)[kBatch], int r0) {
+            constexpr int R = decltype(place)::value;
 #pragma unroll
-            for (int r = 0; r < N; ++r) {
-                const int64_t i = i0 + r0 + r;
-                if (i >= a.queries || j >= a.keys) continue;
-                T* o = out + i * a.out_pitch[2] + j;
-                float v[N];
-#pragma unroll
-                for (int k = 0; k < N; ++k) v[k] = a.scale * x[r][k];
-                // (a place that is not seen is +0 whatever the scale's sign)
-                const int64_t limit = row_limit(a, s, i);
-                if (j + N > limit) {
-#pragma unroll
-                    for (int k = 0; k < N; ++k) v[k] = j + k < limit ? v[k] : 0.0f;
+            for (int r = 0; r < kBatch; ++r) {
+                const int n = varies ? seen(r0 + r) : fixed;
+                if (varies || odd) {
+                    span.align(x[r]);
+                    if (n < N) x[r].keep(n);
                 }
-                if (j + N <= a.keys) {
-                    store_n<N>(o, v);
-                } else {
+                if constexpr (SCORES) {
+                    if ((!varies || i0 + r0 + r < queries) && j < keys) {
+                        float v[N];
 #pragma unroll
-                    for (int k = 0; k < N; ++k)
-                        if (j + k < a.keys) put(o + k, v[k]);
+                        for (int k = 0; k < N; ++k) v[k] = a.scale * x[r].at(k);
+                        if (n < N) {
+#pragma unroll
+                            for (int k = 0; k < N; ++k) v[k] = k < n ? v[k] : 0.0f;
+                        }
+                        span.store(left, v);
+                    }
+                    left += a.out_pitch[2];
                 }
+#pragma unroll
+                for (int k = 0; k < N; ++k) acc[k - (R + r) + N - 1] += x[r].at(k);
             }
-        }
+        };
+        // the diagonals that get nothing more from this lane, with what the lane
+        // to the left had of them N rows before
+        const auto pass = [&](int r0, bool end) {
 #pragma unroll
-        for (int r = 0; r < N; ++r)
+            for (int k = 0; k < N; ++k) {
+                const float below = from_below(carry[k]);
+                carry[k] = (l == 0 ? 0.0f : below) + acc[N - 1 + k];
+            }
+            if (end || l == lanes - 1) {
+                float* f = diag + l * N - r0 + a.rows;
 #pragma unroll
-            for (int k = 0; k < N; ++k) acc[k - r + N - 1] += x[r][k];
-        float* f = diag + l * N - r0 + a.rows;
+                for (int k = 0; k < N; ++k) f[k] = carry[k];
+            }
 #pragma unroll
-        for (int k = 0; k < N; ++k) f[k] += acc[N - 1 + k];
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            for (int k = 0; k < N - 1; ++k) acc[N + k] = acc[k];
 #pragma unroll
-        for (int k = 0; k < N - 1; ++k) acc[N + k] = acc[k];
-#pragma unroll
-        for (int k = 0; k < N; ++k) acc[k] = 0.0f;
+            for (int k = 0; k < N; ++k) acc[k] = 0.0f;
+        };
+        // two batches of rows in turn, one under way while the other is summed
+        using First = std::integral_constant<int, 0>;
+        using Second = std::integral_constant<int, N == kBatch ? 0 : kBatch>;
+        const auto walk = [&](auto varies) {
+            Row<T> x[kBatch], y[kBatch];
+            load(varies, x, 0);
+            for (int r0 = 0; r0 < a.rows; r0 += 2 * kBatch) {
+                load(varies, y, r0 + kBatch);
+                work(varies, First{}, x, r0);
+                if constexpr (N == kBatch) pass(r0, false);
+                if (r0 + 2 * kBatch < a.rows) load(varies, x, r0 + 2 * kBatch);
+                work(varies, Second{}, y, r0 + kBatch);
+                pass(r0 + 2 * kBatch - N, false);
+            }
+        };
+        if (__all(fixed == seen(a.rows - 1) && i0 + a.rows <= queries)) walk(std::false_type{});
+        else walk(std::true_type{});
+        pass(a.rows, true);
     }
-    // what the last rows left: the diagonals left of the lane's columns
-    float* f = diag + l * N;
-#pragma unroll
-    for (int k = 0; k < N - 1; ++k) f[k + 1] += acc[N + k];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    // the diagonals' sums to buckets: as d grows, the buckets follow one another
-    float* part = a.parts + ((h * a.batch + b) * (a.row_tiles * a.col_tiles) + rt * a.col_tiles + ct) *
-                                a.buckets;
+    // the diagonals' sums to buckets, a bucket a lane; the last of each side, which
+    // may have most of the diagonals, by all lanes
+    const int last = pitch - 1;                     // diagonals 1..last
     for (int u0 = 0; u0 < a.buckets; u0 += 64) {
-        const int left = a.buckets - u0 < 64 ? a.buckets - u0 : 64;
-        float total = 0.0f;                         // lane u's bucket u0 + u
-        for (int g = 0; g < groups; ++g) {
+        const int u = u0 + lane;
+        // its distances, as places of diagonals: d from lo to hi
+        int lo = 1, hi = 0;
+        if (here && u < a.buckets) bucket_range(a, u, lo, hi);
+        const bool wide = hi - lo >= kFewDiagonals;
+        float total = 0.0f;
+        for (int g = 0; here && g < groups; ++g) {
             const float* from = mine + g * pitch;
-            // d of from[x] is x + d0, 1 <= x < lanes N + a.rows
-            const int64_t d0 = c0 - ((rt * groups + g) * static_cast<int64_t>(a.rows) + s.start) - a.rows;
-            const int last = lanes * N + a.rows - 1;
-            int x = 1;
-            while (x <= last) {
-                const int d = static_cast<int>(d0 + x);
-                const int u = bucket_of(a, edges, d);
-                // where this bucket ends
-                int64_t end;
-                if (d <= 0) {
-                    const int side = u;
-                    end = side == 0 ? (a.two_sided ? 0 : int64_t(1) << 40)
-                                    : -static_cast<int64_t>(side_begin(a, edges, side));
-                } else if (!a.two_sided || u == a.half * 2 - 1) {
-                    end = int64_t(1) << 40;
-                } else {
-                    // the next bucket that begins later (edges may coincide)
-                    int side = u - a.half + 1;
-                    while (side < a.half - 1 && side_begin(a, edges, side) <= d) ++side;
-                    end = static_cast<int64_t>(side_begin(a, edges, side)) - 1;
-                    if (end < d) end = int64_t(1) << 40;
+            // from[x] is of d = x + d0
+            const int d0 = ct * lanes * N - ((rt * groups + g) * a.rows + s.start) - a.rows;
+            const int x0 = lo - d0 > 1 ? lo - d0 : 1, x1 = hi - d0 < last ? hi - d0 : last;
+            if (!wide) {
+                for (int x = x0; x <= x1; x += 4) {
+                    float q[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) q[k] = from[x + k <= x1 ? x + k : x];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) total += x + k <= x1 ? q[k] : 0.0f;
                 }
-                const int64_t stop = end - d0;
-                const int to = stop < last ? static_cast<int>(stop) : last;
-                if (u >= u0 && u < u0 + left) {
-                    float q = 0.0f;
-                    for (int y = x + lane; y <= to; y += 64) q += from[y];
-                    q = wave_sum(q);
-                    if (lane == u - u0) total += q;
-                }
-                x = to + 1;
+            }
+            uint64_t many = __ballot(wide && x0 <= x1);
+            while (many) {
+                const int k = __builtin_ctzll(many);
+                many &= many - 1;
+                const int begin = __builtin_amdgcn_readlane(x0, k), end = __builtin_amdgcn_readlane(x1, k);
+                float q = 0.0f;
+                for (int x = begin + lane; x <= end; x += 64) q += from[x];
+                q = wave_sum(q);
+                if (lane == k) total += q;
             }
         }
-        if (lane < left) part[u0 + lane] = total;
+        if (u < a.buckets) totals[wave][u] = total;
+    }
+    __syncthreads();
+    float* part = a.parts + ((static_cast<int64_t>(h) * a.batch + b) * a.plane_blocks + in_plane) * a.buckets;
+    for (int u = threadIdx.x; u < a.buckets; u += kThreads) {
+        float q = totals[0][u];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) q += totals[w][u];
+        part[u] = q;
     }
 }
 
@@ -393,7 +580,7 @@ template <typename TT>
 __global__ void __launch_bounds__(kSumThreads) k_relpos_sum(RelposArgs a)
 {
     __shared__ double sums[kSumThreads];
-    const int64_t h = blockIdx.x, n = a.batch * a.row_tiles * a.col_tiles;
+    const int64_t h = blockIdx.x, n = a.batch * a.plane_blocks;
     const float* part = a.parts + h * n * a.buckets;
     // a power of two of lanes across the buckets
     int across = 1;
@@ -425,21 +612,32 @@ __global__ void __launch_bounds__(kSumThreads) k_relpos_sum(RelposArgs a)
     }
 }
 
-template <typename T, typename TT, int N, bool SCORES>
+template <typename T, typename TT, bool SCORES, bool NT>
 void bias_launch(const RelposArgs& a, int64_t b0, uint32_t n, hipStream_t st)
 {
     if (a.lane_vectors > 1)
-        k_relpos_bias<T, TT, N, SCORES, 1, kRelposLaneVectors><<<n, kThreads, 0, st>>>(a, b0);
+        k_relpos_bias<T, TT, SCORES, NT, 1, kRelposLaneVectors><<<n, kThreads, 0, st>>>(a, b0);
     else if (a.queries == 1)
-        k_relpos_bias<T, TT, N, SCORES, 1, 1><<<n, kThreads, 0, st>>>(a, b0);
+        k_relpos_bias<T, TT, SCORES, NT, 1, 1><<<n, kThreads, 0, st>>>(a, b0);
     else
-        k_relpos_bias<T, TT, N, SCORES, kRelposLaneRows, 1><<<n, kThreads, 0, st>>>(a, b0);
+        k_relpos_bias<T, TT, SCORES, NT, kRelposLaneRows, 1><<<n, kThreads, 0, st>>>(a, b0);
 }
-template <typename T, typename TT, int N>
+template <typename T, typename TT>
 void bias_launch(const RelposArgs& a, int64_t b0, uint32_t n, hipStream_t st)
 {
-    if (a.in) bias_launch<T, TT, N, true>(a, b0, n, st);
-    else bias_launch<T, TT, N, false>(a, b0, n, st);
+    if (!a.in) bias_launch<T, TT, false, false>(a, b0, n, st);
+    else if (a.nt) bias_launch<T, TT, true, true>(a, b0, n, st);
+    else bias_launch<T, TT, true, false>(a, b0, n, st);
+}
+template <typename T>
+void grad_launch(const RelposArgs& a, int64_t b0, uint32_t n, hipStream_t st)
+{
+    if (a.out)
+        a.nt ? k_relpos_grad<T, true, true><<<n, kThreads, 0, st>>>(a, b0)
+             : k_relpos_grad<T, true, false><<<n, kThreads, 0, st>>>(a, b0);
+    else
+        a.nt ? k_relpos_grad<T, false, true><<<n, kThreads, 0, st>>>(a, b0)
+             : k_relpos_grad<T, false, false><<<n, kThreads, 0, st>>>(a, b0);
 }
 
 }  // namespace
@@ -448,15 +646,15 @@ int enqueue_relpos_bias(const RelposArgs& a, void* stream)
 {
     hipStream_t st = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
-    for (int64_t b0 = 0; b0 < a.tiles; b0 += max_blocks(kThreads)) {
+    for (int64_t b0 = 0; b0 < a.blocks; b0 += max_blocks(kThreads)) {
         const uint32_t n = static_cast<uint32_t>(
-            a.tiles - b0 < max_blocks(kThreads) ? a.tiles - b0 : max_blocks(kThreads));
+            a.blocks - b0 < max_blocks(kThreads) ? a.blocks - b0 : max_blocks(kThreads));
         if (a.f32)
-            a.table_f32 ? bias_launch<float, float, 4>(a, b0, n, st)
-                        : bias_launch<float, uint16_t, 4>(a, b0, n, st);
+            a.table_f32 ? bias_launch<float, float>(a, b0, n, st)
+                        : bias_launch<float, uint16_t>(a, b0, n, st);
         else
-            a.table_f32 ? bias_launch<uint16_t, float, 8>(a, b0, n, st)
-                        : bias_launch<uint16_t, uint16_t, 8>(a, b0, n, st);
+            a.table_f32 ? bias_launch<uint16_t, float>(a, b0, n, st)
+                        : bias_launch<uint16_t, uint16_t>(a, b0, n, st);
         if (hipGetLastError() != hipSuccess) return ZS_ELAUNCH;
     }
     return ZS_OK;
@@ -466,17 +664,11 @@ int enqueue_relpos_grad(const RelposArgs& a, void* stream)
 {
     hipStream_t st = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
-    const int64_t blocks = (a.tiles + kThreads / 64 - 1) / (kThreads / 64);
-    for (int64_t b0 = 0; b0 < blocks; b0 += max_blocks(kThreads)) {
+    for (int64_t b0 = 0; b0 < a.blocks; b0 += max_blocks(kThreads)) {
         const uint32_t n = static_cast<uint32_t>(
-            blocks - b0 < max_blocks(kThreads) ? blocks - b0 : max_blocks(kThreads));
-        if (a.f32) {
-            if (a.out) k_relpos_grad<float, 4, true><<<n, kThreads, 0, st>>>(a, b0);
-            else k_relpos_grad<float, 4, false><<<n, kThreads, 0, st>>>(a, b0);
-        } else {
-            if (a.out) k_relpos_grad<uint16_t, 8, true><<<n, kThreads, 0, st>>>(a, b0);
-            else k_relpos_grad<uint16_t, 8, false><<<n, kThreads, 0, st>>>(a, b0);
-        }
+            a.blocks - b0 < max_blocks(kThreads) ? a.blocks - b0 : max_blocks(kThreads));
+        if (a.f32) grad_launch<float>(a, b0, n, st);
+        else grad_launch<uint16_t>(a, b0, n, st);
         if (hipGetLastError() != hipSuccess) return ZS_ELAUNCH;
     }
     if (a.table_f32) k_relpos_sum<float><<<static_cast<uint32_t>(a.heads), kSumThreads, 0, st>>>(a);

@@ -549,13 +549,15 @@ typedef struct zs_relpos {
  *   query_starts  device int[B] or NULL: each sequence's own query_start (held to
  *                 +-ZS_RELPOS_FAR); one token a sequence is queries = 1.
  * Errors: ZS_ENULL, ZS_EINVAL_RELPOS (also: in place with other pitches),
- * ZS_EALIGN, ZS_ELAUNCH. */
+ * ZS_EALIGN, ZS_EUNSUPPORTED (more than 2^31 tiles: 4 rows of up to 512 keys in
+ * bf16, 256 in fp32), ZS_ELAUNCH. */
 int relpos_bias(const zs_relpos* r, const void* table, const void* scores,
                 const void* key_lengths, const void* query_starts, void* out, void* stream);
 
 /* Bytes of device workspace relpos_bias_grad needs: a row of buckets (fp32) for
- * each tile of the scores (at least 128 places), rounded up to 256.  0 for a NULL
- * or invalid r.  Host only. */
+ * every four tiles of the scores (8 to 128 rows of up to 512 keys in bf16, 256 in
+ * fp32), rounded up to 256.  0 for a NULL or invalid r, and above 2^31 tiles.
+ * Host only. */
 size_t zs_relpos_workspace_bytes(const zs_relpos* r);
 
 /* The gradient of relpos_bias.  With g = grad[b,h,i,j] (in_pitch):
@@ -569,7 +571,8 @@ size_t zs_relpos_workspace_bytes(const zs_relpos* r);
  * tile and in fp64 over the tiles, in an order that depends on the sizes alone.
  *   workspace  16-byte aligned, >= zs_relpos_workspace_bytes(r) bytes; contents
  *              on entry are ignored.
- * Errors: ZS_ENULL, ZS_EINVAL_RELPOS, ZS_EALIGN, ZS_EWORKSPACE, ZS_ELAUNCH. */
+ * Errors: ZS_ENULL, ZS_EINVAL_RELPOS, ZS_EALIGN, ZS_EUNSUPPORTED, ZS_EWORKSPACE,
+ * ZS_ELAUNCH. */
 int relpos_bias_grad(const zs_relpos* r, const void* grad, const void* key_lengths,
                      const void* query_starts, void* grad_table, void* grad_scores,
                      int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);

@@ -79,6 +79,13 @@ def test_pointers_are_refused():
 
 
 @no_gpu
+def test_too_many_tiles_are_refused():
+    r = Z.make_relpos(65536, 1 << 22, 1, dtype=Z.ZS_F32)        # 2^33 tiles of 32 rows
+    assert bias(r) == Z.ZS_EUNSUPPORTED and Z.zs_relpos_workspace_bytes(r) == 0
+    assert grad(r, nbytes=1 << 60) == Z.ZS_EUNSUPPORTED
+
+
+@no_gpu
 @pytest.mark.parametrize("empty", [dict(batch=0), dict(queries=0), dict(keys=0)])
 def test_no_places_is_no_launch(empty):
     assert bias(relpos(**empty), table=None, out=None) == Z.ZS_OK
