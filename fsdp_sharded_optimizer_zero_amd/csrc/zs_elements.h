@@ -105,5 +105,16 @@ __device__ __forceinline__ void store_nt(float* p, const float v[N])
                                     reinterpret_cast<f32x4_u*>(p + i));
 }
 
+// Block b of n in an order in which each of the 8 XCDs, to which consecutive
+// blocks are dealt in turn, has stretches of STRETCH blocks (a power of two):
+// neighbours that share a cache line or a page of HBM are then mostly on one XCD,
+// and work that is uneven over n still falls to all.
+template <int STRETCH, typename I>
+__device__ __forceinline__ I xcd_order(I b, int64_t n)
+{
+    const I in = b & (8 * STRETCH - 1), first = b - in;
+    return first + 8 * STRETCH <= n ? first + (in & 7) * STRETCH + (in >> 3) : b;
+}
+
 }  // namespace
 }  // namespace zs

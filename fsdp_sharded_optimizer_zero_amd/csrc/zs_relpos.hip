@@ -236,17 +236,6 @@ struct Span {
 
 // ---- bias -------------------------------------------------------------------------
 
-// Block b of n in an order in which each of the 8 XCDs, to which consecutive
-// blocks are dealt in turn, has stretches of kStretch blocks: neighbours that
-// share a cache line are then mostly in one L2, and sequences of different
-// lengths still fall to all.
-constexpr uint32_t kStretch = 256;
-__device__ __forceinline__ uint32_t xcd_order(uint32_t b, int64_t n)
-{
-    const uint32_t in = b % (8 * kStretch), first = b - in;
-    return first + 8 * kStretch <= n ? first + (in & 7) * kStretch + (in >> 3) : b;
-}
-
 constexpr int kFewEdges = 16;
 // The buckets of W diagonals d0, d0 + 1, ...: for few edges by looking at all
 // of them (scalars), else by search in LDS.
@@ -297,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) k_relpos_bias(RelposArgs a, int64_t 
         for (int e = threadIdx.x; e < a.edge_count; e += kThreads) edges[e] = a.edges[e];
         __syncthreads();
     }
-    const uint32_t block = xcd_order(static_cast<uint32_t>(b0) + blockIdx.x, a.blocks);
+    const uint32_t block = xcd_order<256>(static_cast<uint32_t>(b0) + blockIdx.x, a.blocks);
     const uint32_t tile = block * kWaves + uniform(threadIdx.x >> 6);
     if (tile >= a.tiles) return;
     int ct, rt, h;

@@ -314,18 +314,19 @@ __device__ void chunk_clip(const TensorsArgs& a, const TensorChunk& c, int part,
 }
 
 // A block takes one part of a piece and ends: 32 bytes a lane of the wider of
-// the two types, nt loads and stores, all loads first.  872 million elements:
-// fp32 to fp32 574 us (6.1 TB/s), bf16 to fp32 409 (6.4), bf16 to bf16 285,
-// fp32 to bf16 407; blocks that walk through their piece 635-680 us for the
-// first, with the next loads under way or not; plain stores 660.  In place a
-// lane has 64 bytes (583 us; 32: 575): what is then within the limit costs half
+// the two types, nt loads and stores, all loads first, in stretches by XCD.  436
+// million elements: fp32 to fp32 554 us (6.3 TB/s), bf16 to fp32 411 (6.4), bf16
+// to bf16 275, one element off 574, 447 and 302 (in the plain order 576, 417 and
+// 291; 611, 447 and 308); blocks that walk through their piece 635-680 us for the
+// first, with the next loads under way or not; plain stores 5% slower.  In place
+// a lane has 64 bytes (583 us; 32: 575): what is then within the limit costs half
 // as many waves that only look.
 __global__ void __launch_bounds__(kThreads) k_tensors_clip(TensorsArgs a, int parts, int64_t b0)
 {
     // a list in place and well within the limit: no wave looks at its piece
-    // (872 million fp32: 24 us, with the division in every wave 55)
+    // (436 million fp32: 24 us, with the division in every wave 55)
     if (*a.sqnorm + a.other <= a.quiet) return;
-    const int64_t b = b0 + blockIdx.x, k = b / parts;
+    const int64_t b = xcd_order<64>(b0 + blockIdx.x, a.chunks * parts), k = b / parts;
     const int part = static_cast<int>(b - k * parts);
     const TensorChunk c = a.table[k];
     constexpr int P = kTensorPlace;
