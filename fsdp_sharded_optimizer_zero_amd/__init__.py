@@ -761,7 +761,9 @@ class Tensors:
     """A list of tensors as tensors_sqnorm, tensors_clip and tensors_clip_norm
     take it: the struct, its plan on the GPU, and the tensors themselves, whose
     memory the plan names.  Make a new one where a tensor is replaced by another
-    (a gradient that was set to None and made anew)."""
+    (a gradient that was set to None and made anew).  One call at a time uses a
+    list (its plan holds their partial sums), and the list lives until its calls
+    have ended on the GPU."""
 
     def __init__(self, struct, plan, tensors, out, device):
         self.struct, self.plan, self.tensors, self.out = struct, plan, tensors, out
@@ -811,17 +813,33 @@ def make_tensors(tensors, out=None) -> Tensors:
     the same shapes (views of a flat buffer, say), or None: in place.
 
     A tensor's elements may be in any order in memory as long as they fill it
-    (a transposed gradient), or its rows may be evenly apart."""
+    (a transposed gradient), or its rows may be evenly apart.  None may be written
+    where another is read or written (the same tensor twice, in place)."""
     tensors = list(tensors)
     out = tensors if out is None else list(out)
     if len(out) != len(tensors):
         raise ValueError(f"{len(tensors)} tensors, {len(out)} out")
-    arr = (zs_tensor * max(len(tensors), 1))(*[_tensor_entry(i, t, o) for i, (t, o)
-                                               in enumerate(zip(tensors, out))])
-    device = _cuda().current_device()
-    for i, t in enumerate(tensors + out):
-        if t.get_device() != device:
-            raise ValueError(f"a tensor on GPU {t.get_device()}: the current device is {device}")
+    cuda = _cuda()
+    kinds = {_torch.bfloat16: ZS_BF16, _torch.float32: ZS_F32}
+    # zs_tensor's seven words a tensor
+    words, devices = [], set()
+    for i, (t, o) in enumerate(zip(tensors, out)):
+        kind, other = kinds.get(getattr(t, "dtype", None)), kinds.get(getattr(o, "dtype", None))
+        if (kind is not None and other is not None and t.is_cuda and o.is_cuda
+                and t.is_contiguous() and o.is_contiguous() and t.shape == o.shape):
+            n = t.numel()
+            words += (t.data_ptr(), o.data_ptr(), 1, n, n, n, kind | other << 32)
+        else:
+            e = _tensor_entry(i, t, o)
+            words += (e.in_ or 0, e.out or 0, e.rows, e.cols, e.in_pitch, e.out_pitch,
+                      e.in_dtype | e.out_dtype << 32)
+        devices.add(t.get_device())
+        devices.add(o.get_device())
+    device = cuda.current_device()
+    for d in devices:
+        if d != device:
+            raise ValueError(f"a tensor on GPU {d}: the current device is {device}")
+    arr = (C.c_int64 * max(len(words), 1))(*words)
     struct = zs_tensors()
     _check(lib().zs_tensors_layout(arr, len(tensors), C.byref(struct)), "zs_tensors_layout")
     host = _torch.empty(struct.plan_bytes, dtype=_torch.uint8)

@@ -9,10 +9,12 @@
 // Accounting: the same page's Theorem "ZeRO memory and communication" (table
 // and proof); the error convention follows the state_bytes helper of
 // "Distributed Training Basics -- DDP and FSDP" (Memory accounting).
+#include <algorithm>
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
 #include <cstring>
+#include <vector>
 
 #include "zs_internal.h"
 
@@ -167,6 +169,75 @@ int check_tensor(const zs_tensor& t)
     if (t.in == t.out &&
         (t.in_dtype != t.out_dtype || (t.rows > 1 && t.in_pitch != t.out_pitch)))
         return ZS_EINVAL_TENSORS;
+    return ZS_OK;
+}
+
+// What one tensor reads or writes: `rows` runs of `width` bytes, `pitch` apart,
+// from `begin` up to before `end`.
+struct Extent {
+    uint64_t begin, end, pitch, width;
+    int64_t tensor;
+    bool out;
+};
+Extent extent(const zs_tensor& t, int64_t i, bool out)
+{
+    const uint64_t size = static_cast<uint64_t>(elem_size(out ? t.out_dtype : t.in_dtype));
+    const uint64_t rows = static_cast<uint64_t>(t.rows);
+    const uint64_t pitch = rows > 1 ? (out ? t.out_pitch : t.in_pitch) * size : 0;
+    Extent e;
+    e.begin = reinterpret_cast<uint64_t>(out ? t.out : t.in);
+    e.width = t.cols * size;
+    e.pitch = pitch;
+    e.end = e.begin + (rows - 1) * pitch + e.width;
+    e.tensor = i;
+    e.out = out;
+    return e;
+}
+
+// Whether two extents that overlap have no byte in common all the same: columns
+// of one matrix (a single row counts as one of the other's).
+bool beside(const Extent& a, const Extent& b)
+{
+    const uint64_t pitch = a.pitch ? a.pitch : b.pitch;
+    if (pitch == 0 || (a.pitch && b.pitch && a.pitch != b.pitch)) return false;
+    if (a.width > pitch || b.width > pitch) return false;
+    // b's columns as seen from a's first, in a row of `pitch`
+    const uint64_t from = b.begin >= a.begin ? (b.begin - a.begin) % pitch
+                                             : (pitch - (a.begin - b.begin) % pitch) % pitch;
+    return from >= a.width && from + b.width <= pitch;
+}
+
+// No tensor is written where another one is read or written (the same tensor
+// twice, in place, would be clipped twice, or once in places).
+int check_overlap(const zs_tensor* list, int64_t count)
+{
+    std::vector<Extent> all;
+    for (int64_t i = 0; i < count; ++i) {
+        const zs_tensor& t = list[i];
+        if (t.rows == 0 || t.cols == 0 || !t.out) continue;
+        all.push_back(extent(t, i, true));
+    }
+    if (all.empty()) return ZS_OK;
+    for (int64_t i = 0; i < count; ++i) {
+        const zs_tensor& t = list[i];
+        if (t.rows == 0 || t.cols == 0 || t.in == t.out) continue;
+        all.push_back(extent(t, i, false));
+    }
+    std::sort(all.begin(), all.end(), [](const Extent& a, const Extent& b) {
+        return a.begin != b.begin ? a.begin < b.begin : a.tensor < b.tensor;
+    });
+    // the extents that the next one may overlap
+    std::vector<const Extent*> open;
+    for (const Extent& e : all) {
+        size_t kept = 0;
+        for (const Extent* o : open) {
+            if (o->end <= e.begin) continue;
+            open[kept++] = o;
+            if ((o->out || e.out) && !beside(*o, e)) return ZS_EINVAL_TENSORS;
+        }
+        open.resize(kept);
+        open.push_back(&e);
+    }
     return ZS_OK;
 }
 
@@ -501,6 +572,12 @@ int zs_tensors_layout(const zs_tensor* list, int64_t count, zs_tensors* t)
         if (!list[i].out) r.has_out = 0;
     }
     if (r.has_out && place) r.has_out = 2;
+    try {
+        const int rc = zs::check_overlap(list, count);
+        if (rc != ZS_OK) return rc;
+    } catch (...) {
+        return ZS_EUNSUPPORTED;         // host memory for the check
+    }
     // as many pieces as fill the GPU, and no more than one block can join
     r.chunk_bytes = zs::kTensorChunkMin;
     while (r.chunk_bytes < 4 * zs::kTensorPart && bytes / r.chunk_bytes > zs::kTensorChunksMin)
@@ -609,8 +686,9 @@ const char* zs_strerror(int code)
     case ZS_EINVAL_DISTILL:
         return "invalid zs_distill (a size, pitch, type, temperature, alpha or scale out of range)";
     case ZS_EINVAL_TENSORS:
-        return "invalid zs_tensor (a size, pitch or type out of range, or in place with another), "
-               "or zs_tensors not as zs_tensors_layout left it";
+        return "invalid zs_tensor (a size, pitch or type out of range, in place with another, or "
+               "written where another of the list is read or written), or zs_tensors not as "
+               "zs_tensors_layout left it";
     case ZS_EINVAL_RELPOS:
         return "invalid zs_relpos (a size, pitch, type, position, bucket count, distance or scale "
                "out of range)";

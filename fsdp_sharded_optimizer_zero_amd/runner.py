@@ -255,7 +255,8 @@ class RelposBias(torch.autograd.Function):
         out = torch.empty(shape, dtype=dtype, device=table.device)
         relpos_bias(r, table.contiguous(), out, None if scores is None else scores.contiguous(),
                     key_lengths, query_starts)
-        ctx.r, ctx.scores = r, scores is not None and ctx.needs_input_grad[2]
+        # the caller may change r before the backward pass
+        ctx.r, ctx.scores = type(r).from_buffer_copy(r), scores is not None and ctx.needs_input_grad[2]
         ctx.save_for_backward(table, key_lengths, query_starts)
         return out
 

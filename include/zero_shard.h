@@ -100,8 +100,10 @@ extern "C" {
 #define ZS_EINVAL_DISTILL (-17)  /* zs_distill: a size, pitch, type, temperature,
                                     alpha or scale out of range */
 #define ZS_EINVAL_TENSORS (-18)  /* zs_tensor: a size, pitch or type out of range,
-                                    or in place with another type or pitch;
-                                    zs_tensors: not as zs_tensors_layout left it */
+                                    in place with another type or pitch, or
+                                    written where another of the list is read or
+                                    written; zs_tensors: not as
+                                    zs_tensors_layout left it */
 #define ZS_EINVAL_RELPOS  (-19)  /* zs_relpos: a size, pitch, type, position, bucket
                                     count, distance or scale out of range */
 
@@ -619,7 +621,10 @@ typedef struct zs_tensors {
     uint32_t stamp;        /* of the fields above, by which a changed one is seen */
 } zs_tensors;
 
-/* Checks a list of `count` tensors and fills *t.  Host only.
+/* Checks a list of `count` tensors and fills *t.  No tensor's `out` may share a
+ * byte with another's `in` or `out`: a tensor listed twice and clipped in place is
+ * refused.  (Columns of one matrix, of one pitch, are beside one another.)  Host
+ * only.
  * Errors: ZS_ENULL (list, with count > 0; out; a tensor's `in`), ZS_EALIGN,
  * ZS_EINVAL_TENSORS, ZS_EUNSUPPORTED (count > ZS_TENSORS_MAX). */
 int zs_tensors_layout(const zs_tensor* list, int64_t count, zs_tensors* t);

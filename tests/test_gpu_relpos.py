@@ -2,11 +2,11 @@
 
 A place of the bias is one fused multiply-add (one fp32 rounding; none for the
 bias alone) and one rounding to the output type: u |value|, then half a step.
-The table's gradient sums fp32 values: a place goes through at most N rows of a
-lane (8), a tile's rows / N additions in LDS (16), a bucket's stretch of a tile's
-diagonals a lane (10), the wave (6) and the groups (8), fewer than 64 additions,
-each of at most u times the sum of absolute values; then fp64, one rounding to
-fp32 and one to the type."""
+The table's gradient sums fp32 values: a place goes through at most 8 additions
+in its lane, 16 from lane to lane (a tile's rows by 8, or 32 by 4 after 4), 16 of
+a bucket's diagonals in a lane or 10 and the wave's 6, 8 groups and 4 waves: fewer
+than 64, each of at most u times the sum of absolute values; then fp64, one
+rounding to fp32 and one to the type."""
 import math
 
 import pytest
@@ -388,3 +388,45 @@ def test_binding_refuses():
     with pytest.raises(ValueError, match="workspace"):
         Z.relpos_bias_grad(r, x, table, torch.empty(16, dtype=torch.uint8, device="cuda"),
                            workspace_bytes=4096)
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    r = Z.make_relpos(4, 10, 20, batch=3, dtype=Z.ZS_F32)
+    x, table = data(r, F32)
+    ws = torch.empty(Z.zs_relpos_workspace_bytes(r), dtype=torch.uint8, device="cuda")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in (lambda: Z.relpos_bias(r, table, x, stream=0),
+                 lambda: Z.relpos_bias_grad(r, x, table, ws, stream=0)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+
+
+@pytest.mark.parametrize("keys", [1, 3, 5, 7, 8, 9, 15, 512 + 7, 1024 + 1, 4096 + 3])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_ends_of_rows(keys, dtype):
+    """Rows of fewer keys than a vector, and every way a row can end in one,
+    the last row's end being the tensor's; in place too."""
+    r = Z.make_relpos(2, 13, keys, batch=2, dtype=KIND[dtype], query_start=keys // 2, scale=0.5)
+    lengths = torch.tensor([keys, max(1, keys - 1)], device="cuda")
+    check(r, dtype, lengths=lengths, seed=keys)
+    x, table = data(r, dtype, keys)
+    want = torch.empty_like(x)
+    Z.relpos_bias(r, table, want, scores=x, key_lengths=lengths)
+    y = x.clone()
+    Z.relpos_bias(r, table, y, scores=y, key_lengths=lengths)
+    assert torch.equal(y, want)
+    ws = torch.empty(Z.zs_relpos_workspace_bytes(r), dtype=torch.uint8, device="cuda")
+    dt, dx = torch.empty_like(table), torch.empty_like(x)
+    Z.relpos_bias_grad(r, x, dt, ws, dx, key_lengths=lengths)
+    y, again = x.clone(), torch.empty_like(table)
+    Z.relpos_bias_grad(r, y, again, ws, y, key_lengths=lengths)
+    assert torch.equal(y, dx) and torch.equal(dt, again)
+
+
+def test_many_rows_and_sequences():
+    """More tiles than the GPU holds at once, in stretches and at their end."""
+    r = Z.make_relpos(16, 100, 70, batch=70, dtype=Z.ZS_BF16, causal=True)
+    check(r, BF16, seed=1)
+    r = Z.make_relpos(33, 1, 2100, batch=65, dtype=Z.ZS_BF16, bidirectional=False, scale=0.125)
+    starts = torch.randint(0, 2100, (65,), generator=torch.Generator().manual_seed(1))
+    check(r, BF16, lengths=(starts + 1).cuda(), starts=starts.cuda(), seed=2)

@@ -342,3 +342,40 @@ def test_binding_refuses():
         Z.make_tensors(tensors, [tensors[0], tensors[0]])
     with pytest.raises(ValueError, match="float64"):
         Z.make_tensors([scalar()])
+
+
+def test_columns_of_one_matrix_and_the_same_tensor_twice():
+    """Three column slices of one gradient are three tensors; the same memory
+    twice is refused."""
+    fused = torch.randn((50, 96), device="cuda").to(BF16)
+    parts = list(fused.split(32, dim=1))
+    check(parts)
+    with pytest.raises(Z.ZSError, match="zs_tensor"):
+        Z.make_tensors([parts[0], fused])
+    with pytest.raises(Z.ZSError, match="zs_tensor"):
+        Z.make_tensors([parts[0], parts[0]])
+    flat = torch.zeros(100, device="cuda")
+    with pytest.raises(Z.ZSError, match="zs_tensor"):
+        Z.make_tensors([parts[0][0], parts[1][0]], [flat[:32], flat[31:63]])
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    tensors = make([10, 20], (F32,))
+    T, q = Z.make_tensors(tensors), scalar()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in (lambda: Z.make_tensors(tensors), lambda: Z.tensors_sqnorm(T, q, stream=0),
+                 lambda: Z.tensors_clip(T, 1.0, q, stream=0),
+                 lambda: Z.tensors_clip_norm(T, 1.0, q, stream=0)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+
+
+def test_a_list_outlives_the_callers_names():
+    """The list keeps its tensors: what the caller lets go is not handed out anew."""
+    T = Z.make_tensors(make([1 << 20, 5], (F32,), seed=14))
+    want = math.fsum(sq_sum(t) for t in T.tensors)
+    for _ in range(5):
+        torch.full((1 << 20,), 7.0, device="cuda")
+    q = scalar()
+    Z.tensors_sqnorm(T, q)
+    assert abs(float(q) - want) <= REL * want

@@ -32,6 +32,11 @@ def layout(entries, count=None):
 
 
 def plan(entries):
+    """The plan of the entries, moved apart in memory."""
+    for i, e in enumerate(entries):
+        place = e.in_ == e.out
+        e.in_ = FAKE + (i << 37)
+        e.out = e.in_ if place else (1 << 60) + (i << 37)
     rc, t, arr = layout(entries)
     assert rc == Z.ZS_OK
     host = np.full(t.plan_bytes, 0xAB, np.uint8)
@@ -105,7 +110,7 @@ BAD = [dict(rows=-1), dict(cols=-1), dict(in_dtype=2), dict(out_dtype=-1),
 
 @pytest.mark.parametrize("bad", BAD)
 def test_entries_are_refused(bad):
-    assert layout([entry(), entry(**bad)])[0] == Z.ZS_EINVAL_TENSORS
+    assert layout([entry(in_=FAKE + 4096, out=2 * FAKE), entry(**bad)])[0] == Z.ZS_EINVAL_TENSORS
 
 
 def test_lists_are_refused():
@@ -121,15 +126,59 @@ def test_lists_are_refused():
     assert L.zs_tensors_layout(None, 0, None) == Z.ZS_ENULL
     # no element is read of a tensor without any
     assert layout([entry(cols=0, in_=None, out=None)])[0] == Z.ZS_OK
-    rc, t, arr = layout([entry(), entry(out=None)])
+    rc, t, arr = layout([entry(), entry(in_=FAKE + 4096, out=None)])
     assert rc == Z.ZS_OK and t.has_out == 0
     host = np.zeros(t.plan_bytes, np.uint8)
     fill = lambda a, s, n=host.nbytes: L.zs_tensors_plan(a, C.byref(s), host.ctypes.data, n)
     assert fill(arr, t, host.nbytes - 1) == Z.ZS_EWORKSPACE
-    other = layout([entry(), entry(cols=101, out=None)])
+    other = layout([entry(), entry(in_=FAKE + 4096, cols=101, out=None)])
     assert fill(other[2], t) == Z.ZS_EINVAL_TENSORS       # another list's
     assert L.zs_tensors_plan(arr, C.byref(t), None, host.nbytes) == Z.ZS_ENULL
     assert L.zs_tensors_plan(arr, None, host.ctypes.data, host.nbytes) == Z.ZS_ENULL
+
+
+def test_overlaps_are_refused():
+    """An `out` that shares a byte with another tensor's `in` or `out`."""
+    A = FAKE
+    own = dict(in_dtype=Z.ZS_F32)
+    place = lambda at, **kw: entry(in_=at, out=at, **own, **kw)
+    go = lambda at, to, **kw: entry(in_=at, out=to, **own, **kw)
+    B = A + (1 << 30)
+    ok = [
+        [place(A), place(A + 400)],
+        [go(A, B), go(A, B + 400)],                                 # read twice
+        [go(A, B), go(A + 200, B + 400)],
+        [place(A, rows=5, cols=30, in_pitch=100, out_pitch=100),    # columns of a matrix
+         place(A + 120, rows=5, cols=70, in_pitch=100, out_pitch=100)],
+        [place(A + 120, rows=5, cols=70, in_pitch=100, out_pitch=100),
+         place(A, rows=5, cols=30, in_pitch=100, out_pitch=100),
+         place(A + 400 * 5, cols=100)],
+        [place(A, rows=5, cols=30, in_pitch=100, out_pitch=100),    # one row beside them
+         place(A + 400 * 2 + 120, cols=70)],
+        [place(A, cols=0), place(A)],
+    ]
+    bad = [
+        [place(A), place(A)],                                       # the same, twice
+        [place(A), place(A + 396)],
+        [go(A, B), go(A + 4000, B)],
+        [go(A, A + 4)],                                             # onto itself, moved
+        [go(A, B), go(B, B + 4000)],                                # reads what is written
+        [go(B, B + 4000), go(A, B)],
+        [place(A), go(A, B)],
+        [place(A, rows=5, cols=30, in_pitch=100, out_pitch=100),
+         place(A + 116, rows=5, cols=70, in_pitch=100, out_pitch=100)],
+        [place(A, rows=5, cols=30, in_pitch=100, out_pitch=100),
+         place(A + 120, rows=5, cols=71, in_pitch=100, out_pitch=100)],
+        [place(A, rows=5, cols=30, in_pitch=100, out_pitch=100),
+         place(A + 120, rows=5, cols=10, in_pitch=50, out_pitch=50)],
+        [place(A, rows=5, cols=30, in_pitch=100, out_pitch=100), place(A + 1100, cols=100)],
+        [place(A, cols=5000), place(A + 400, cols=1), place(A + 8000, cols=1)],
+    ]
+    for entries in ok:
+        assert layout(entries)[0] == Z.ZS_OK, entries
+    for entries in bad:
+        assert layout(entries)[0] == Z.ZS_EINVAL_TENSORS, entries
+        assert layout(entries[::-1])[0] == Z.ZS_EINVAL_TENSORS, entries
 
 
 @no_gpu
