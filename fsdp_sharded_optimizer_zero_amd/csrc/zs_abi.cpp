@@ -6,6 +6,7 @@
 // What each entry point computes is stated with its declaration in
 // zero_shard.h, with the passage of "Data parallelism, ZeRO and FSDP" (and
 // its companion pages) that defines it.
+#include <cmath>
 #include <cstdint>
 
 #include "zs_internal.h"
@@ -564,7 +565,7 @@ int set_clip(const zs_tensors* t, double max_norm, const double* sqnorm, double 
     a->max_norm = max_norm;
     // sqrt(Q) + 1e-6 <= max_norm, with room for the roundings on both sides
     const double most = max_norm - 1e-6;
-    a->quiet = t->has_out == 2 && most > 0.0 ? most * most * (1.0 - 1e-9) : -1.0;
+    a->quiet = t->has_out == 2 && most > 0.0 ? most * most * (1.0 - 1e-9) : -HUGE_VAL;
     return ZS_OK;
 }
 

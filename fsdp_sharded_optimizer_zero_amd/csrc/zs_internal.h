@@ -328,7 +328,7 @@ struct TensorsArgs {
     int32_t accumulate;
     const double* sqnorm;
     double other, max_norm;
-    double quiet;           // all in place: up to this Q the coefficient is 1 (else < 0)
+    double quiet;           // all in place: up to this Q the coefficient is 1 (else -Inf)
 };
 int enqueue_tensors_sqnorm(const TensorsArgs& a, void* stream);
 int enqueue_tensors_clip(const TensorsArgs& a, void* stream);

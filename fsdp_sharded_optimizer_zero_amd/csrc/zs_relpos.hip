@@ -3,9 +3,9 @@
 //
 // What is computed is stated with the entry points in zero_shard.h.  Both are
 // bound by HBM: the bias of a place depends on its diagonal (key minus query)
-// alone, so a block works its buckets out once for a diagonal and not for a
-// place, and the gradient sums diagonals in registers and turns them into
-// buckets once at the end.
+// alone, so a lane works out the bucket of a diagonal and not of a place, and the
+// gradient sums diagonals in registers and turns them into buckets once at the
+// end.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -52,7 +52,7 @@ __device__ __forceinline__ void bucket_range(const RelposArgs& a, int u, int& lo
 {
     const bool behind = u >= a.half;
     const int v = behind ? u - a.half : u;
-    constexpr int kAll = 1 << 30;
+    constexpr int kAll = INT32_MAX;
     // distances of one side, from begin up to before end
     const int begin = v <= a.exact ? v : a.edges[v - a.exact - 1];
     const int end = v == a.half - 1 ? kAll : v < a.exact ? v + 1 : a.edges[v - a.exact];
@@ -524,13 +524,16 @@ __global__ void __launch_bounds__(kThreads) k_relpos_grad(RelposArgs a, int64_t 
         // its distances, as places of diagonals: d from lo to hi
         int lo = 1, hi = 0;
         if (here && u < a.buckets) bucket_range(a, u, lo, hi);
-        const bool wide = hi - lo >= kFewDiagonals;
+        const bool wide = static_cast<int64_t>(hi) - lo >= kFewDiagonals;
         float total = 0.0f;
         for (int g = 0; here && g < groups; ++g) {
             const float* from = mine + g * pitch;
             // from[x] is of d = x + d0
             const int d0 = ct * lanes * N - ((rt * groups + g) * a.rows + s.start) - a.rows;
-            const int x0 = lo - d0 > 1 ? lo - d0 : 1, x1 = hi - d0 < last ? hi - d0 : last;
+            // (in 64 bits: distances may be 2^30, and a range all of them)
+            const int64_t begin64 = static_cast<int64_t>(lo) - d0, end64 = static_cast<int64_t>(hi) - d0;
+            const int x0 = begin64 < 1 ? 1 : begin64 > last ? last + 1 : static_cast<int>(begin64);
+            const int x1 = end64 < 0 ? 0 : end64 > last ? last : static_cast<int>(end64);
             if (!wide) {
                 for (int x = x0; x <= x1; x += 4) {
                     float q[4];

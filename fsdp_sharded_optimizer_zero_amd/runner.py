@@ -261,6 +261,7 @@ class RelposBias(torch.autograd.Function):
         return out
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         table, key_lengths, query_starts = ctx.saved_tensors
         dtable = torch.empty(table.shape, dtype=table.dtype, device=table.device)

@@ -430,3 +430,34 @@ def test_many_rows_and_sequences():
     r = Z.make_relpos(33, 1, 2100, batch=65, dtype=Z.ZS_BF16, bidirectional=False, scale=0.125)
     starts = torch.randint(0, 2100, (65,), generator=torch.Generator().manual_seed(1))
     check(r, BF16, lengths=(starts + 1).cuda(), starts=starts.cuda(), seed=2)
+
+
+@pytest.mark.parametrize("start", [Z.ZS_RELPOS_FAR, -Z.ZS_RELPOS_FAR])
+@pytest.mark.parametrize("by_query", [True, False])
+def test_ends_of_the_range(start, by_query):
+    """As many queries, or keys, as a call may have, at the ends of the positions:
+    a gradient of ones counts the places of each bucket, and the bias of the
+    first and last places is their bucket's."""
+    far = Z.ZS_RELPOS_FAR
+    q, k = (far, 1) if by_query else (1, far)
+    r = Z.make_relpos(1, q, k, query_start=start, dtype=Z.ZS_BF16)
+    g = torch.ones((1, 1, q, k), dtype=BF16, device="cuda")
+    ws = torch.empty(Z.zs_relpos_workspace_bytes(r), dtype=torch.uint8, device="cuda")
+    dt = torch.empty((32, 1), device="cuda")
+    Z.relpos_bias_grad(r, g, dt, ws)
+    # distances run over a stretch of far numbers from d0 on
+    d0 = (-start - (far - 1)) if by_query else -start
+    first = max(d0, -200)
+    near = torch.arange(first, max(first, min(d0 + far, 200)))
+    want = torch.bincount(buckets_of(r, near), minlength=32).double() if len(near) else \
+        torch.zeros(32, dtype=torch.float64)
+    want[15] += max(0, min(d0 + far, -200) - d0)
+    want[31] += max(0, d0 + far - max(d0, 200))
+    # counts of up to 2^29: exact in the tiles and in fp64, rounded once to fp32
+    assert want.sum() == far and torch.equal(dt[:, 0].cpu(), want.float())
+    table = torch.arange(32, dtype=F32, device="cuda")[:, None].contiguous()
+    Z.relpos_bias(r, table, g)
+    flat = g.reshape(-1)
+    at = torch.tensor([0, 1, 130, far // 2, far - 131, far - 2, far - 1])
+    d = (-at - start) if by_query else (at - start)
+    assert torch.equal(flat[at.cuda()].cpu().long(), buckets_of(r, d))
