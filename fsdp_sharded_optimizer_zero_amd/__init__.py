@@ -768,6 +768,7 @@ class Tensors:
     def __init__(self, struct, plan, tensors, out, device):
         self.struct, self.plan, self.tensors, self.out = struct, plan, tensors, out
         self.device = device
+        self.refs = C.byref(struct), plan.data_ptr()      # what every call hands over
 
 
 def _tensor_entry(i, t, o):
@@ -850,8 +851,7 @@ def make_tensors(tensors, out=None) -> Tensors:
 
 
 def _tensors_on(t: Tensors, stream, *scalars):
-    stream = _stream_on(stream, t.plan, *scalars)
-    return C.byref(t.struct), t.plan.data_ptr(), stream
+    return (*t.refs, _stream_on(stream, t.plan, *scalars))
 
 
 def tensors_sqnorm(t: Tensors, sqnorm_out, tensor_sqnorms=None, accumulate: bool = False,

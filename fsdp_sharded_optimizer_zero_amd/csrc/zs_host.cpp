@@ -371,6 +371,7 @@ void relpos_buckets(const zs_relpos* r, RelposArgs* a)
         }
         a->edges[k - 1] = static_cast<int32_t>(edge);
     }
+    a->far = a->edge_count > 0 ? a->edges[a->edge_count - 1] : a->exact;
 }
 
 namespace {

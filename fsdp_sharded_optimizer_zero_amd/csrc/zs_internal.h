@@ -372,6 +372,7 @@ struct RelposArgs {
     int32_t rows;           // of a tile (gradient: of a group of lanes)
     int32_t buckets, two_sided, causal;
     int32_t half, exact;    // buckets of a side; those of single distances
+    int32_t far;            // where a side's last bucket begins
     int32_t edge_count;
     int32_t edge_span;      // largest power of two up to edge_count
     int32_t f32, table_f32, id64, accumulate;

@@ -33,7 +33,7 @@ constexpr int kSumThreads = 1024;
 __device__ __forceinline__ int side_bucket(const RelposArgs& a, const int32_t* edges, int n)
 {
     if (n < a.exact) return n;
-    if (a.edge_count == 0 || n >= edges[a.edge_count - 1]) return a.exact + a.edge_count;
+    if (n >= a.far) return a.half - 1;
     int at = 0;
     for (int half = a.edge_span; half > 0; half >>= 1)
         if (at + half <= a.edge_count && edges[at + half - 1] <= n) at += half;
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads) k_relpos_bias(RelposArgs a, int64_t 
                 if (r < rows && span.j < limit[r]) x[v][r] = span.template load<NT>(in + r * a.in_pitch[2]);
         }
     }
-    const int far = a.edge_count > 0 ? a.edges[a.edge_count - 1] : a.exact;
+    const int far = a.far;
     constexpr int W = N + R - 1;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
