@@ -510,8 +510,9 @@ extern "C" int relpos_bias_grad(const zs_relpos* r, const void* grad, const void
     if (!grad_table || !workspace || (!grad && !relpos_empty(r))) return ZS_ENULL;
     if (!aligned16(workspace) || !aligned_to(grad_table, elem_bytes(r->table_dtype)))
         return ZS_EALIGN;
-    if (!relpos_grad_shape(&a)) return ZS_EUNSUPPORTED;
-    if (workspace_bytes < static_cast<size_t>(relpos_parts_bytes(a))) return ZS_EWORKSPACE;
+    if (!relpos_grad_shape(&a, grad_scores != nullptr)) return ZS_EUNSUPPORTED;
+    // (what zs_relpos_workspace_bytes asks for: enough with and without grad_scores)
+    if (workspace_bytes < zs_relpos_workspace_bytes(r)) return ZS_EWORKSPACE;
     a.table_grad = grad_table;
     a.parts = static_cast<float*>(workspace);
     a.accumulate = accumulate ? 1 : 0;

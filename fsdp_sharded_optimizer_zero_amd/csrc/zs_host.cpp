@@ -406,7 +406,7 @@ bool relpos_bias_shape(RelposArgs* a)
     return a->blocks <= INT32_MAX / kRelposWaves;
 }
 
-bool relpos_grad_shape(RelposArgs* a)
+bool relpos_grad_shape(RelposArgs* a, bool scores)
 {
     const int64_t n = a->f32 ? 4 : 8;
     a->lane_shift = 3;
@@ -415,7 +415,8 @@ bool relpos_grad_shape(RelposArgs* a)
     a->col_tiles = (a->keys + lanes * n - 1) / (lanes * n);
     const int64_t planes = a->batch * a->heads;
     // a multiple of 8 rows: two batches of the kernel's
-    int64_t rows = kRelposRows / groups;
+    int64_t rows = (scores ? kRelposScoreRows : kRelposRows) / groups;
+    if (rows < 8) rows = 8;
     const auto row_tiles = [&] { return (a->queries + rows * groups - 1) / (rows * groups); };
     while (rows > 8 && planes * a->col_tiles * row_tiles() < kRelposGradTiles) rows /= 2;
     a->rows = static_cast<int32_t>(rows);
@@ -538,8 +539,12 @@ size_t zs_relpos_workspace_bytes(const zs_relpos* r)
     a.keys = r->keys;
     a.buckets = r->buckets;
     a.f32 = r->dtype == ZS_F32;
-    if (!zs::relpos_grad_shape(&a)) return 0;
-    return static_cast<size_t>(zs::relpos_parts_bytes(a));
+    // enough for either: with the scores' gradient and without
+    if (!zs::relpos_grad_shape(&a, false)) return 0;
+    const int64_t alone = zs::relpos_parts_bytes(a);
+    if (!zs::relpos_grad_shape(&a, true)) return 0;
+    const int64_t both = zs::relpos_parts_bytes(a);
+    return static_cast<size_t>(alone > both ? alone : both);
 }
 
 size_t zs_distill_workspace_bytes(const zs_distill* d)

@@ -338,13 +338,17 @@ int check_tensors(const zs_tensors* t);
 // ---- the position-bias table (zs_relpos.hip) ---------------------------------------
 
 constexpr int kRelposThreads = 256;
-constexpr int kRelposRows = 128;            // of a gradient's tile, at most
+// Rows of a gradient's tile, at most: 64, and 16 where the scores' gradient is
+// written too (34 heads, 928 x 10308 bf16, both: 273 us, with 32 293, 64 317, 128 344;
+// 8 x 16 x 2048 x 2048, the table's alone: 64 167, 32 172, 16 182, 128 168).
+constexpr int kRelposRows = 64;
+constexpr int kRelposScoreRows = 16;
 constexpr int kRelposLaneRows = 4;          // of the bias a lane has, and for one
 constexpr int kRelposLaneVectors = 4;       // query vectors, from so many tiles on
 constexpr int64_t kRelposManyTiles = 8192;
-// Waves a gradient is cut into, if its rows allow it: as many as the GPU holds
-// (8 of 4 SIMDs of 256 CUs).
-constexpr int64_t kRelposGradTiles = 8192;
+// Waves a gradient is cut into by shorter tiles, if its rows allow it: 2 for each
+// SIMD (28 x 29 x 120 x 198: 17.8 us, with 4096 waves and more 20.8, 1024 19.8).
+constexpr int64_t kRelposGradTiles = 2048;
 // From so many bytes of scores on, loads bypass the caches' reuse (gradient of 1.07
 // GB: 168 us and 193, 403 MB 66 and 79; bias onto 201 MB 62 and 78, 100 MB 37 and
 // 32; both scores' gradients of 100 MB 45 and 43).
@@ -384,7 +388,7 @@ struct RelposArgs {
 // How a call cuts its work (fills the tile fields); false where the tiles are
 // more than 31 bits number.
 bool relpos_bias_shape(RelposArgs* a);
-bool relpos_grad_shape(RelposArgs* a);
+bool relpos_grad_shape(RelposArgs* a, bool scores);
 // The bucket fields from r.
 void relpos_buckets(const zs_relpos* r, RelposArgs* a);
 int64_t relpos_parts_bytes(const RelposArgs& a);

@@ -557,7 +557,7 @@ int relpos_bias(const zs_relpos* r, const void* table, const void* scores,
                 const void* key_lengths, const void* query_starts, void* out, void* stream);
 
 /* Bytes of device workspace relpos_bias_grad needs: a row of buckets (fp32) for
- * every four tiles of the scores (8 to 128 rows of up to 512 keys in bf16, 256 in
+ * every four tiles of the scores (8 to 64 rows of up to 512 keys in bf16, 256 in
  * fp32), rounded up to 256.  0 for a NULL or invalid r, and above 2^31 tiles.
  * Host only. */
 size_t zs_relpos_workspace_bytes(const zs_relpos* r);
