@@ -273,8 +273,8 @@ __device__ __forceinline__ void buckets_of(const RelposArgs& a, const int32_t* e
 // lane 199, eight 184; diagonals built once in LDS for 16 rows and more 202-260).
 // In the plain order of blocks 187 us, and rows that begin anywhere cost more (a
 // fill 2 bytes off 211 us, in this order 153).  Waves and not blocks have tiles, so
-// that a row's last few keys cost a wave (48 x 1024 x 2051: 37 us, with tiles of
-// 256 lanes 53; 2048 keys 33).
+// that a row's last few keys cost a wave (48 x 1024 x 2051: 35 us, with tiles of
+// 256 lanes 53; 2048 keys 34).
 // V > 1, for one query: vectors a tile's lanes apart (64 x 16 x 1 x 8192 onto
 // scores: 12 us, one vector a lane 13; but 32 x 4099 alone 5.2 us and 4.4).
 template <typename T, typename TT, bool SCORES, bool NT, int R, int V>
@@ -305,11 +305,20 @@ __global__ void __launch_bounds__(kThreads) k_relpos_bias(RelposArgs a, int64_t 
     int limit[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) limit[r] = row_limit(a, s, i0 + r);
+    // the row's last vector ends with the row, and repeats places of the one before:
+    // both write the same bits (18 x 22 x 4044 x 22 fp32 onto scores 64 us; moved down
+    // and stored element by element 78).  In place the other may have written them
+    // already.
+    const bool apart = a.in != a.out && keys >= N;
+    const auto vector_at = [&](int v) {
+        const int j = j0 + v * step;
+        return apart && j < keys && j + N > keys ? keys - N : j;
+    };
     Row<T> x[V][R];
     if constexpr (SCORES) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const Span<T> span(j0 + v * step, keys);
+            const Span<T> span(vector_at(v), keys);
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 if (r < rows && span.j < limit[r]) x[v][r] = span.template load<NT>(in + r * a.in_pitch[2]);
@@ -319,9 +328,9 @@ __global__ void __launch_bounds__(kThreads) k_relpos_bias(RelposArgs a, int64_t 
     constexpr int W = N + R - 1;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const Span<T> span(j0 + v * step, keys);
+        if (j0 + v * step >= keys) continue;
+        const Span<T> span(vector_at(v), keys);
         const int j = span.j;
-        if (j >= keys) continue;
         // w[k - r + R - 1]: the bias of place (i0 + r, j + k)
         float w[W];
         const int d0 = j - i0 - s.start - (R - 1);
@@ -391,8 +400,8 @@ __device__ __forceinline__ float from_below(float x)
 // get nothing more from this lane and pass to the lane to the right, which meets
 // them N rows later.  So each diagonal's sum leaves the wave once, at its right
 // edge or below its last row, into LDS, where it is added to its bucket.  Bound
-// by HBM: 8 x 16 x 2048 x 2048 bf16 in 168 us, 6.4 TB/s, 606 MB of them seen in
-// sequences of 0 to 2048 keys 118 (with the diagonals added to LDS every N rows
+// by HBM: 8 x 16 x 2048 x 2048 bf16 in 165 us, 6.5 TB/s, 606 MB of them seen in
+// sequences of 0 to 2048 keys 112 (with the diagonals added to LDS every N rows
 // 486 and 428; all of a bucket's diagonals by the whole wave, one bucket after the
 // other, 20 us more a call).  The two loads of kBatch rows in turn keep one under way; 8
 // rows loaded, then summed, 187 us; what is said of a row is worked out for all
@@ -439,7 +448,6 @@ __global__ void __launch_bounds__(kThreads) k_relpos_grad(RelposArgs a, int64_t 
             return n < 0 ? 0 : n < N ? n : N;
         };
         const int fixed = seen(0);
-        const bool odd = span.shift > 0 || fixed < N;
         const T* next = in;
         // VARIES: rows see different numbers of keys, or are not there
         const auto load = [&](auto varies, Row<T>(&x)[kBatch], int r0) {
@@ -457,10 +465,9 @@ __global__ void __launch_bounds__(kThreads) k_relpos_grad(RelposArgs a, int64_t 
 #pragma unroll
             for (int r = 0; r < kBatch; ++r) {
                 const int n = varies ? seen(r0 + r) : fixed;
-                if (varies || odd) {
-                    span.align(x[r]);
-                    if (n < N) x[r].keep(n);
-                }
+                // the places that this lane has and sees, the others 0
+                span.align(x[r]);
+                if (n < N) x[r].keep(n);
                 if constexpr (SCORES) {
                     if ((!varies || i0 + r0 + r < queries) && j < keys) {
                         float v[N];
