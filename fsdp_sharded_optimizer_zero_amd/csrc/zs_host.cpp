@@ -272,6 +272,21 @@ Cut cut_tensor(const zs_tensor& t, int64_t chunk_bytes)
 
 }  // namespace
 
+// Whether an output has no two places in one: by size of their pitches, each
+// dimension steps over all that the smaller ones take.
+static bool places_apart(const int64_t pitch[3], const int64_t n[3], int64_t keys)
+{
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int a, int b) { return pitch[a] < pitch[b]; });
+    int64_t span = keys;
+    for (int k : order) {
+        if (n[k] < 2) continue;
+        if (pitch[k] < span) return false;
+        span += (n[k] - 1) * pitch[k];      // (n pitch is at most 2^56)
+    }
+    return true;
+}
+
 int check_relpos(const zs_relpos* r)
 {
     if (!r) return ZS_ENULL;
@@ -293,6 +308,7 @@ int check_relpos(const zs_relpos* r)
             r->in_pitch[k] > most / n[k] || r->out_pitch[k] > most / n[k])
             return ZS_EINVAL_RELPOS;
     }
+    if (!empty && !places_apart(r->out_pitch, n, r->keys)) return ZS_EINVAL_RELPOS;
     if (r->table_pitch < r->heads || r->table_pitch > most) return ZS_EINVAL_RELPOS;
     if (r->query_start < -far || r->query_start > far) return ZS_EINVAL_RELPOS;
     if ((r->bidirectional != 0 && r->bidirectional != 1) || (r->causal != 0 && r->causal != 1))

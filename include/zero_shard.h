@@ -526,9 +526,10 @@ int distill_loss_grad(const zs_distill* d, const void* logits, const zs_targets*
 typedef struct zs_relpos {
     int64_t batch, heads, queries, keys;   /* B, Q, K >= 0, 1 <= H <= 65536 */
     int64_t in_pitch[3];   /* scores or gradient: elements from one sequence, head,
-                              query to the next (a pitch of a dimension of one is
-                              not looked at); keys are adjacent */
-    int64_t out_pitch[3];  /* the same of the output */
+                              query to the next, >= K (a pitch of a dimension of one
+                              is not looked at); keys are adjacent */
+    int64_t out_pitch[3];  /* the same of the output, of which no two places are one:
+                              each pitch is past what the smaller ones span */
     int64_t table_pitch;   /* elements from one bucket's row to the next, >= heads */
     int64_t query_start;   /* position of query 0, key 0 being at 0 */
     int64_t max_distance;  /* from here on a distance is in its side's last bucket;

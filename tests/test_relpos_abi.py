@@ -57,6 +57,24 @@ def test_struct_is_refused(bad):
 
 
 @no_gpu
+@pytest.mark.parametrize("pitch", [(800, 20, 20), (800, 190, 20), (200, 200, 20), (781, 200, 20),
+                                   (20, 20, 20), (799, 20, 80)])
+def test_output_over_itself_is_refused(pitch):
+    # heads, then sequences, that begin before the smaller dimensions end
+    r = relpos(out_pitch=pitch)
+    assert bias(r) == Z.ZS_EINVAL_RELPOS
+    assert grad(r, scores=FAKE, nbytes=1 << 60) == Z.ZS_EINVAL_RELPOS
+
+
+@no_gpu
+@pytest.mark.parametrize("pitch", [(800, 200, 20), (800, 20, 80), (200, 600, 20), (20, 600, 60),
+                                   (80, 20, 240), (20, 60, 240), (960, 240, 24)])
+def test_output_in_any_order_is_taken(pitch):
+    # told by the next check: a table that is not there
+    assert bias(relpos(out_pitch=pitch), table=None) == Z.ZS_ENULL
+
+
+@no_gpu
 def test_pointers_are_refused():
     r = relpos()
     assert bias(None) == Z.ZS_ENULL and grad(None, nbytes=0) == Z.ZS_ENULL
