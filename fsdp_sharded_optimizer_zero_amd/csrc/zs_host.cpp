@@ -435,6 +435,10 @@ bool relpos_grad_shape(RelposArgs* a, bool scores)
     if (rows < 8) rows = 8;
     const auto row_tiles = [&] { return (a->queries + rows * groups - 1) / (rows * groups); };
     while (rows > 8 && planes * a->col_tiles * row_tiles() < kRelposGradTiles) rows /= 2;
+    // so many tiles, of rows as near alike as multiples of 8 are (8 x 32 heads, 8 x
+    // 4096 bf16: 8.7 us, with 64 rows 21.6; 65 x 4096 29 us and 35)
+    const int64_t tall = groups * std::max<int64_t>(row_tiles(), 1);
+    rows = std::max<int64_t>(round_up((a->queries + tall - 1) / tall, 8), 8);
     a->rows = static_cast<int32_t>(rows);
     a->row_tiles = row_tiles();
     a->plane_blocks = (a->row_tiles * a->col_tiles + kRelposWaves - 1) / kRelposWaves;
