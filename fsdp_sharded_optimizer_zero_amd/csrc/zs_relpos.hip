@@ -195,6 +195,36 @@ struct Row<float> {
     }
 };
 
+// The first n of v, fewer than all, in at most three stores.
+__device__ __forceinline__ void store_part(uint16_t* p, const float (&v)[8], int n)
+{
+    typedef uint32_t u32_u __attribute__((aligned(2)));
+    uint32_t a = pack_bf16x2(v[0], v[1]), b = pack_bf16x2(v[2], v[3]);
+    if (n & 4) {
+        *reinterpret_cast<u32x2_u*>(p) = u32x2_u{a, b};
+        a = pack_bf16x2(v[4], v[5]);
+        b = pack_bf16x2(v[6], v[7]);
+        p += 4;
+    }
+    if (n & 2) {
+        *reinterpret_cast<u32_u*>(p) = a;
+        a = b;
+        p += 2;
+    }
+    if (n & 1) *p = static_cast<uint16_t>(a);
+}
+__device__ __forceinline__ void store_part(float* p, const float (&v)[4], int n)
+{
+    typedef float f32x2_u __attribute__((ext_vector_type(2), aligned(4)));
+    float a = v[0];
+    if (n & 2) {
+        *reinterpret_cast<f32x2_u*>(p) = f32x2_u{v[0], v[1]};
+        a = v[2];
+        p += 2;
+    }
+    if (n & 1) *p = a;
+}
+
 // A lane's N places of a row of `keys`, from column j on.  Those that reach
 // past the row are loaded as the row's last N and moved down at use (element by
 // element, a wave waits for each of its rows: 48 x 1024 x 2047 bf16, the gradient
@@ -224,13 +254,8 @@ struct Span {
     }
     __device__ __forceinline__ void store(T* row, const float (&v)[N]) const
     {
-        if (j + N <= keys) {
-            store_n<N>(row + j, v);
-            return;
-        }
-#pragma unroll
-        for (int k = 0; k < N - 1; ++k)
-            if (j + k < keys) put(row + j + k, v[k]);
+        if (j + N <= keys) store_n<N>(row + j, v);
+        else store_part(row + j, v, keys - j);
     }
 };
 
