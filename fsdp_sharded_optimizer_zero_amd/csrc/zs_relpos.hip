@@ -433,6 +433,9 @@ __device__ __forceinline__ float from_below(float x)
 // rows at once where they see the same (partly filled tiles are bound by that).
 constexpr int kBatch = 4;
 constexpr int kFewDiagonals = 16;   // of a bucket, up to which one lane sums them
+// Of a tile of several groups, 64 at a time: 32 lanes' keys and its rows.
+template <int N>
+constexpr int kGroupDiagonals = (32 * N + kRelposRows + 63) / 64;
 template <typename T, bool SCORES, bool NT>
 __global__ void __launch_bounds__(kThreads) k_relpos_grad(RelposArgs a, int64_t b0)
 {
@@ -548,20 +551,35 @@ __global__ void __launch_bounds__(kThreads) k_relpos_grad(RelposArgs a, int64_t 
         pass(a.rows, true);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    // the groups' diagonals to the tile's: group g's are (groups - 1 - g) * rows on
+    const int last = pitch - 1 + (groups - 1) * a.rows;     // diagonals 1..last
+    if (here && groups > 1) {
+        float q[kGroupDiagonals<N>];
+#pragma unroll
+        for (int k = 0; k < kGroupDiagonals<N>; ++k) {
+            q[k] = 0.0f;
+            for (int g = 0; g < groups; ++g) {
+                const int x = lane + 64 * k - (groups - 1 - g) * a.rows;
+                if (x >= 1 && x < pitch) q[k] += mine[g * pitch + x];
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int k = 0; k < kGroupDiagonals<N>; ++k)
+            if (lane + 64 * k <= last) mine[lane + 64 * k] = q[k];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
     // the diagonals' sums to buckets, a bucket a lane; the last of each side, which
-    // may have most of the diagonals, by all lanes
-    const int last = pitch - 1;                     // diagonals 1..last
+    // may have most of the diagonals, by all lanes.  mine[x] is of d = x + d0
+    const int d0 = ct * lanes * N - ((rt + 1) * groups * a.rows + s.start);
     for (int u0 = 0; u0 < a.buckets; u0 += 64) {
         const int u = u0 + lane;
-        // its distances, as places of diagonals: d from lo to hi
-        int lo = 1, hi = 0;
-        if (here && u < a.buckets) bucket_range(a, u, lo, hi);
-        const bool wide = static_cast<int64_t>(hi) - lo >= kFewDiagonals;
         float total = 0.0f;
-        for (int g = 0; here && g < groups; ++g) {
-            const float* from = mine + g * pitch;
-            // from[x] is of d = x + d0
-            const int d0 = ct * lanes * N - ((rt * groups + g) * a.rows + s.start) - a.rows;
+        if (here) {
+            // its distances, as places of diagonals: d from lo to hi
+            int lo = 1, hi = 0;
+            if (u < a.buckets) bucket_range(a, u, lo, hi);
+            const bool wide = static_cast<int64_t>(hi) - lo >= kFewDiagonals;
             // (in 64 bits: distances may be 2^30, and a range all of them)
             const int64_t begin64 = static_cast<int64_t>(lo) - d0, end64 = static_cast<int64_t>(hi) - d0;
             const int x0 = begin64 < 1 ? 1 : begin64 > last ? last + 1 : static_cast<int>(begin64);
@@ -570,7 +588,7 @@ __global__ void __launch_bounds__(kThreads) k_relpos_grad(RelposArgs a, int64_t 
                 for (int x = x0; x <= x1; x += 4) {
                     float q[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) q[k] = from[x + k <= x1 ? x + k : x];
+                    for (int k = 0; k < 4; ++k) q[k] = mine[x + k <= x1 ? x + k : x];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) total += x + k <= x1 ? q[k] : 0.0f;
                 }
@@ -581,7 +599,7 @@ __global__ void __launch_bounds__(kThreads) k_relpos_grad(RelposArgs a, int64_t 
                 many &= many - 1;
                 const int begin = __builtin_amdgcn_readlane(x0, k), end = __builtin_amdgcn_readlane(x1, k);
                 float q = 0.0f;
-                for (int x = begin + lane; x <= end; x += 64) q += from[x];
+                for (int x = begin + lane; x <= end; x += 64) q += mine[x];
                 q = wave_sum(q);
                 if (lane == k) total += q;
             }
