@@ -406,6 +406,16 @@ bool relpos_bias_shape(RelposArgs* a)
     const int64_t n = a->f32 ? 4 : 8;
     a->lane_shift = 3;
     while (a->lane_shift < 6 && (n << a->lane_shift) < a->keys) ++a->lane_shift;
+    // Of a bias alone: 32 lanes a row where that leaves out a sixth of the columns that
+    // tiles of 64 cover (13 x 44 x 943 x 539 bf16: 122 us, with 64 132), or 16 for rows
+    // of one tile (300 x 280: 27 us, with 64 36; longer ones lose, 300 x 1067 82 and
+    // 75, and so does a bias onto scores, 300 x 380: 57 and 49).
+    const auto covers = [&](int shift) { return round_up(a->keys, n << shift); };
+    const int most = a->lane_shift;
+    for (int shift = 5; !a->in && most == 6 && shift >= (a->keys <= n << 6 ? 4 : 5); --shift)
+        if (a->queries >= (kRelposLaneRows * int64_t(64) >> shift) &&
+            covers(shift) * 6 < covers(a->lane_shift) * 5)
+            a->lane_shift = shift;
     const int64_t lanes = int64_t(1) << a->lane_shift, groups = 64 / lanes;
     const int64_t planes = a->batch * a->heads;
     a->col_tiles = (a->keys + lanes * n - 1) / (lanes * n);
