@@ -557,16 +557,19 @@ int set_sqnorm(double* sqnorm_out, double* tensor_sqnorms, int32_t accumulate, T
 int set_clip(const zs_tensors* t, double max_norm, const double* sqnorm, double other_sqnorm,
              TensorsArgs* a)
 {
-    if (!(max_norm > 0.0 && max_norm <= 1.7976931348623157e308) || other_sqnorm < 0.0)
+    constexpr double kLargest = 1.7976931348623157e308;     // of the finite ones
+    if (!(max_norm > 0.0 && max_norm <= kLargest) || other_sqnorm < 0.0)
         return ZS_EINVAL_HPARAM;
     if (!sqnorm || !t->has_out) return ZS_ENULL;
     if (!aligned8(sqnorm)) return ZS_EALIGN;
     a->sqnorm = sqnorm;
     a->other = other_sqnorm;
     a->max_norm = max_norm;
-    // sqrt(Q) + 1e-6 <= max_norm, with room for the roundings on both sides
+    // sqrt(Q) + 1e-6 <= max_norm, with room for the roundings on both sides; an
+    // infinite Q, whose coefficient is 0, is above it whatever the limit
     const double most = max_norm - 1e-6;
-    a->quiet = t->has_out == 2 && most > 0.0 ? most * most * (1.0 - 1e-9) : -HUGE_VAL;
+    a->quiet = t->has_out == 2 && most > 0.0 ? std::fmin(most * most * (1.0 - 1e-9), kLargest)
+                                             : -HUGE_VAL;
     return ZS_OK;
 }
 

@@ -379,3 +379,29 @@ def test_a_list_outlives_the_callers_names():
     q = scalar()
     Z.tensors_sqnorm(T, q)
     assert abs(float(q) - want) <= REL * want
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("max_norm", [1e150, 1.5e154, 1e300, 1.7976931348623157e308])
+def test_an_infinite_norm_is_past_every_limit(dtype, max_norm):
+    """In place, also with limits whose square is not finite: a list with an
+    infinite element is clipped by 0, one without stays as it is."""
+    fine = make([300, 20000, 7], (dtype,), seed=9)
+    bits = [t.clone() for t in fine]
+    q = scalar()
+    Z.tensors_clip_norm(Z.make_tensors(fine), max_norm, q)
+    assert all(torch.equal(a, b) for a, b in zip(fine, bits))
+    # another rank's norm
+    T = Z.make_tensors(fine)
+    Z.tensors_clip(T, max_norm, q, other_sqnorm=math.inf)
+    assert all(bool((t == 0).all()) for t in fine)
+    tensors = make([300, 20000, 7], (dtype,), seed=9)
+    tensors[1][-1] = math.inf
+    outs = [torch.empty_like(t) for t in tensors]
+    Z.tensors_clip_norm(Z.make_tensors(tensors, outs), max_norm, q)
+    Z.tensors_clip_norm(Z.make_tensors(tensors), max_norm, q)
+    assert float(q) == math.inf
+    for k, (t, o) in enumerate(zip(tensors, outs)):
+        assert same(t, o)
+        assert bool((t.nan_to_num(nan=0.0) == 0).all())
+        assert int(t.isnan().sum()) == (k == 1)
