@@ -511,8 +511,10 @@ extern "C" int relpos_bias_grad(const zs_relpos* r, const void* grad, const void
     if (!aligned16(workspace) || !aligned_to(grad_table, elem_bytes(r->table_dtype)))
         return ZS_EALIGN;
     if (!relpos_grad_shape(&a, grad_scores != nullptr)) return ZS_EUNSUPPORTED;
-    // (what zs_relpos_workspace_bytes asks for: enough with and without grad_scores)
-    if (workspace_bytes < zs_relpos_workspace_bytes(r)) return ZS_EWORKSPACE;
+    // enough with and without grad_scores; 0: too many tiles in one of the two
+    const size_t need = zs_relpos_workspace_bytes(r);
+    if (need == 0) return ZS_EUNSUPPORTED;
+    if (workspace_bytes < need) return ZS_EWORKSPACE;
     a.table_grad = grad_table;
     a.parts = static_cast<float*>(workspace);
     a.accumulate = accumulate ? 1 : 0;

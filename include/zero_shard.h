@@ -559,8 +559,9 @@ int relpos_bias(const zs_relpos* r, const void* table, const void* scores,
 
 /* Bytes of device workspace relpos_bias_grad needs: a row of buckets (fp32) for
  * every four tiles of the scores (8 to 64 rows of up to 512 keys in bf16, 256 in
- * fp32), rounded up to 256.  0 for a NULL or invalid r, and above 2^31 tiles.
- * Host only. */
+ * fp32), rounded up to 256; enough with grad_scores and without.  0 for a NULL or
+ * invalid r, and where either has more than 2^31 tiles (relpos_bias_grad:
+ * ZS_EUNSUPPORTED).  Host only. */
 size_t zs_relpos_workspace_bytes(const zs_relpos* r);
 
 /* The gradient of relpos_bias.  With g = grad[b,h,i,j] (in_pitch):

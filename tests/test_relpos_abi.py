@@ -104,6 +104,18 @@ def test_too_many_tiles_are_refused():
 
 
 @no_gpu
+@pytest.mark.parametrize("nbytes", [0, 16, 1 << 60])
+def test_no_workspace_size_is_refused(nbytes):
+    """Where the scores' gradient would take too many tiles there is no size of the
+    workspace, for the table's gradient alone neither (2^30 tiles here, in blocks of
+    four, and 2^31 with the scores')."""
+    r = Z.make_relpos(16384, 129, 33, batch=16384, dtype=Z.ZS_F32)
+    assert Z.zs_relpos_workspace_bytes(r) == 0
+    assert grad(r, nbytes=nbytes) == Z.ZS_EUNSUPPORTED
+    assert grad(r, scores=2 * FAKE, nbytes=nbytes) == Z.ZS_EUNSUPPORTED
+
+
+@no_gpu
 @pytest.mark.parametrize("empty", [dict(batch=0), dict(queries=0), dict(keys=0)])
 def test_no_places_is_no_launch(empty):
     assert bias(relpos(**empty), table=None, out=None) == Z.ZS_OK
