@@ -316,6 +316,9 @@ class TableRun:
     all-reduce's stand-in), their squared norm is added to the shards', and the
     same coefficient clips them into the flat fp32 gradient of their own step:
             tensors_sqnorm(accumulate), tensors_clip, zero_shard_step (stage 0)
+
+    max_grad_norm: the global norm's limit; <= 0: no clip, of shards and whole
+    parameters alike.
     """
 
     def __init__(self, rows: int, dim: int, n_d: int, tokens: int, k: int, scale: float = 1.0,
@@ -447,7 +450,11 @@ class TableRun:
             for r in range(self.n_d):
                 g.add_(self.rank_grads[r][k].float(), alpha=valid[r] / total)
         tensors_sqnorm(self.whole_list, self.sqnorm, accumulate=True)
-        tensors_clip(self.whole_list, self.max_grad_norm, self.sqnorm)
+        if self.max_grad_norm > 0.0:
+            tensors_clip(self.whole_list, self.max_grad_norm, self.sqnorm)
+        else:                                   # no clip, as in zero_shard_step
+            for flat, g in zip(self.whole_list.out, self.whole_grads):
+                flat.copy_(g)
 
     def step(self, t: int, batches):
         """One optimizer step at bias-correction step t from one batch a rank."""

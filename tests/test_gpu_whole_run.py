@@ -138,3 +138,27 @@ def test_relpos_function_gradients():
     assert alone.shape == (2, 3, 13, 13)
     once = torch.autograd.grad(alone[torch.isfinite(alone)].sum(), table)[0]
     assert torch.equal(once.sum(0), torch.full((3,), 2.0 * 91, device="cuda"))
+
+
+@pytest.mark.parametrize("none", [0.0, -1.0])
+def test_step_without_a_clip(none):
+    """max_grad_norm <= 0 is no clip: the same bits as a limit that is not reached."""
+    n_d, rows, dim, k, heads = 2, 90, 24, 5, 4
+    seqs, length = 4, 17
+    runs = []
+    for max_norm in (none, 1e6):
+        g = torch.Generator().manual_seed(1)
+        whole = [torch.randn((8, heads), generator=g) * 0.3, torch.ones(dim)]
+        run = TableRun(rows, dim, n_d, seqs * length, k, alpha=0.6, body=Mixer(seqs, length, heads),
+                       whole=whole, max_grad_norm=max_norm)
+        run.load((torch.randn((rows, dim), generator=g) * 0.3).cuda())
+        for t in (1, 2):
+            run.step(t, [make_batch(seqs * length, rows, k, 10 * t + r) for r in range(n_d)])
+            flat = torch.cat([x.reshape(-1) for x in run.whole_grads])
+            assert torch.equal(run.whole_mean[:len(flat)], flat) and bool((flat != 0).any())
+        runs.append(run)
+    a, b = runs
+    assert torch.equal(a.sqnorm, b.sqnorm) and torch.equal(a.gather, b.gather)
+    assert torch.equal(a.whole_gather, b.whole_gather)
+    for x, y in zip([a.whole_state, *a.state], [b.whole_state, *b.state]):
+        assert all(torch.equal(u, v) for u, v in zip(x, y))
