@@ -310,11 +310,12 @@ class TableRun:
     body: a differentiable function of the hidden states [T, dim] that stands
     for the model between the two uses of the table; None: the identity.
 
-    whole: parameters of body (fp32 initial values; body is called with their
-    bf16 copies behind the hidden states) that every rank keeps whole.  Their
-    gradients, tensor by tensor, are averaged over the ranks by valid tokens (the
-    all-reduce's stand-in), their squared norm is added to the shards', and the
-    same coefficient clips them into the flat fp32 gradient of their own step:
+    whole: parameters of body (fp32 initial values; body is required then, and is
+    called with their bf16 copies behind the hidden states) that every rank keeps
+    whole.  Their gradients, tensor by tensor, are averaged over the ranks by valid
+    tokens (the all-reduce's stand-in), their squared norm is added to the shards',
+    and the same coefficient clips them into the flat fp32 gradient of their own
+    step:
             tensors_sqnorm(accumulate), tensors_clip, zero_shard_step (stage 0)
 
     max_grad_norm: the global norm's limit; <= 0: no clip, of shards and whole
@@ -325,6 +326,9 @@ class TableRun:
                  temperature: float = 1.0, alpha: float = 1.0, f32_grads: bool = True, body=None,
                  lr: float = 1e-3, weight_decay: float = 0.01, max_grad_norm: float = 1.0,
                  whole=(), device: str = "cuda"):
+        whole = list(whole)
+        if whole and body is None:
+            raise ValueError("whole parameters are the body's: a body is required")
         self.rows, self.dim, self.n_d, self.tokens = rows, dim, n_d, tokens
         self.body, self.f32_grads = body, f32_grads
         self.lr, self.weight_decay, self.max_grad_norm = lr, weight_decay, max_grad_norm
@@ -358,7 +362,7 @@ class TableRun:
 
         self.whole = []
         if whole:
-            self._keep_whole(list(whole), device)
+            self._keep_whole(whole, device)
 
     def _keep_whole(self, values, device):
         numel = [v.numel() for v in values]
