@@ -264,7 +264,9 @@ class RelposBias(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         table, key_lengths, query_starts = ctx.saved_tensors
-        dtable = torch.empty(table.shape, dtype=table.dtype, device=table.device)
+        # the call writes its rows of buckets and columns of heads alone
+        full = table.numel() == ctx.r.buckets * ctx.r.heads
+        dtable = (torch.empty if full else torch.zeros)(table.shape, dtype=table.dtype, device=table.device)
         dscores = torch.empty_like(grad, memory_format=torch.contiguous_format) \
             if ctx.scores else None
         workspace = torch.empty(zs_relpos_workspace_bytes(ctx.r), dtype=torch.uint8,

@@ -162,3 +162,21 @@ def test_step_without_a_clip(none):
     assert torch.equal(a.whole_gather, b.whole_gather)
     for x, y in zip([a.whole_state, *a.state], [b.whole_state, *b.state]):
         assert all(torch.equal(u, v) for u, v in zip(x, y))
+
+
+@pytest.mark.parametrize("shape,pitch", [((32, 6), 6), ((13, 5), 5), ((75,), 5)])
+def test_relpos_function_gradient_of_unused_entries(shape, pitch):
+    """A table with more rows or columns than the call uses: 0 for those."""
+    r = Z.make_relpos(5, 9, 70, buckets=8, max_distance=20, dtype=Z.ZS_F32, table_pitch=pitch)
+    table = torch.randn(shape, device="cuda", requires_grad=True)
+    out = RelposBias.apply(r, table)
+    # what the next allocations find
+    stale = [torch.full(shape, math.nan, device="cuda") for _ in range(4)]
+    del stale
+    got = torch.autograd.grad(out.sum(), table)[0]
+    assert got.shape == table.shape
+    rows = got.view(-1, pitch)
+    used = torch.zeros_like(rows, dtype=torch.bool)
+    used[:8, :5] = True
+    assert bool((rows[~used] == 0).all())
+    assert torch.equal(rows[:8, :5].sum(0), torch.full((5,), 9.0 * 70, device="cuda"))
