@@ -33,6 +33,7 @@ gradient.
 """
 from __future__ import annotations
 
+import math
 from dataclasses import dataclass
 
 import torch
@@ -243,10 +244,17 @@ class ShardRun:
         return red * self.units, upd * self.units
 
 
+def _room(shape, n, like):
+    """Memory of a gradient of `shape` of which a call writes n elements; others are 0."""
+    make = torch.empty if math.prod(shape) == n else torch.zeros
+    return make(shape, dtype=like.dtype, device=like.device)
+
+
 class RelposBias(torch.autograd.Function):
     """RelposBias.apply(r, table, scores, key_lengths, query_starts): relpos_bias
     of make_relpos's r (pitches without gaps), differentiable in table and
-    scores; scores None: the bias alone, [batch, heads, queries, keys]."""
+    scores; scores None: the bias alone, [batch, heads, queries, keys].  Scores and
+    table may be of any shape relpos_bias takes; gradients are of the same."""
 
     @staticmethod
     def forward(ctx, r, table, scores=None, key_lengths=None, query_starts=None):
@@ -256,7 +264,8 @@ class RelposBias(torch.autograd.Function):
         relpos_bias(r, table.contiguous(), out, None if scores is None else scores.contiguous(),
                     key_lengths, query_starts)
         # the caller may change r before the backward pass
-        ctx.r, ctx.scores = type(r).from_buffer_copy(r), scores is not None and ctx.needs_input_grad[2]
+        ctx.r = type(r).from_buffer_copy(r)
+        ctx.scores = scores.shape if scores is not None and ctx.needs_input_grad[2] else None
         ctx.save_for_backward(table, key_lengths, query_starts)
         return out
 
@@ -264,11 +273,9 @@ class RelposBias(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         table, key_lengths, query_starts = ctx.saved_tensors
-        # the call writes its rows of buckets and columns of heads alone
-        full = table.numel() == ctx.r.buckets * ctx.r.heads
-        dtable = (torch.empty if full else torch.zeros)(table.shape, dtype=table.dtype, device=table.device)
-        dscores = torch.empty_like(grad, memory_format=torch.contiguous_format) \
-            if ctx.scores else None
+        dtable = _room(table.shape, ctx.r.buckets * ctx.r.heads, table)
+        # of the scores' own shape: a flat buffer may be longer than the places
+        dscores = None if ctx.scores is None else _room(ctx.scores, grad.numel(), grad)
         workspace = torch.empty(zs_relpos_workspace_bytes(ctx.r), dtype=torch.uint8,
                                 device=grad.device)
         relpos_bias_grad(ctx.r, grad.contiguous(), dtable, workspace, dscores, key_lengths,

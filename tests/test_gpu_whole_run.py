@@ -180,3 +180,25 @@ def test_relpos_function_gradient_of_unused_entries(shape, pitch):
     used[:8, :5] = True
     assert bool((rows[~used] == 0).all())
     assert torch.equal(rows[:8, :5].sum(0), torch.full((5,), 9.0 * 70, device="cuda"))
+
+
+@pytest.mark.parametrize("extra", [0, 11])
+def test_relpos_function_of_flat_scores(extra):
+    """Scores as a flat buffer, and without the batch of one: the gradient has
+    their shape, 0 behind the places."""
+    r = Z.make_relpos(3, 9, 70, dtype=Z.ZS_F32, scale=0.5)
+    n = 3 * 9 * 70
+    table = torch.randn((32, 3), device="cuda", requires_grad=True)
+    flat = torch.randn(n + extra, device="cuda", requires_grad=True)
+    weight = torch.randn((1, 3, 9, 70), device="cuda")
+    out = RelposBias.apply(r, table, flat)
+    stale = [torch.full((n + extra,), math.nan, device="cuda") for _ in range(4)]
+    del stale
+    got = torch.autograd.grad((out * weight).sum(), flat)[0]
+    assert got.shape == flat.shape and bool((got[n:] == 0).all())
+    assert torch.equal(got[:n], (weight * 0.5).reshape(-1))
+    three = flat.detach()[:n].view(3, 9, 70).requires_grad_()
+    out3 = RelposBias.apply(r, table, three)
+    assert torch.equal(out3, out)
+    got = torch.autograd.grad((out3 * weight).sum(), three)[0]
+    assert torch.equal(got, weight[0] * 0.5)
