@@ -244,10 +244,11 @@ class ShardRun:
         return red * self.units, upd * self.units
 
 
-def _room(shape, n, like):
-    """Memory of a gradient of `shape` of which a call writes n elements; others are 0."""
+def _room(shape, dtype, n, device):
+    """Memory of a gradient of `shape` of which a call writes n elements; others (a
+    table's unused rows, the end of a flat buffer) are 0."""
     make = torch.empty if math.prod(shape) == n else torch.zeros
-    return make(shape, dtype=like.dtype, device=like.device)
+    return make(shape, dtype=dtype, device=device)
 
 
 class RelposBias(torch.autograd.Function):
@@ -266,16 +267,19 @@ class RelposBias(torch.autograd.Function):
         # the caller may change r before the backward pass
         ctx.r = type(r).from_buffer_copy(r)
         ctx.scores = scores.shape if scores is not None and ctx.needs_input_grad[2] else None
-        ctx.save_for_backward(table, key_lengths, query_starts)
+        # of the table the gradient needs no value: it may be written between the passes
+        ctx.table = table.shape, table.dtype
+        ctx.save_for_backward(key_lengths, query_starts)
         return out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
-        table, key_lengths, query_starts = ctx.saved_tensors
-        dtable = _room(table.shape, ctx.r.buckets * ctx.r.heads, table)
-        # of the scores' own shape: a flat buffer may be longer than the places
-        dscores = None if ctx.scores is None else _room(ctx.scores, grad.numel(), grad)
+        key_lengths, query_starts = ctx.saved_tensors
+        dtable = _room(*ctx.table, ctx.r.buckets * ctx.r.heads, grad.device)
+        dscores = None
+        if ctx.scores is not None:
+            dscores = _room(ctx.scores, grad.dtype, grad.numel(), grad.device)
         workspace = torch.empty(zs_relpos_workspace_bytes(ctx.r), dtype=torch.uint8,
                                 device=grad.device)
         relpos_bias_grad(ctx.r, grad.contiguous(), dtable, workspace, dscores, key_lengths,

@@ -202,3 +202,20 @@ def test_relpos_function_of_flat_scores(extra):
     assert torch.equal(out3, out)
     got = torch.autograd.grad((out3 * weight).sum(), three)[0]
     assert torch.equal(got, weight[0] * 0.5)
+
+
+def test_relpos_function_when_the_table_changes():
+    """The gradient does not depend on the table: it may be written between the
+    passes, as an embedding's may.  The lengths are needed and may not."""
+    r = Z.make_relpos(3, 9, 70, batch=2, dtype=Z.ZS_F32)
+    table = torch.randn((32, 3), device="cuda", requires_grad=True)
+    lengths = torch.tensor([70, 20], device="cuda")
+    want = torch.autograd.grad(RelposBias.apply(r, table, None, lengths)[0].sum(), table)[0]
+    out = RelposBias.apply(r, table, None, lengths)
+    with torch.no_grad():
+        table.mul_(2.0)
+    assert torch.equal(torch.autograd.grad(out[0].sum(), table)[0], want)
+    out = RelposBias.apply(r, table, None, lengths)
+    lengths.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        torch.autograd.grad(out[0].sum(), table)
