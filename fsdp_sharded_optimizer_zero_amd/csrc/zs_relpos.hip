@@ -618,8 +618,9 @@ __global__ void __launch_bounds__(kThreads) k_relpos_grad(RelposArgs a, int64_t 
     }
 }
 
-// The table's gradient from the tiles' parts, one block a head: buckets across
-// the lanes, tiles down; summed in fp64 in a fixed order.
+// The table's gradient from the parts of the tiles' blocks (fp32), one block a head:
+// buckets across the lanes, parts down; summed in fp64 in a fixed order.  Rounded to
+// fp32, then to bf16: off by half a step of bf16 and at most half a step of fp32.
 template <typename TT>
 __global__ void __launch_bounds__(kSumThreads) k_relpos_sum(RelposArgs a)
 {

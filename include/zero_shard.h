@@ -572,7 +572,10 @@ size_t zs_relpos_workspace_bytes(const zs_relpos* r);
  *   grad_scores      = scale * g where seen, +0 where not (out_pitch), or NULL;
  *                      may be `grad`, of its pitches.
  * g is not read where it is not seen.  Summed in fp32 along the diagonals of a
- * tile and in fp64 over the tiles, in an order that depends on the sizes alone.
+ * tile, from there to its buckets and over the four tiles of a block, in fp64 over
+ * the blocks; rounded to fp32, then to table_dtype.  The order is fixed by the sizes,
+ * the dtype and whether grad_scores is given (its tiles have fewer rows): the same
+ * call gives the same bits, with grad_scores and without they may differ.
  *   workspace  16-byte aligned, >= zs_relpos_workspace_bytes(r) bytes; contents
  *              on entry are ignored.
  * Errors: ZS_ENULL, ZS_EINVAL_RELPOS, ZS_EALIGN, ZS_EUNSUPPORTED, ZS_EWORKSPACE,
