@@ -461,3 +461,78 @@ def test_ends_of_the_range(start, by_query):
     at = torch.tensor([0, 1, 130, far // 2, far - 131, far - 2, far - 1])
     d = (-at - start) if by_query else (at - start)
     assert torch.equal(flat[at.cuda()].cpu().long(), buckets_of(r, d))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("causal", [False, True])
+def test_scores_past_the_caches(dtype, causal):
+    """Calls large enough for loads past the caches' reuse, rows of an odd length,
+    against one call a sequence, which are not; in place too.  A place's bias and
+    its scores' gradient do not depend on how a call is cut; gradients of -1, 0
+    and 1 are summed exactly in any order (2.1 million places a plane, 10.6 million
+    a head: below 2^24)."""
+    b, h, q, k = 5, 8, 1031, 2053
+    kw = dict(dtype=KIND[dtype], causal=causal, query_start=900 if causal else 0, scale=0.5,
+              bidirectional=not causal)
+    r, one = Z.make_relpos(h, q, k, batch=b, **kw), Z.make_relpos(h, q, k, **kw)
+    limit = 160 << 20
+    assert h * q * k * (2 if dtype == BF16 else 4) < limit <= b * h * q * k * 2
+    x, table = data(r, dtype, 11)
+    lengths = torch.tensor([k, 2048, 700, 0, 1], device="cuda")
+    want = torch.empty_like(x)
+    for i in range(b):
+        Z.relpos_bias(one, table, want[i:i + 1], scores=x[i:i + 1], key_lengths=lengths[i:i + 1])
+    out = torch.empty_like(x)
+    Z.relpos_bias(r, table, out, scores=x, key_lengths=lengths)
+    assert torch.equal(out, want)
+    out.copy_(x)
+    Z.relpos_bias(r, table, out, scores=out, key_lengths=lengths)
+    assert torch.equal(out, want)
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x = torch.randint(-1, 2, x.shape, generator=g, device="cuda", dtype=torch.int8).to(dtype)
+    ws = torch.empty(Z.zs_relpos_workspace_bytes(r), dtype=torch.uint8, device="cuda")
+    dt = torch.zeros((32, h), device="cuda")
+    for i in range(b):
+        Z.relpos_bias_grad(one, x[i:i + 1], dt, ws, want[i:i + 1], lengths[i:i + 1],
+                           accumulate=True)
+    assert bool((dt != 0).any()) and float(dt.abs().max()) < 2.0 ** 24
+    for place in (None, out, x):
+        got = torch.full_like(dt, math.nan)
+        Z.relpos_bias_grad(r, x, got, ws, place, lengths)
+        assert torch.equal(got, dt)
+        if place is not None:
+            assert torch.equal(place, want)
+
+
+@pytest.mark.parametrize("dtype,keys", [(BF16, 82003), (F32, 41001)])
+def test_one_token_a_sequence_past_the_caches(dtype, keys):
+    """The same for one query, four vectors a lane."""
+    b, h = 64, 16
+    kw = dict(dtype=KIND[dtype], scale=0.5, bidirectional=False, causal=True)
+    r, one = Z.make_relpos(h, 1, keys, batch=b, **kw), Z.make_relpos(h, 1, keys, **kw)
+    x, table = data(r, dtype, 13)
+    assert x.numel() * x.element_size() >= 160 << 20
+    starts = torch.randint(0, keys, (b,), generator=torch.Generator().manual_seed(14)).cuda()
+    starts[0], starts[1] = 0, keys - 1
+    lengths = starts + 1
+    want, out = torch.empty_like(x), torch.empty_like(x)
+    for i in range(b):
+        Z.relpos_bias(one, table, want[i:i + 1], scores=x[i:i + 1], key_lengths=lengths[i:i + 1],
+                      query_starts=starts[i:i + 1])
+    Z.relpos_bias(r, table, out, scores=x, key_lengths=lengths, query_starts=starts)
+    assert torch.equal(out, want)
+    Z.relpos_bias(r, table, x, scores=x, key_lengths=lengths, query_starts=starts)
+    assert torch.equal(x, want)
+
+
+def test_one_token_a_sequence_fp32():
+    """Four vectors a lane in fp32 (more than 8192 tiles), onto scores and alone."""
+    r = Z.make_relpos(33, 1, 2101, batch=65, dtype=Z.ZS_F32, bidirectional=False, scale=0.125)
+    starts = torch.randint(0, 2101, (65,), generator=torch.Generator().manual_seed(1))
+    lengths, starts = (starts + 1).cuda(), starts.cuda()
+    check(r, F32, lengths=lengths, starts=starts, seed=2, grads=False)
+    x, table = data(r, F32, 2)
+    want = torch.empty_like(x)
+    Z.relpos_bias(r, table, want, scores=x, key_lengths=lengths, query_starts=starts)
+    Z.relpos_bias(r, table, x, scores=x, key_lengths=lengths, query_starts=starts)
+    assert torch.equal(x, want)
