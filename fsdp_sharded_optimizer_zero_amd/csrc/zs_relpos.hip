@@ -660,12 +660,20 @@ __global__ void __launch_bounds__(kSumThreads) k_relpos_sum(RelposArgs a)
 template <typename T, typename TT, bool SCORES, bool NT>
 void bias_launch(const RelposArgs& a, int64_t b0, uint32_t n, hipStream_t st)
 {
-    if (a.lane_vectors > 1)
+    // one query past the caches is in tiles (of 64 lanes' vectors at most) enough for
+    // kRelposLaneVectors
+    static_assert(kRelposManyTiles * 64 * 16 <= kRelposNt, "NT with one vector a lane");
+    if (a.lane_vectors > 1) {
         k_relpos_bias<T, TT, SCORES, NT, 1, kRelposLaneVectors><<<n, kThreads, 0, st>>>(a, b0);
-    else if (a.queries == 1)
-        k_relpos_bias<T, TT, SCORES, NT, 1, 1><<<n, kThreads, 0, st>>>(a, b0);
-    else
-        k_relpos_bias<T, TT, SCORES, NT, kRelposLaneRows, 1><<<n, kThreads, 0, st>>>(a, b0);
+        return;
+    }
+    if constexpr (!NT) {
+        if (a.queries == 1) {
+            k_relpos_bias<T, TT, SCORES, NT, 1, 1><<<n, kThreads, 0, st>>>(a, b0);
+            return;
+        }
+    }
+    k_relpos_bias<T, TT, SCORES, NT, kRelposLaneRows, 1><<<n, kThreads, 0, st>>>(a, b0);
 }
 template <typename T, typename TT>
 void bias_launch(const RelposArgs& a, int64_t b0, uint32_t n, hipStream_t st)
