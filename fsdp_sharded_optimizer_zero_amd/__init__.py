@@ -761,7 +761,8 @@ class Tensors:
     """A list of tensors as tensors_sqnorm, tensors_clip and tensors_clip_norm
     take it: the struct, its plan on the GPU, and the tensors themselves, whose
     memory the plan names.  Make a new one where a tensor is replaced by another
-    (a gradient that was set to None and made anew).  One call at a time uses a
+    (a gradient that was set to None and made anew), or keep gradients where they
+    are: a list of 1500 takes 2 to 3 ms to make.  One call at a time uses a
     list (its plan holds their partial sums), and the list lives until its calls
     have ended on the GPU."""
 

@@ -280,7 +280,7 @@ struct TensorChunk {
     int64_t in_pitch, out_pitch;
     int32_t rows, cols;
     int32_t kind;           // kChunkInF32 | kChunkOutF32 | kChunkPlace
-    int32_t tensor;
+    int32_t tensor;         // whose piece it is (no kernel needs it)
 };
 static_assert(sizeof(TensorChunk) == 48, "the plan's layout");
 constexpr int32_t kChunkInF32 = 1, kChunkOutF32 = 2, kChunkPlace = 4;
@@ -347,7 +347,8 @@ constexpr int kRelposLaneRows = 4;          // of the bias a lane has, and for o
 constexpr int kRelposLaneVectors = 4;       // query vectors, from so many tiles on
 constexpr int64_t kRelposManyTiles = 8192;
 // Waves a gradient is cut into by shorter tiles, if its rows allow it: 2 for each
-// SIMD (28 x 29 x 120 x 198: 17.8 us, with 4096 waves and more 20.8, 1024 19.8).
+// SIMD (28 x 29 x 120 x 198: 17.8 us, with 4096 waves and more 20.8, 1024 19.8; the
+// bytes' floor is 5.9).
 constexpr int64_t kRelposGradTiles = 2048;
 // From so many bytes of scores on, loads bypass the caches' reuse (gradient of 1.07
 // GB: 168 us and 193, 403 MB 66 and 79; bias onto 201 MB 62 and 78, 100 MB 37 and

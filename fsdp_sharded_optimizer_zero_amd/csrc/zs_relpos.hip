@@ -426,7 +426,8 @@ __device__ __forceinline__ float from_below(float x)
 // get nothing more from this lane and pass to the lane to the right, which meets
 // them N rows later.  So each diagonal's sum leaves the wave once, at its right
 // edge or below its last row, into LDS, where it is added to its bucket.  Bound
-// by HBM: 8 x 16 x 2048 x 2048 bf16 in 165 us, 6.5 TB/s, 606 MB of them seen in
+// by HBM: 8 x 16 x 2048 x 2048 bf16 in 165 us, 6.5 TB/s (over two buffers in turn
+// 174-193), 606 MB of them seen in
 // sequences of 0 to 2048 keys 112 (with the diagonals added to LDS every N rows
 // 486 and 428; all of a bucket's diagonals by the whole wave, one bucket after the
 // other, 20 us more a call).  The two loads of kBatch rows in turn keep one under way; 8
@@ -435,7 +436,8 @@ __device__ __forceinline__ float from_below(float x)
 constexpr int kBatch = 4;
 constexpr int kFewDiagonals = 16;   // of a bucket, up to which one lane sums them
 // Of a tile of several groups, 64 at a time: 32 lanes' keys and its rows.  Joined
-// before the buckets: 28 x 29 x 120 x 64 bf16 12.0 us, buckets by group 14.5.
+// before the buckets: 28 x 29 x 120 x 64 bf16 12.0 us, buckets by group 14.5 (the
+// bytes' floor is 2).
 template <int N>
 constexpr int kGroupDiagonals = (32 * N + kRelposRows + 63) / 64;
 template <typename T, bool SCORES, bool NT>

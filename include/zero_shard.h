@@ -628,8 +628,8 @@ typedef struct zs_tensors {
 
 /* Checks a list of `count` tensors and fills *t.  No tensor's `out` may share a
  * byte with another's `in` or `out`: a tensor listed twice and clipped in place is
- * refused.  (Columns of one matrix, of one pitch, are beside one another.)  Host
- * only.
+ * refused.  (Columns of one matrix, of one pitch, are beside one another; time
+ * grows with the square of how many are listed.)  Host only.
  * Errors: ZS_ENULL (list, with count > 0; out; a tensor's `in`), ZS_EALIGN,
  * ZS_EINVAL_TENSORS, ZS_EUNSUPPORTED (count > ZS_TENSORS_MAX). */
 int zs_tensors_layout(const zs_tensor* list, int64_t count, zs_tensors* t);
